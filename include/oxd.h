@@ -78,7 +78,7 @@ typedef enum {
 #define OXD_DEVICE_BAD_PAGE 1       /* a listed page index is outside [0, num_pages) */
 #define OXD_DEVICE_PLAN_MISMATCH 2  /* device indptr/last_page_len differ from the plan's */
 #define OXD_DEVICE_WAIT_TIMEOUT 3   /* an internal pipeline wait gave up (about 1 s) */
-#define OXD_DEVICE_SHARED_PAGE 4    /* an append targeted a page whose reference count is not 1 */
+#define OXD_DEVICE_SHARED_PAGE 4    /* an append or copy targeted a page whose reference count is not 1 */
 #define OXD_DEVICE_BAD_POSITION 5   /* an append's request or position lies outside its table */
 
 typedef struct oxd_plan_s* oxd_plan; /* opaque, host-owned, immutable after planning */
@@ -138,7 +138,8 @@ typedef struct {
     int32_t max_chunks;         /* most chunks any request got */
     int32_t chunk_pages;        /* planner's chunk length in pages */
     int32_t num_slots;          /* partial-state slots in the workspace */
-    int32_t kernel_variant;     /* 0/1: CUDA-core G=1/G=2; 2,3,4: tensor-core G<=8, <=16, <=32 */
+    int32_t kernel_variant;     /* 0/1: CUDA-core G=1/G=2; 2,3,4: tensor-core G<=8, <=16, <=32;
+                                   5: tcgen05, G 17..32; 6,7,8: 4-bit cache G<=8, <=16, <=32 */
     int32_t grid_ctas;          /* persistent decode CTAs launched per run */
     int32_t ctas_per_sm;        /* resident decode CTAs per SM assumed by the planner */
     int32_t num_sms;
@@ -528,6 +529,173 @@ oxd_status oxd_prefill_plan_set_timing_events(oxd_prefill_plan plan, void* event
                                               void* event_after);
 oxd_status oxd_prefill_plan_get_info(oxd_prefill_plan plan, oxd_prefill_plan_info* info);
 oxd_status oxd_prefill_plan_destroy(oxd_prefill_plan plan);
+
+/* ------------------------------------------------------------------ 4-bit cache
+ *
+ * A paged cache held in 4 bits: the decode that reads it, the append that
+ * writes it and the copies that move its pages and convert them to and from
+ * bf16 pages. (The source pages have no counterpart; the entry points follow
+ * the bf16 ones: same block tables, plan lifecycle, checks, streams and device
+ * status.)
+ *
+ * Format OXD_FORMAT_E2M1. The 128 values of one (token, KV head) row are four
+ * groups of 32 consecutive columns. A group has one f16 scale s and 32 codes,
+ * each an e2m1 number (sign, 2-bit exponent, 1-bit mantissa: 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6 and their negatives); column d stands for s[d / 32] * e2m1(code d).
+ *   codes   [num_pages][page_size][Hkv][64] bytes (NHD) or
+ *           [num_pages][Hkv][page_size][64] bytes (HND), 16-byte aligned; byte
+ *           i of a row holds column 2i in its low and 2i + 1 in its high half
+ *   scales  [num_pages][Hkv][page_size][4] f16 in both layouts, 16-byte aligned
+ *           (a head's scales of a page are contiguous, so a head read alone
+ *           moves no other head's bytes)
+ * 72 bytes a row against 256 in bf16.
+ * Rows are held as: s = the f16 number nearest to min(amax / 6, 10912), amax
+ * the largest size of the group's 32 bf16 values; code = the e2m1 number
+ * nearest to x / s, ties to the even code (the one with mantissa bit 0), sizes
+ * above 6 taken as 6; a value that rounds to zero may get either zero; a group
+ * with s = 0 (amax up to about 1.8e-7) is all zeros. So values are held up to +-65472 (larger ones, infinities too, are
+ * held as that) and a NaN is held as some finite value.
+ */
+typedef enum {
+    OXD_FORMAT_BF16 = 0,
+    OXD_FORMAT_E2M1 = 1
+} oxd_kv_format;
+
+/* The pools of one cache (device addresses). bf16: k and v are the pools the
+ * bf16 entry points take and the scales are NULL; E2M1: k and v are codes. */
+typedef struct {
+    void* k;
+    void* v;
+    void* k_scales;
+    void* v_scales;
+} oxd_kv_pools;
+
+/*
+ * Plan one batch of decode over a 4-bit cache: as oxd_paged_decode_plan, for
+ * the same desc, tables and errors. The plan serves oxd_quant_decode_run only
+ * (oxd_paged_decode_run refuses it with OXD_ERR_PLAN_MISMATCH, and the other
+ * way round); oxd_plan_bind_workspace, _get_info, _set_timing_events and
+ * _destroy take it as any plan. A shared prefix (shared_prefix_tokens > 0) is
+ * OXD_ERR_UNSUPPORTED; tensor_path is ignored.
+ */
+oxd_status oxd_quant_decode_plan(const oxd_paged_decode_desc* desc, const int32_t* indptr_host,
+                                 const int32_t* last_page_len_host, int device,
+                                 oxd_plan* plan_out, size_t* workspace_bytes_out);
+
+/*
+ * Enqueue one decode step over a 4-bit cache: out and lse as
+ * oxd_paged_decode_run computes them for the values the cache stands for.
+ * Logits, softmax statistics and the output accumulator are F32; q enters the
+ * score product as f16 scaled by a power of two per head (exact for columns
+ * within 2^-14 of the head's largest), codes exactly and K's scales in F32; a
+ * V value (code times scale) and a softmax weight are each rounded once to
+ * f16. Arguments, errors, status codes and determinism as
+ * oxd_paged_decode_run; the four pools of `cache` are read only.
+ */
+oxd_status oxd_quant_decode_run(oxd_plan plan, const void* q, const oxd_kv_pools* cache,
+                                const int32_t* indptr, const int32_t* indices,
+                                const int32_t* last_page_len, float sm_scale, void* out,
+                                float* lse, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * Rotary embedding with several position axes, fused with the paged append.
+ * As oxd_rope_append, except that each rotary pair i < 64 turns by one of
+ * num_axes positions of its token (time, height and width of an image patch,
+ * say): the angle of pair i of token t is
+ *   rope_positions[pair_axis[i]][t] * rope_theta^(-2i/128).
+ * The cache slot still goes by positions[t], the token's place in its
+ * request. Text tokens carry the same number on every axis.
+ *
+ *   rope_positions  device int32 [num_axes][T], or NULL: positions on every axis
+ * A rope position outside [0, 2^24) counts as OXD_DEVICE_BAD_POSITION: the
+ * token's K/V rows are not written (its q_out rows are rotated at the low 24
+ * bits). Everything else as oxd_rope_append, the errors too; num_axes outside
+ * [1, 4] or a pair_axis entry not below num_axes is OXD_ERR_INVALID_ARGUMENT.
+ */
+typedef struct {
+    int32_t num_tokens;     /* T */
+    int32_t batch;
+    int32_t num_qo_heads;
+    int32_t num_kv_heads;
+    int32_t head_dim;       /* 128 */
+    int32_t page_size;      /* 8, 16, 32 or 64 */
+    int32_t layout;         /* oxd_kv_layout */
+    int32_t num_indices;    /* entries of `indices` */
+    int64_t num_pages;
+    double rope_theta;
+    int32_t num_axes;       /* 1 .. 4 */
+    int32_t reserved;       /* must be zero */
+    uint8_t pair_axis[64];  /* axis of each rotary pair */
+} oxd_axes_append_desc;
+
+oxd_status oxd_rope_axes_append(const oxd_axes_append_desc* desc, const void* q, const void* k,
+                                const void* v, const int32_t* token_request,
+                                const int32_t* positions, const int32_t* rope_positions,
+                                const int32_t* indptr, const int32_t* indices,
+                                const int32_t* page_refcount, void* q_out, void* k_pages,
+                                void* v_pages, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * The same append into a 4-bit cache: the K row bf16(RoPE(k[t])) -- here the
+ * bf16 number nearest to the rotated value, so that which code a value gets
+ * does not hang on float error -- and the V row v[t] are held in 4 bits in
+ * the token's slot of the four pools of `cache`.
+ */
+oxd_status oxd_quant_rope_append(const oxd_axes_append_desc* desc, const void* q, const void* k,
+                                 const void* v, const int32_t* token_request,
+                                 const int32_t* positions, const int32_t* rope_positions,
+                                 const int32_t* indptr, const int32_t* indices,
+                                 const int32_t* page_refcount, void* q_out,
+                                 const oxd_kv_pools* cache, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * Copy pages, K and V together: page dst_pages[i] of `dst` becomes page
+ * src_pages[i] of `src`, i < num_pairs. The pools may be one cache (a fork's
+ * private copy of a shared page, a compaction's moves) or two, in two layouts
+ * and formats: bf16 to E2M1 holds every row in 4 bits, E2M1 to bf16 writes the
+ * values the codes stand for, rounded once to bf16 (so a 4-bit request can be
+ * prefilled against), and equal formats copy bit for bit.
+ *
+ * A pair with src_pages[i] = -1 is skipped, so a captured call can be replayed
+ * on lists of any length up to num_pairs. dst pages must be distinct, and with
+ * src and dst in one cache no page may be both a source and a destination of
+ * different pairs; pages that break this end up with unspecified contents.
+ *
+ *   src, dst      pools (host struct of device addresses). If they overlap,
+ *                 they must be the same pools, in one format, layout and size
+ *   src_pages, dst_pages  device int32 [num_pairs]
+ *   dst_refcount  device int32 [dst_num_pages] or NULL: as for the append, a
+ *                 destination whose count is not 1 is not written
+ *                 (OXD_DEVICE_SHARED_PAGE); NULL: no check
+ *   workspace     device, >= 256 bytes, 256-byte aligned: the status word
+ * num_pairs = 0 is allowed. A pair with an index outside its pool copies
+ * nothing and records OXD_DEVICE_BAD_PAGE; the other pairs are copied.
+ * Host-side errors (nothing enqueued): OXD_ERR_INVALID_ARGUMENT (NULL, sizes,
+ * formats, scales of a bf16 cache not NULL), OXD_ERR_UNSUPPORTED (head_dim,
+ * page size), OXD_ERR_ALIGNMENT, OXD_ERR_ALIAS, OXD_ERR_WORKSPACE_TOO_SMALL,
+ * OXD_ERR_CUDA.
+ */
+typedef struct {
+    int32_t num_pairs;
+    int32_t num_kv_heads;
+    int32_t head_dim;       /* 128 */
+    int32_t page_size;      /* 8, 16, 32 or 64, of both caches */
+    int32_t src_format;     /* oxd_kv_format */
+    int32_t src_layout;     /* oxd_kv_layout */
+    int32_t dst_format;
+    int32_t dst_layout;
+    int64_t src_num_pages;
+    int64_t dst_num_pages;
+    int32_t reserved[2];    /* must be zero */
+} oxd_copy_pages_desc;
+
+oxd_status oxd_copy_pages(const oxd_copy_pages_desc* desc, const oxd_kv_pools* src,
+                          const oxd_kv_pools* dst, const int32_t* src_pages,
+                          const int32_t* dst_pages, const int32_t* dst_refcount,
+                          void* workspace, size_t workspace_bytes, void* stream);
 
 /* Planner decisions of a plan (host only). */
 oxd_status oxd_plan_get_info(oxd_plan plan, oxd_plan_info* info);

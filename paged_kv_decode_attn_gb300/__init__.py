@@ -11,7 +11,11 @@ The functions keep the C names:
 * :func:`oxd_paged_decode_plan` -> :class:`Plan` (owns the opaque handle)
 * :func:`oxd_paged_decode_run`, :func:`oxd_plan_bind_workspace`
 * :func:`oxd_merge_states`
-* :func:`oxd_rope_append` (fused rotary embedding + paged KV append)
+* :func:`oxd_rope_append` (fused rotary embedding + paged KV append),
+  :func:`oxd_rope_axes_append` (the same with several position axes)
+* the 4-bit cache: :func:`oxd_quant_decode_plan` -> :class:`Plan`,
+  :func:`oxd_quant_decode_run`, :func:`oxd_quant_rope_append`
+* :func:`oxd_copy_pages` (pages copied and converted between caches)
 * :func:`oxd_plan_get_info`, :func:`oxd_plan_set_timing_events`,
   :func:`oxd_plan_destroy`, :func:`oxd_read_device_status`,
   :func:`oxd_status_string`, :func:`oxd_device_status_string`, :func:`oxd_version`
@@ -43,6 +47,9 @@ __all__ = [
     "oxd_paged_prefill_plan", "oxd_paged_prefill_run", "oxd_prefill_plan_bind_workspace",
     "oxd_prefill_plan_get_info", "oxd_prefill_plan_set_timing_events",
     "oxd_prefill_plan_destroy",
+    "OXD_FORMAT_BF16", "OXD_FORMAT_E2M1", "KvPools", "AxesAppendDesc", "make_axes_append_desc",
+    "CopyPagesDesc", "make_copy_pages_desc", "oxd_quant_decode_plan", "oxd_quant_decode_run",
+    "oxd_rope_axes_append", "oxd_quant_rope_append", "oxd_copy_pages",
 ]
 
 OXD_OK = 0
@@ -58,6 +65,9 @@ OXD_ERR_NO_MEMORY = 9
 
 OXD_LAYOUT_NHD = 0
 OXD_LAYOUT_HND = 1
+
+OXD_FORMAT_BF16 = 0
+OXD_FORMAT_E2M1 = 1
 
 OXD_DEVICE_OK = 0
 OXD_DEVICE_BAD_PAGE = 1
@@ -75,6 +85,8 @@ EXPORTED_SYMBOLS = (
     "oxd_paged_prefill_plan", "oxd_paged_prefill_run", "oxd_prefill_plan_bind_workspace",
     "oxd_prefill_plan_get_info", "oxd_prefill_plan_set_timing_events",
     "oxd_prefill_plan_destroy",
+    "oxd_quant_decode_plan", "oxd_quant_decode_run", "oxd_rope_axes_append",
+    "oxd_quant_rope_append", "oxd_copy_pages",
 )
 
 
@@ -171,6 +183,78 @@ class PrefillPlanInfo(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class AxesAppendDesc(ctypes.Structure):
+    """``oxd_axes_append_desc``."""
+
+    _fields_ = [
+        ("num_tokens", ctypes.c_int32), ("batch", ctypes.c_int32),
+        ("num_qo_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("layout", ctypes.c_int32), ("num_indices", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64), ("rope_theta", ctypes.c_double),
+        ("num_axes", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("pair_axis", ctypes.c_uint8 * 64),
+    ]
+
+
+class CopyPagesDesc(ctypes.Structure):
+    """``oxd_copy_pages_desc``."""
+
+    _fields_ = [
+        ("num_pairs", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("src_format", ctypes.c_int32), ("src_layout", ctypes.c_int32),
+        ("dst_format", ctypes.c_int32), ("dst_layout", ctypes.c_int32),
+        ("src_num_pages", ctypes.c_int64), ("dst_num_pages", ctypes.c_int64),
+        ("reserved", ctypes.c_int32 * 2),
+    ]
+
+
+class KvPools:
+    """The pools of one cache (``oxd_kv_pools``): tensors or addresses. bf16 pools
+    have no scales; a 4-bit cache's ``k`` and ``v`` are its codes. The tensors are
+    kept alive; replacing one means making a new object."""
+
+    class _Struct(ctypes.Structure):
+        _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                    ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        self.tensors = (k, v, k_scales, v_scales)
+        self.struct = self._Struct(*(_addr(x) for x in self.tensors))
+
+
+def make_axes_append_desc(num_tokens, batch, num_qo_heads, num_kv_heads, page_size, layout,
+                          num_pages, num_indices, rope_theta=10000.0, sections=(64,),
+                          pair_axis=None, head_dim=128) -> AxesAppendDesc:
+    """Convenience constructor. ``sections`` gives each axis that many consecutive
+    rotary pairs (they add up to 64; ``(64,)`` is the one-axis embedding);
+    ``pair_axis`` names the axis of each of the 64 pairs instead, for interleaved
+    arrangements."""
+    if isinstance(layout, str):
+        layout = {"NHD": OXD_LAYOUT_NHD, "HND": OXD_LAYOUT_HND}[layout]
+    if pair_axis is None:
+        pair_axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    if len(pair_axis) != 64:
+        raise OxdError("make_axes_append_desc", OXD_ERR_INVALID_ARGUMENT,
+                       f"{len(pair_axis)} rotary pairs given, 64 are needed")
+    return AxesAppendDesc(num_tokens, batch, num_qo_heads, num_kv_heads, head_dim, page_size,
+                          layout, num_indices, num_pages, rope_theta, max(pair_axis) + 1, 0,
+                          (ctypes.c_uint8 * 64)(*pair_axis))
+
+
+def make_copy_pages_desc(num_pairs, num_kv_heads, page_size, src_format, src_layout,
+                         src_num_pages, dst_format, dst_layout, dst_num_pages,
+                         head_dim=128) -> CopyPagesDesc:
+    """Convenience constructor; formats may be "bf16"/"e2m1", layouts "NHD"/"HND"."""
+    formats = {"bf16": OXD_FORMAT_BF16, "e2m1": OXD_FORMAT_E2M1}
+    layouts = {"NHD": OXD_LAYOUT_NHD, "HND": OXD_LAYOUT_HND}
+    return CopyPagesDesc(num_pairs, num_kv_heads, head_dim, page_size,
+                         formats.get(src_format, src_format), layouts.get(src_layout, src_layout),
+                         formats.get(dst_format, dst_format), layouts.get(dst_layout, dst_layout),
+                         src_num_pages, dst_num_pages, (ctypes.c_int32 * 2)(0, 0))
+
+
 def make_prefill_desc(batch, num_qo_heads, num_kv_heads, page_size, layout, num_pages,
                       head_dim=128, max_splits=0, num_sms=0, wait_timeout_ns=0,
                       tile_rows=0) -> PrefillDesc:
@@ -221,6 +305,11 @@ def lib():
             L.oxd_prefill_plan_get_info.argtypes = [vp, ctypes.POINTER(PrefillPlanInfo)]
             L.oxd_prefill_plan_set_timing_events.argtypes = [vp, vp, vp]
             L.oxd_prefill_plan_destroy.argtypes = [vp]
+            L.oxd_quant_decode_plan.argtypes = L.oxd_paged_decode_plan.argtypes
+            L.oxd_quant_decode_run.argtypes = [vp] * 6 + [ctypes.c_float, vp, vp, vp, sz, vp]
+            L.oxd_rope_axes_append.argtypes = [ctypes.POINTER(AxesAppendDesc)] + [vp] * 13 + [sz, vp]
+            L.oxd_quant_rope_append.argtypes = [ctypes.POINTER(AxesAppendDesc)] + [vp] * 12 + [sz, vp]
+            L.oxd_copy_pages.argtypes = [ctypes.POINTER(CopyPagesDesc)] + [vp] * 6 + [sz, vp]
             L.oxd_read_device_status.argtypes = [vp, vp, ctypes.POINTER(i32)]
             L.oxd_read_static_workspace_status.argtypes = [vp, ctypes.POINTER(i32)]
             for f in ("oxd_paged_decode_plan", "oxd_paged_decode_run",
@@ -230,7 +319,9 @@ def lib():
                       "oxd_read_device_status", "oxd_plan_bind_workspace", "oxd_rope_append",
                       "oxd_paged_prefill_plan", "oxd_paged_prefill_run",
                       "oxd_prefill_plan_bind_workspace", "oxd_prefill_plan_get_info",
-                      "oxd_prefill_plan_set_timing_events", "oxd_prefill_plan_destroy"):
+                      "oxd_prefill_plan_set_timing_events", "oxd_prefill_plan_destroy",
+                      "oxd_quant_decode_plan", "oxd_quant_decode_run", "oxd_rope_axes_append",
+                      "oxd_quant_rope_append", "oxd_copy_pages"):
                 getattr(L, f).restype = ctypes.c_int
             L.oxd_status_string.argtypes = [ctypes.c_int]
             L.oxd_status_string.restype = ctypes.c_char_p
@@ -330,19 +421,28 @@ def _handle(plan):
     return plan.handle if isinstance(plan, (Plan, PrefillPlan)) else plan
 
 
-def oxd_paged_decode_plan(desc: Desc, indptr_host, last_page_len_host, device: int = 0) -> Plan:
-    """Plan a decode batch from host block tables; returns a :class:`Plan`."""
+def _plan_decode(name, desc: Desc, indptr_host, last_page_len_host, device) -> Plan:
     indptr = np.ascontiguousarray(np.asarray(indptr_host), dtype=np.int32)
     last = np.ascontiguousarray(np.asarray(last_page_len_host), dtype=np.int32)
     if indptr.shape != (desc.batch + 1,) or last.shape != (desc.batch,):
-        raise OxdError("oxd_paged_decode_plan", OXD_ERR_INVALID_ARGUMENT,
+        raise OxdError(name, OXD_ERR_INVALID_ARGUMENT,
                        "indptr must be [batch+1] and last_page_len [batch]")
     h = ctypes.c_void_p()
     ws = ctypes.c_size_t()
-    st = lib().oxd_paged_decode_plan(ctypes.byref(desc), indptr.ctypes.data, last.ctypes.data,
-                                     int(device), ctypes.byref(h), ctypes.byref(ws))
-    _check("oxd_paged_decode_plan", st)
+    st = getattr(lib(), name)(ctypes.byref(desc), indptr.ctypes.data, last.ctypes.data,
+                              int(device), ctypes.byref(h), ctypes.byref(ws))
+    _check(name, st)
     return Plan(h.value, ws.value, desc)
+
+
+def oxd_paged_decode_plan(desc: Desc, indptr_host, last_page_len_host, device: int = 0) -> Plan:
+    """Plan a decode batch from host block tables; returns a :class:`Plan`."""
+    return _plan_decode("oxd_paged_decode_plan", desc, indptr_host, last_page_len_host, device)
+
+
+def oxd_quant_decode_plan(desc: Desc, indptr_host, last_page_len_host, device: int = 0) -> Plan:
+    """Plan a decode batch over a 4-bit cache (for :func:`oxd_quant_decode_run`)."""
+    return _plan_decode("oxd_quant_decode_plan", desc, indptr_host, last_page_len_host, device)
 
 
 def oxd_paged_decode_run(plan, q, k_pages, v_pages, indptr, indices, last_page_len, sm_scale,
@@ -544,3 +644,58 @@ def oxd_prefill_plan_destroy(plan) -> None:
         plan.destroy()
     else:
         _check("oxd_prefill_plan_destroy", lib().oxd_prefill_plan_destroy(plan))
+
+
+# ------------------------------------------------------------------ 4-bit cache, axes, page copies
+
+def oxd_quant_decode_run(plan, q, cache: KvPools, indptr, indices, last_page_len, sm_scale, out,
+                         lse, workspace, workspace_bytes=None, stream=None) -> None:
+    """Enqueue one decode step over a 4-bit cache (see ``oxd_quant_decode_run`` in
+    include/oxd.h)."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    st = lib().oxd_quant_decode_run(
+        _handle(plan), _addr(q), ctypes.byref(cache.struct), _addr(indptr), _addr(indices),
+        _addr(last_page_len), float(sm_scale), _addr(out), _addr(lse), _addr(workspace),
+        int(workspace_bytes), _stream(stream, q))
+    _check("oxd_quant_decode_run", st)
+
+
+def oxd_rope_axes_append(desc: AxesAppendDesc, q, k, v, token_request, positions, rope_positions,
+                         indptr, indices, page_refcount, q_out, k_pages, v_pages, workspace,
+                         workspace_bytes=None, stream=None) -> None:
+    """Enqueue a rotary embedding with position axes + paged KV append (see
+    ``oxd_rope_axes_append`` in include/oxd.h)."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    st = lib().oxd_rope_axes_append(
+        ctypes.byref(desc), _addr(q), _addr(k), _addr(v), _addr(token_request), _addr(positions),
+        _addr(rope_positions), _addr(indptr), _addr(indices), _addr(page_refcount), _addr(q_out),
+        _addr(k_pages), _addr(v_pages), _addr(workspace), int(workspace_bytes), _stream(stream, q))
+    _check("oxd_rope_axes_append", st)
+
+
+def oxd_quant_rope_append(desc: AxesAppendDesc, q, k, v, token_request, positions, rope_positions,
+                          indptr, indices, page_refcount, q_out, cache: KvPools, workspace,
+                          workspace_bytes=None, stream=None) -> None:
+    """Enqueue a rotary embedding + append into a 4-bit cache (see
+    ``oxd_quant_rope_append`` in include/oxd.h)."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    st = lib().oxd_quant_rope_append(
+        ctypes.byref(desc), _addr(q), _addr(k), _addr(v), _addr(token_request), _addr(positions),
+        _addr(rope_positions), _addr(indptr), _addr(indices), _addr(page_refcount), _addr(q_out),
+        ctypes.byref(cache.struct), _addr(workspace), int(workspace_bytes), _stream(stream, q))
+    _check("oxd_quant_rope_append", st)
+
+
+def oxd_copy_pages(desc: CopyPagesDesc, src: KvPools, dst: KvPools, src_pages, dst_pages,
+                   dst_refcount, workspace, workspace_bytes=None, stream=None) -> None:
+    """Enqueue page copies between caches (see ``oxd_copy_pages`` in include/oxd.h)."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    st = lib().oxd_copy_pages(
+        ctypes.byref(desc), ctypes.byref(src.struct), ctypes.byref(dst.struct), _addr(src_pages),
+        _addr(dst_pages), _addr(dst_refcount), _addr(workspace), int(workspace_bytes),
+        _stream(stream, workspace))
+    _check("oxd_copy_pages", st)

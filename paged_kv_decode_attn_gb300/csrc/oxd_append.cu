@@ -29,8 +29,6 @@ namespace {
 constexpr int kAppendWarps = 8;
 constexpr int kKvRows = 8;  // K/V rows (KV heads of one token) per KV warp
 constexpr int kQRows = 8;   // query rows (heads of one token) per query warp
-constexpr int kDeviceSharedPage = 4;
-constexpr int kDeviceBadPosition = 5;
 
 // cos and sin of the angles of this lane's two pairs (2l, 2l + 1) at `pos`.
 __device__ __forceinline__ void rope_angles(int pos, const float* turns_hi, const float* turns_lo,

@@ -1141,6 +1141,9 @@ VariantShape variant_shape(int variant) {
         case kVariantMma8: return shape_of<CfgMma8>();
         case kVariantMma16: return shape_of<CfgMma16>();
         case kVariantWide: return wide_shape();
+        case kVariantQuant8:
+        case kVariantQuant16:
+        case kVariantQuant32: return quant_shape(variant);
         default: return shape_of<CfgMma16>();  // kVariantMma32: two 16-row CTAs per piece
     }
 }
@@ -1152,6 +1155,9 @@ cudaError_t variant_occupancy(int variant, int* n) {
         case kVariantMma8: return occupancy_of<CfgMma8>(n);
         case kVariantMma16: return occupancy_of<CfgMma16>(n);
         case kVariantWide: return wide_occupancy(n);
+        case kVariantQuant8:
+        case kVariantQuant16:
+        case kVariantQuant32: return quant_occupancy(variant, n);
         default: return occupancy_of<CfgMma16>(n);
     }
 }

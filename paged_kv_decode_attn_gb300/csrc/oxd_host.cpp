@@ -34,6 +34,7 @@ using namespace oxd;
 struct oxd_plan_s {
     oxd_paged_decode_desc desc;
     int device;  // -1 for a host-only plan (desc.num_sms given)
+    bool quant;  // for a 4-bit cache (oxd_quant_decode_run), else for bf16 pools
     int group;
     int variant;
     int n_items;
@@ -113,7 +114,8 @@ bool plan_alive(oxd_plan p) {
     return g_plans.count(p) != 0;
 }
 
-int choose_variant(int G, int tensor_path) {
+int choose_variant(int G, int tensor_path, bool quant) {
+    if (quant) return G <= 8 ? kVariantQuant8 : G <= 16 ? kVariantQuant16 : kVariantQuant32;
     if (G == 1) return kVariantFmaG1;
     if (G == 2) return kVariantFmaG2;
     if (G <= 8) return kVariantMma8;
@@ -150,6 +152,27 @@ EncodeTiledFn get_encoder() {
 
 bool encode_pool(CUtensorMap* map, const void* pool, const oxd_paged_decode_desc& d) {
     return encode_kv_pool(map, pool, d.layout, d.page_size, d.num_kv_heads, d.num_pages);
+}
+
+// 4-D map over a pool of 4-bit codes: (byte, A, B, page) with (A, B) = (head,
+// token) for NHD and (token, head) for HND; a box is the 64 code bytes of up to
+// 32 tokens of one page and head, stored with the 64-byte swizzle.
+bool encode_code_pool(CUtensorMap* map, const void* pool, const oxd_paged_decode_desc& d) {
+    EncodeTiledFn enc = get_encoder();
+    if (enc == nullptr) return false;
+    const cuuint64_t ps = static_cast<cuuint64_t>(d.page_size);
+    const cuuint64_t H = static_cast<cuuint64_t>(d.num_kv_heads);
+    const cuuint32_t rows = static_cast<cuuint32_t>(std::min(d.page_size, kQuantChunk));
+    const bool nhd = d.layout == OXD_LAYOUT_NHD;
+    const cuuint64_t dims[4] = {kCodeBytes, nhd ? H : ps, nhd ? ps : H,
+                                static_cast<cuuint64_t>(d.num_pages)};
+    const cuuint64_t strides[3] = {kCodeBytes, (nhd ? H : ps) * kCodeBytes, ps * H * kCodeBytes};
+    const cuuint32_t box[4] = {kCodeBytes, nhd ? 1u : rows, nhd ? rows : 1u, 1u};
+    const cuuint32_t elem[4] = {1, 1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pool), dims, strides,
+                     box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
 }
 
 // 2-D map over q as [B*Hq rows][128] for the tcgen05 variant: a box is 32
@@ -293,9 +316,15 @@ const char* oxd_device_status_string(int32_t code) {
     return "unknown device status";
 }
 
-oxd_status oxd_paged_decode_plan(const oxd_paged_decode_desc* desc, const int32_t* indptr,
-                                 const int32_t* last, int device, oxd_plan* plan_out,
-                                 size_t* ws_out) {
+}  // extern "C"
+
+namespace {
+
+// The planner of oxd_paged_decode_plan and, for a 4-bit cache (`quant`), of
+// oxd_quant_decode_plan.
+oxd_status plan_decode(const oxd_paged_decode_desc* desc, const int32_t* indptr,
+                       const int32_t* last, int device, bool quant, oxd_plan* plan_out,
+                       size_t* ws_out) {
     if (desc == nullptr || indptr == nullptr || last == nullptr || plan_out == nullptr ||
         ws_out == nullptr)
         return OXD_ERR_INVALID_ARGUMENT;
@@ -303,6 +332,7 @@ oxd_status oxd_paged_decode_plan(const oxd_paged_decode_desc* desc, const int32_
     if (st != OXD_OK) return st;
     const oxd_paged_decode_desc& d = *desc;
     const int B = d.batch, ps = d.page_size;
+    if (quant && d.shared_prefix_tokens > 0) return OXD_ERR_UNSUPPORTED;
     if (indptr[0] < 0) return OXD_ERR_INVALID_ARGUMENT;
     int64_t total_pages = 0, total_tokens = 0;
     for (int b = 0; b < B; ++b) {
@@ -314,7 +344,7 @@ oxd_status oxd_paged_decode_plan(const oxd_paged_decode_desc* desc, const int32_
     }
 
     const int G = d.num_qo_heads / d.num_kv_heads;
-    const int variant = choose_variant(G, d.tensor_path);
+    const int variant = choose_variant(G, d.tensor_path, quant);
     const VariantShape vs = variant_shape(variant);
     int num_sms = d.num_sms, ctas_per_sm = 0, plan_device = -1;
     if (num_sms == 0) {
@@ -379,7 +409,7 @@ oxd_status oxd_paged_decode_plan(const oxd_paged_decode_desc* desc, const int32_
     // Groups of more than 16 query heads run every piece on a pair of CTAs,
     // one per 16-row half, side by side (the second read of each page is
     // then served by L2); the partition below is over CTA pairs.
-    const int copies = variant == kVariantMma32 ? 2 : 1;
+    const int copies = variant == kVariantMma32 || variant == kVariantQuant32 ? 2 : 1;
     const int64_t resident = static_cast<int64_t>(num_sms) * ctas_per_sm / copies;
     auto tokens_to = [&](int b, int k) {  // tokens in pages [0, k) of request b
         const int P = indptr[b + 1] - indptr[b];
@@ -674,6 +704,7 @@ oxd_status oxd_paged_decode_plan(const oxd_paged_decode_desc* desc, const int32_
     if (P == nullptr) return OXD_ERR_NO_MEMORY;
     P->desc = d;
     P->device = plan_device;
+    P->quant = quant;
     P->group = G;
     P->variant = variant;
     P->n_items = n_units;
@@ -764,6 +795,157 @@ oxd_status oxd_paged_decode_plan(const oxd_paged_decode_desc* desc, const int32_
     return OXD_OK;
 }
 
+// The operand checks of a decode run (bf16 or 4-bit) but for the pools' own
+// NULL checks. pools: the cache's arrays, each with its bytes and alignment.
+struct PoolArg {
+    const void* p;
+    size_t bytes;
+};
+
+oxd_status check_run(oxd_plan plan, const void* q, const PoolArg* pools, int n_pools,
+                     const int32_t* indptr, const int32_t* indices, const int32_t* last_page_len,
+                     float sm_scale, const void* out, const float* lse, const void* workspace,
+                     size_t workspace_bytes) {
+    if (!std::isfinite(sm_scale)) return OXD_ERR_INVALID_ARGUMENT;
+    const oxd_paged_decode_desc& d = plan->desc;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(indptr, 4) || !aligned(indices, 4) ||
+        !aligned(last_page_len, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
+        return OXD_ERR_ALIGNMENT;
+    for (int i = 0; i < n_pools; ++i)
+        if (!aligned(pools[i].p, 16)) return OXD_ERR_ALIGNMENT;
+    if (workspace_bytes < plan->ws_bytes) return OXD_ERR_WORKSPACE_TOO_SMALL;
+
+    const size_t rows = static_cast<size_t>(d.batch) * d.num_qo_heads;
+    const Span in[] = {span(q, rows * kHeadDim * 2),
+                       span(indptr, (static_cast<size_t>(d.batch) + 1) * 4),
+                       span(indices, static_cast<size_t>(plan->nnz) * 4),
+                       span(last_page_len, static_cast<size_t>(d.batch) * 4)};
+    const Span outs[] = {span(out, rows * kHeadDim * 2),
+                         lse ? span(lse, rows * 4) : Span{0, 0},
+                         span(workspace, plan->ws_bytes)};
+    for (const Span& o : outs) {
+        for (const Span& i : in)
+            if (overlap(o, i)) return OXD_ERR_ALIAS;
+        for (int i = 0; i < n_pools; ++i)
+            if (overlap(o, span(pools[i].p, pools[i].bytes))) return OXD_ERR_ALIAS;
+    }
+    if (overlap(outs[0], outs[1]) || overlap(outs[0], outs[2]) || overlap(outs[1], outs[2]))
+        return OXD_ERR_ALIAS;
+    if (plan->device >= 0) {
+        int cur = -1;
+        if (cudaGetDevice(&cur) != cudaSuccess) return OXD_ERR_CUDA;
+        if (cur != plan->device) return OXD_ERR_PLAN_MISMATCH;
+    }
+    return OXD_OK;
+}
+
+constexpr size_t kStampOff = offsetof(WsHeader, stamp);
+
+// Work list of a run: read from the workspace when the plan is bound to it or
+// the list was too long for the parameter buffers. An unbound run with a long
+// list uploads it together with a zero stamp, which also ends any binding of
+// another plan to this workspace.
+oxd_status upload_list(oxd_plan plan, uint8_t* ws, bool bound, cudaStream_t s) {
+    if (!bound && plan->upload &&
+        cudaMemcpyAsync(ws + kStampOff, static_cast<uint8_t*>(plan->meta) + kStampOff,
+                        plan->meta_bytes - kStampOff, cudaMemcpyHostToDevice,
+                        s) != cudaSuccess)
+        return OXD_ERR_CUDA;
+    return OXD_OK;
+}
+
+DecodeParams decode_params(oxd_plan plan, uint8_t* ws, bool bound, const void* q,
+                           const int32_t* indptr, const int32_t* indices,
+                           const int32_t* last_page_len, float sm_scale, void* out, float* lse) {
+    const oxd_paged_decode_desc& d = plan->desc;
+    const bool in_ws = bound || plan->upload;
+    DecodeParams p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.out = static_cast<uint16_t*>(out);
+    p.lse = lse;
+    p.indptr = indptr;
+    p.indices = indices;
+    p.last_page_len = last_page_len;
+    p.units = in_ws ? reinterpret_cast<const int4*>(ws + plan->off_units) : nullptr;
+    p.cta_rec = in_ws ? reinterpret_cast<const int4*>(ws + plan->off_cta) : nullptr;
+    p.ws_stamp = bound ? reinterpret_cast<const unsigned long long*>(ws + kStampOff) : nullptr;
+    p.stamp = plan->stamp;
+    p.clear_stamp = bound ? nullptr : reinterpret_cast<unsigned long long*>(ws + kStampOff);
+    p.n_units = plan->n_items;
+    p.n_slots = plan->n_slots;
+    p.batch = d.batch;
+    p.nnz = plan->nnz;
+    p.part_o = reinterpret_cast<float*>(ws + plan->off_part_o);
+    p.part_lse = reinterpret_cast<float*>(ws + plan->off_part_lse);
+    p.status = reinterpret_cast<unsigned long long*>(ws + offsetof(WsHeader, status));
+    p.last_epoch = reinterpret_cast<uint32_t*>(ws + offsetof(WsHeader, last_epoch));
+    p.epoch = next_epoch();
+    p.num_qo_heads = d.num_qo_heads;
+    p.num_kv_heads = d.num_kv_heads;
+    p.group = plan->group;
+    p.page_size = d.page_size;
+    p.layout = d.layout;
+    p.num_pages = d.num_pages;
+    p.scale_log2 = sm_scale * 1.4426950408889634f;  // log2(e)
+    p.cluster_c = plan->cluster_c;
+    p.wait_ns = d.wait_timeout_ns > 0 ? d.wait_timeout_ns : kWaitTimeoutNs;
+    return p;
+}
+
+// The merge of a run's split streams, behind its decode kernel.
+oxd_status merge_run(oxd_plan plan, const DecodeParams& p, uint8_t* ws, bool in_ws,
+                     cudaStream_t s) {
+    if (plan->n_split == 0) return OXD_OK;
+    const oxd_paged_decode_desc& d = plan->desc;
+    MergeParams mp{};
+    mp.v = p.part_o;
+    mp.s = p.part_lse;
+    mp.out = p.out;
+    mp.lse = p.lse;
+    mp.entries = in_ws ? reinterpret_cast<const int4*>(ws + plan->off_split) : nullptr;
+    mp.ws_stamp = p.ws_stamp;
+    mp.stamp = p.stamp;
+    mp.n_rows = static_cast<int64_t>(d.batch) * d.num_qo_heads;
+    mp.n_states = static_cast<int64_t>(plan->n_slots) * plan->group;
+    mp.uniform = 0;
+    mp.n = plan->n_split;
+    mp.S = 0;
+    mp.R = plan->group;
+    mp.D = kHeadDim;
+    mp.s_to_ln = 0.693147180559945309f;  // partial LSEs are log2
+    mp.max_count = plan->max_chunks + (plan->casc_units > 0 ? 1 : 0);
+    // With timing events the decode kernel must end before ev_after, so
+    // the merge is then launched without the early-start attribute.
+    if (launch_split_merge(mp, in_ws ? nullptr : plan->splits, s, plan->ev_after == nullptr) !=
+        cudaSuccess)
+        return OXD_ERR_CUDA;
+    return OXD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+oxd_status oxd_paged_decode_plan(const oxd_paged_decode_desc* desc, const int32_t* indptr,
+                                 const int32_t* last, int device, oxd_plan* plan_out,
+                                 size_t* ws_out) {
+    try {
+        return plan_decode(desc, indptr, last, device, false, plan_out, ws_out);
+    } catch (const std::bad_alloc&) {
+        return OXD_ERR_NO_MEMORY;
+    }
+}
+
+oxd_status oxd_quant_decode_plan(const oxd_paged_decode_desc* desc, const int32_t* indptr,
+                                 const int32_t* last, int device, oxd_plan* plan_out,
+                                 size_t* ws_out) {
+    try {
+        return plan_decode(desc, indptr, last, device, true, plan_out, ws_out);
+    } catch (const std::bad_alloc&) {
+        return OXD_ERR_NO_MEMORY;
+    }
+}
+
 oxd_status oxd_plan_get_info(oxd_plan plan, oxd_plan_info* info) {
     if (info == nullptr) return OXD_ERR_INVALID_ARGUMENT;
     if (plan == nullptr || !plan_alive(plan)) return OXD_ERR_PLAN_MISMATCH;
@@ -845,42 +1027,17 @@ oxd_status oxd_paged_decode_run(oxd_plan plan, const void* q, const void* k_page
                                 const int32_t* indices, const int32_t* last_page_len,
                                 float sm_scale, void* out, float* lse, void* workspace,
                                 size_t workspace_bytes, void* stream) {
-    if (plan == nullptr || !plan_alive(plan)) return OXD_ERR_PLAN_MISMATCH;
+    if (plan == nullptr || !plan_alive(plan) || plan->quant) return OXD_ERR_PLAN_MISMATCH;
     if (q == nullptr || k_pages == nullptr || v_pages == nullptr || indptr == nullptr ||
         indices == nullptr || last_page_len == nullptr || out == nullptr || workspace == nullptr)
         return OXD_ERR_INVALID_ARGUMENT;
-    if (!std::isfinite(sm_scale)) return OXD_ERR_INVALID_ARGUMENT;
     const oxd_paged_decode_desc& d = plan->desc;
-    if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||
-        !aligned(indptr, 4) || !aligned(indices, 4) || !aligned(last_page_len, 4) ||
-        !aligned(lse, 4) || !aligned(workspace, 256))
-        return OXD_ERR_ALIGNMENT;
-    if (workspace_bytes < plan->ws_bytes) return OXD_ERR_WORKSPACE_TOO_SMALL;
-
-    const size_t rows = static_cast<size_t>(d.batch) * d.num_qo_heads;
     const size_t pool = static_cast<size_t>(d.num_pages) * d.page_size * d.num_kv_heads *
                         d.head_dim * 2;
-    const Span in[] = {span(q, rows * kHeadDim * 2),
-                       span(k_pages, pool),
-                       span(v_pages, pool),
-                       span(indptr, (static_cast<size_t>(d.batch) + 1) * 4),
-                       span(indices, static_cast<size_t>(plan->nnz) * 4),
-                       span(last_page_len, static_cast<size_t>(d.batch) * 4)};
-    const Span outs[] = {span(out, rows * kHeadDim * 2),
-                         lse ? span(lse, rows * 4) : Span{0, 0},
-                         span(workspace, plan->ws_bytes)};
-    for (const Span& o : outs) {
-        for (const Span& i : in)
-            if (overlap(o, i)) return OXD_ERR_ALIAS;
-    }
-    if (overlap(outs[0], outs[1]) || overlap(outs[0], outs[2]) || overlap(outs[1], outs[2]))
-        return OXD_ERR_ALIAS;
-
-    if (plan->device >= 0) {
-        int cur = -1;
-        if (cudaGetDevice(&cur) != cudaSuccess) return OXD_ERR_CUDA;
-        if (cur != plan->device) return OXD_ERR_PLAN_MISMATCH;
-    }
+    const PoolArg pools[] = {{k_pages, pool}, {v_pages, pool}};
+    const oxd_status chk = check_run(plan, q, pools, 2, indptr, indices, last_page_len, sm_scale,
+                                     out, lse, workspace, workspace_bytes);
+    if (chk != OXD_OK) return chk;
     CUtensorMap tk, tv, tq, tq3;
     if (!encode_pool(&tk, k_pages, d) || !encode_pool(&tv, v_pages, d)) return OXD_ERR_CUDA;
     if (plan->variant == kVariantWide && !encode_q(&tq, q, d)) return OXD_ERR_CUDA;
@@ -900,46 +1057,11 @@ oxd_status oxd_paged_decode_run(oxd_plan plan, const void* q, const void* k_page
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const bool bound = plan->bound_ws.load() == workspace;
-    // An unbound run with a long list uploads it together with a zero stamp,
-    // which also ends any binding of another plan to this workspace.
     const bool in_ws = bound || plan->upload;
-    constexpr size_t kStampOff = offsetof(WsHeader, stamp);
-    if (!bound && plan->upload &&
-        cudaMemcpyAsync(ws + kStampOff, static_cast<uint8_t*>(plan->meta) + kStampOff,
-                        plan->meta_bytes - kStampOff, cudaMemcpyHostToDevice,
-                        s) != cudaSuccess)
-        return OXD_ERR_CUDA;
-
-    DecodeParams p{};
-    p.q = static_cast<const uint16_t*>(q);
-    p.out = static_cast<uint16_t*>(out);
-    p.lse = lse;
-    p.indptr = indptr;
-    p.indices = indices;
-    p.last_page_len = last_page_len;
-    p.units = in_ws ? reinterpret_cast<const int4*>(ws + plan->off_units) : nullptr;
-    p.cta_rec = in_ws ? reinterpret_cast<const int4*>(ws + plan->off_cta) : nullptr;
-    p.ws_stamp = bound ? reinterpret_cast<const unsigned long long*>(ws + kStampOff) : nullptr;
-    p.stamp = plan->stamp;
-    p.clear_stamp = bound ? nullptr : reinterpret_cast<unsigned long long*>(ws + kStampOff);
-    p.n_units = plan->n_items;
-    p.n_slots = plan->n_slots;
-    p.batch = d.batch;
-    p.nnz = plan->nnz;
-    p.part_o = reinterpret_cast<float*>(ws + plan->off_part_o);
-    p.part_lse = reinterpret_cast<float*>(ws + plan->off_part_lse);
-    p.status = reinterpret_cast<unsigned long long*>(ws + offsetof(WsHeader, status));
-    p.last_epoch = reinterpret_cast<uint32_t*>(ws + offsetof(WsHeader, last_epoch));
-    p.epoch = next_epoch();
-    p.num_qo_heads = d.num_qo_heads;
-    p.num_kv_heads = d.num_kv_heads;
-    p.group = plan->group;
-    p.page_size = d.page_size;
-    p.layout = d.layout;
-    p.num_pages = d.num_pages;
-    p.scale_log2 = sm_scale * 1.4426950408889634f;  // log2(e)
-    p.cluster_c = plan->cluster_c;
-    p.wait_ns = d.wait_timeout_ns > 0 ? d.wait_timeout_ns : kWaitTimeoutNs;
+    const oxd_status up = upload_list(plan, ws, bound, s);
+    if (up != OXD_OK) return up;
+    const DecodeParams p = decode_params(plan, ws, bound, q, indptr, indices, last_page_len,
+                                         sm_scale, out, lse);
 
     if (plan->ev_before != nullptr && cudaEventRecord(plan->ev_before, s) != cudaSuccess)
         return OXD_ERR_CUDA;
@@ -995,31 +1117,53 @@ oxd_status oxd_paged_decode_run(oxd_plan plan, const void* q, const void* k_page
                                   plan->ev_after == nullptr) != cudaSuccess)
             return OXD_ERR_CUDA;
     }
-    if (plan->n_split > 0) {
-        MergeParams mp{};
-        mp.v = p.part_o;
-        mp.s = p.part_lse;
-        mp.out = p.out;
-        mp.lse = lse;
-        mp.entries = in_ws ? reinterpret_cast<const int4*>(ws + plan->off_split) : nullptr;
-        mp.ws_stamp = p.ws_stamp;
-        mp.stamp = p.stamp;
-        mp.n_rows = static_cast<int64_t>(d.batch) * d.num_qo_heads;
-        mp.n_states = static_cast<int64_t>(plan->n_slots) * plan->group;
-        mp.uniform = 0;
-        mp.n = plan->n_split;
-        mp.S = 0;
-        mp.R = plan->group;
-        mp.D = kHeadDim;
-        mp.s_to_ln = 0.693147180559945309f;  // partial LSEs are log2
-        mp.max_count = plan->max_chunks + (plan->casc_units > 0 ? 1 : 0);
-        // With timing events the decode kernel must end before ev_after, so
-        // the merge is then launched without the early-start attribute.
-        if (launch_split_merge(mp, in_ws ? nullptr : plan->splits, s,
-                               plan->ev_after == nullptr) != cudaSuccess)
-            return OXD_ERR_CUDA;
-    }
-    return OXD_OK;
+    return merge_run(plan, p, ws, in_ws, s);
+}
+
+oxd_status oxd_quant_decode_run(oxd_plan plan, const void* q, const oxd_kv_pools* cache,
+                                const int32_t* indptr, const int32_t* indices,
+                                const int32_t* last_page_len, float sm_scale, void* out,
+                                float* lse, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+    if (plan == nullptr || !plan_alive(plan) || !plan->quant) return OXD_ERR_PLAN_MISMATCH;
+    if (q == nullptr || cache == nullptr || cache->k == nullptr || cache->v == nullptr ||
+        cache->k_scales == nullptr || cache->v_scales == nullptr || indptr == nullptr ||
+        indices == nullptr || last_page_len == nullptr || out == nullptr || workspace == nullptr)
+        return OXD_ERR_INVALID_ARGUMENT;
+    const oxd_paged_decode_desc& d = plan->desc;
+    const size_t rows = static_cast<size_t>(d.num_pages) * d.page_size * d.num_kv_heads;
+    const PoolArg pools[] = {{cache->k, rows * kCodeBytes},
+                             {cache->v, rows * kCodeBytes},
+                             {cache->k_scales, rows * kScaleBytes},
+                             {cache->v_scales, rows * kScaleBytes}};
+    const oxd_status chk = check_run(plan, q, pools, 4, indptr, indices, last_page_len, sm_scale,
+                                     out, lse, workspace, workspace_bytes);
+    if (chk != OXD_OK) return chk;
+    CUtensorMap tk, tv;
+    if (!encode_code_pool(&tk, cache->k, d) || !encode_code_pool(&tv, cache->v, d))
+        return OXD_ERR_CUDA;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const bool bound = plan->bound_ws.load() == workspace;
+    const bool in_ws = bound || plan->upload;
+    const oxd_status up = upload_list(plan, ws, bound, s);
+    if (up != OXD_OK) return up;
+    QuantDecodeParams p{};
+    p.d = decode_params(plan, ws, bound, q, indptr, indices, last_page_len, sm_scale, out, lse);
+    p.k_codes = static_cast<const uint8_t*>(cache->k);
+    p.v_codes = static_cast<const uint8_t*>(cache->v);
+    p.k_scales = static_cast<const uint16_t*>(cache->k_scales);
+    p.v_scales = static_cast<const uint16_t*>(cache->v_scales);
+    if (plan->ev_before != nullptr && cudaEventRecord(plan->ev_before, s) != cudaSuccess)
+        return OXD_ERR_CUDA;
+    const bool pdl = d.pdl != 0 && plan->ev_before == nullptr && !(!bound && plan->upload);
+    if (launch_decode_quant(plan->variant, tk, tv, p, in_ws ? nullptr : plan->work, plan->grid, s,
+                            pdl) != cudaSuccess)
+        return OXD_ERR_CUDA;
+    if (plan->ev_after != nullptr && cudaEventRecord(plan->ev_after, s) != cudaSuccess)
+        return OXD_ERR_CUDA;
+    return merge_run(plan, p.d, ws, in_ws, s);
 }
 
 oxd_status oxd_merge_states(const float* v, const float* s, int32_t N, int32_t S, int32_t H,

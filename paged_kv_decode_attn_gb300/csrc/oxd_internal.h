@@ -22,7 +22,10 @@ enum Variant : int {
     kVariantMma16 = 3,   // mma.sync, 9 <= G <= 16
     kVariantMma32 = 4,   // 17 <= G <= 32: each piece runs on a pair of 16-row CTAs
     kVariantWide = 5,    // 17 <= G <= 32: tcgen05 (TMEM accumulators), one CTA per piece
-    kNumVariants = 6
+    kVariantQuant8 = 6,  // 4-bit cache (oxd_decode_quant.cu), G <= 8
+    kVariantQuant16 = 7, // 9 <= G <= 16
+    kVariantQuant32 = 8, // 17 <= G <= 32: each piece runs on a pair of 16-row CTAs
+    kNumVariants = 9
 };
 
 struct VariantShape {
@@ -184,6 +187,70 @@ cudaError_t wide_occupancy(int* ctas_per_sm);
 cudaError_t launch_decode_wide(const CUtensorMap& tk, const CUtensorMap& tv,
                                const CUtensorMap& tq, const DecodeParams& p, const WorkList* w,
                                int grid, cudaStream_t stream, bool pdl);
+// Decode over a 4-bit cache (oxd_decode_quant.cu). tk, tv: maps over the code
+// pools (64-byte swizzle, boxes of up to kQuantChunk tokens).
+constexpr int kCodeBytes = 64;   // 4-bit codes of one (token, head) row
+constexpr int kScaleBytes = 8;   // its four f16 scales
+constexpr int kQuantChunk = 32;  // tokens a consumer warp takes at a time
+struct QuantDecodeParams {
+    DecodeParams d;
+    const uint8_t* k_codes;
+    const uint8_t* v_codes;
+    const uint16_t* k_scales;    // f16 [num_pages][Hkv][page_size][4]
+    const uint16_t* v_scales;
+};
+VariantShape quant_shape(int variant);
+cudaError_t quant_occupancy(int variant, int* ctas_per_sm);
+cudaError_t launch_decode_quant(int variant, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const QuantDecodeParams& p, const WorkList* w, int grid,
+                                cudaStream_t stream, bool pdl);
+
+// RoPE with position axes + paged append, into bf16 or 4-bit pages
+// (oxd_append_axes.cu).
+struct AxesAppendParams {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    const int32_t* token_request;
+    const int32_t* positions;
+    const int32_t* rope_positions;  // [num_axes][T]
+    const int32_t* indptr;
+    const int32_t* indices;
+    const int32_t* refcount;
+    uint16_t* q_out;
+    void* k_pages;                  // bf16 rows, or codes when k_scales is set
+    void* v_pages;
+    uint16_t* k_scales;             // nullptr: bf16 pages
+    uint16_t* v_scales;
+    unsigned long long* status;
+    uint32_t* last_epoch;
+    uint32_t epoch;
+    int32_t T, B, Hq, Hkv, page_size, layout, num_indices, num_axes;
+    int64_t num_pages;
+    double turns[kHeadDim / 2];     // theta^(-2i/128) / (2 pi)
+    uint8_t pair_axis[kHeadDim / 2];
+};
+cudaError_t launch_axes_append(const AxesAppendParams& p, cudaStream_t stream);
+
+// Page copies and conversions (oxd_pages.cu).
+struct PagePools {
+    uint8_t* data[2];        // K, V: bf16 rows or codes
+    uint16_t* scales[2];     // nullptr for bf16
+    int64_t num_pages;
+    int32_t layout;
+};
+struct CopyPagesParams {
+    PagePools src, dst;
+    const int32_t* src_pages;
+    const int32_t* dst_pages;
+    const int32_t* refcount; // of dst pages, or nullptr
+    unsigned long long* status;
+    uint32_t* last_epoch;
+    uint32_t epoch;
+    int32_t n, H, page_size;
+};
+cudaError_t launch_copy_pages(const CopyPagesParams& p, cudaStream_t stream);
+
 // Uniform-state merge (the public entry point).
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream);
 // Merge of the split (request, KV head) streams of a decode run, launched

@@ -12,6 +12,8 @@ namespace {
 constexpr int kDeviceBadPage = 1;
 constexpr int kDevicePlanMismatch = 2;
 constexpr int kDeviceWaitTimeout = 3;
+constexpr int kDeviceSharedPage = 4;
+constexpr int kDeviceBadPosition = 5;
 constexpr float kLn2 = 0.693147180559945309f;
 
 // ------------------------------------------------------------------ PTX wrappers
