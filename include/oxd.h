@@ -589,7 +589,7 @@ oxd_status oxd_quant_decode_plan(const oxd_paged_decode_desc* desc, const int32_
  * score product as f16 scaled by a power of two per head (exact for columns
  * within 2^-14 of the head's largest), codes exactly and K's scales in F32; a
  * V value (code times scale) and a softmax weight are each rounded once to
- * f16. Arguments, errors, status codes and determinism as
+ * f16, weights below 2^-24 of the largest to multiples of 2^-34 of it. Arguments, errors, status codes and determinism as
  * oxd_paged_decode_run; the four pools of `cache` are read only.
  */
 oxd_status oxd_quant_decode_run(oxd_plan plan, const void* q, const oxd_kv_pools* cache,

@@ -68,13 +68,14 @@ def tokens(pool, pages, layout):
 
 
 def decode(q, kv, vv, indptr, indices, lengths, layout, sm_scale):
-    """(out, lse, spread, size) in f64: spread = sum w |v| bounds what relative errors of w and v
-    move, size = the largest sum |q k| sm_scale of a row's logits."""
+    """(out, lse, spread, size, total) in f64: spread = sum w |v| bounds what relative errors of w
+    and v move, size = the largest sum |q k| sm_scale of a row's logits, total = sum |v| bounds
+    what an error of every weight by the same small number moves."""
     B, Hq, _ = q.shape
     Hkv = kv.shape[2] if layout == "NHD" else kv.shape[1]
     G = Hq // Hkv
     out, lse = np.zeros((B, Hq, 128)), np.zeros((B, Hq))
-    spread, size = np.zeros((B, Hq, 128)), np.zeros((B, Hq))
+    spread, size, total = np.zeros((B, Hq, 128)), np.zeros((B, Hq)), np.zeros((B, Hq, 128))
     for b in range(B):
         pages = indices[indptr[b]:indptr[b + 1]]
         k = tokens(kv, pages, layout)[:, :lengths[b]]
@@ -89,8 +90,9 @@ def decode(q, kv, vv, indptr, indices, lengths, layout, sm_scale):
             out[b, rows] = w @ v[h] / z
             lse[b, rows] = (m + np.log(z))[:, 0]
             spread[b, rows] = w @ np.abs(v[h]) / z
+            total[b, rows] = np.abs(v[h]).sum(0)
             size[b, rows] = (np.abs(qh) @ np.abs(k[h]).T * abs(sm_scale)).max(-1)
-    return out, lse, spread, size
+    return out, lse, spread, size, total
 
 
 def rotate(x, angle_positions, pair_axis, theta):
