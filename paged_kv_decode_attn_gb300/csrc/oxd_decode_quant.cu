@@ -7,9 +7,12 @@
 // delivers them (about 42 codes a clock and SM) the codes' conversion and the
 // products have to be lean, so
 //   * each of a CTA's four warps streams its own 32-token chunks of the CTA's
-//     work units through a private ring of shared-memory slots (TMA copies that
-//     the warp itself refills; no producer warp, no barrier between warps until
-//     a unit ends);
+//     work units through a private ring of shared-memory slots, which it refills
+//     itself by 16-byte cp.async (9 a lane and chunk); no barrier between warps
+//     until a unit ends. (A page of 16 tokens is 4 bulk copies of 1 KB and 128 B
+//     a head, and a bulk copy with lane-wise operands costs about 20 issue
+//     slots: refilled by TMA, the copies took 234 of 765 instructions a chunk,
+//     and one producer warp a CTA could issue them at half HBM's rate.)
 //   * the tokens are the M dimension of mma.sync m16n8k16 (S^T = K Q^T,
 //     O^T = V^T P^T), so the unpacked codes are the A fragment as they come out
 //     of shared memory, a group of up to 8 heads is one N tile, and neither
@@ -22,11 +25,9 @@
 //     chunks need one warp vote and no reduction or rescaling. P is held in f16
 //     as exp2(x - m + 10): at most 2^14, and full precision down to 2^-24 of
 //     the largest weight.
-// A unit's four warp states are merged through the slots the warps last read;
+// A unit's warp states are merged through the chunks the warps last read;
 // split streams leave F32 partial states for the merge kernel, as in the bf16
-// decode. Waits are bounded: a warp whose wait runs out records it, skips the
-// rest of its work but not the unit barriers, and waits for its copies in
-// flight before it leaves.
+// decode. The only waits are for a warp's own loads and the CTA's barriers.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -39,34 +40,47 @@
 namespace oxd {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr float kLazy = 4.f;     // log2: how far a score may pass the running maximum
 constexpr float kPOffset = 10.f; // log2 of the weight a score at the running maximum gets
 
-// kNT: 8-head tiles a warp holds.
-template <int kNT_, int kStages_, int kCtas_>
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+
+// kNT: 8-head tiles a warp holds. kCtas: resident CTAs a SM, which caps the
+// registers at 65536 / (kThreads * kCtas). kPs: page size.
+template <int kNT_, int kStages_, int kCtas_, int kPs_>
 struct QCfg {
     static constexpr int kNT = kNT_;
     static constexpr int kRows = 8 * kNT;
     static constexpr int kStages = kStages_;
-    static constexpr int kCtas = kCtas_;  // resident CTAs a SM (registers)
-    // slot: K codes | V codes | K scales | V scales of 32 tokens. 512-byte
-    // aligned, the period of the 64-byte swizzle.
+    static constexpr int kCtas = kCtas_;
+    static constexpr int kPs = kPs_;
+    static constexpr int kPagesPerChunk = kPs < kQuantChunk ? kQuantChunk / kPs : 1;
+    static constexpr int kRun = 32 / kPagesPerChunk;  // chunks whose pages a window of 32 holds
+    // slot: K codes | V codes | K scales | V scales of 32 tokens. 16-byte piece
+    // i of a token's codes sits at piece i ^ (token / 2 % 4).
     static constexpr int kVOff = kQuantChunk * kCodeBytes;
     static constexpr int kKsOff = 2 * kVOff;
     static constexpr int kVsOff = kKsOff + kQuantChunk * kScaleBytes;
     static constexpr int kSlotBytes = kVsOff + kQuantChunk * kScaleBytes;
-    static_assert(kSlotBytes % 512 == 0, "slots keep the swizzle phase");
     static_assert(8 * kHeadDim * 4 <= kSlotBytes, "a dumped 8-row state fits a slot");
-    static constexpr int kRingBytes = kWarps * kStages * kSlotBytes;
-    static constexpr int kBarOff = kRingBytes;
-    static constexpr int kRedOff = kBarOff + kWarps * kStages * 8;
-    static constexpr int kFlagOff = kRedOff + 2 * kWarps * 8 * 4;  // abort, dump slot of each warp
-    static constexpr int kSmemBytes = 512 + kFlagOff + 32;
+    static constexpr int kRedOff = kWarps * kStages * kSlotBytes;
+    static constexpr int kFlagOff = kRedOff + 2 * kWarps * 8 * 4;
+    static constexpr int kSmemBytes = kFlagOff + 32;  // dump slot of each warp, unit range
 };
-using CfgQ8 = QCfg<1, 3, 4>;
-using CfgQ16 = QCfg<2, 4, 3>;
+template <int kPs> using CfgQ8 = QCfg<1, 3, 4, kPs>;
+template <int kPs> using CfgQ16 = QCfg<2, 4, 3, kPs>;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -94,6 +108,16 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// D = A * B.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
@@ -145,128 +169,138 @@ __device__ __forceinline__ Unit decode_unit(const DecodeParams& p, const int4 it
 }
 
 // One warp's stream of chunks: the refilling side, up to kStages chunks ahead
-// of the consuming one. Chunk k of the warp in a unit is the unit's chunk
-// warp + 4 k. The page indices of a run of chunks sit in the lanes (`win`,
-// the next run in `ahead`), and the next unit's entry and first indices are
-// read while the current unit's chunks are still being issued.
+// of the consuming one. The warp takes every fourth chunk of a unit. The page
+// indices of a run of its chunks sit in the lanes (`win`, the next run in
+// `ahead`), and the next unit's entry and first indices are read while the
+// current unit's chunks are still being issued.
 template <class C>
 struct Stream {
-    const QuantDecodeParams* qp;
-    const int4* units;
-    int u_end;
-    int warp, lane;
-    uint32_t ring, bars;   // shared addresses of the warp's slots and barriers
-    int rows, ppc, run;    // tokens a box, pages a chunk, chunks a window
-    int unit;              // unit being issued
-    Unit u;
-    int k;                 // next chunk of this warp in it
-    int win, ahead, win_k;
+    int u_end, unit;             // unit being issued
+    int n_pages, n_chunks, first;
+    int c;                       // this warp's next chunk of it
+    int win_c, win, ahead;       // indices of the chunks from win_c on, and of the next run
     int4 nx_it;
     int nx_win;
-    bool nx_have;          // nx_win holds unit + 1's first indices
-    int issued;
+    bool nx_have;                // nx_win holds unit + 1's first indices
+    // this lane's addresses in page 0 of the unit's head: the 16-byte piece
+    // lane % 4 of token lane / 4 of K and V, and the scales of tokens
+    // 2 (lane % 16), + 1 of K (lanes 0..15) or V
+    const uint8_t* k;
+    const uint8_t* v;
+    const uint8_t* sc;
 
-    __device__ __forceinline__ int load_window(const Unit& x, int k0) const {
-        const int ps = qp->d.page_size;
-        const int c = warp + kWarps * (k0 + lane / ppc);
-        const int pg = (c * kQuantChunk) / ps + lane % ppc;
-        int v = 0;
-        if (x.ok && lane / ppc < run && c < x.n_chunks && pg < x.n_pages)
-            v = __ldg(qp->d.indices + x.first + pg);
-        return v;
+    __device__ __forceinline__ int load_window(const int32_t* indices, int c0, int lane) const {
+        const int cc = c0 + kWarps * (lane / C::kPagesPerChunk);
+        const int pg = cc * kQuantChunk / C::kPs + lane % C::kPagesPerChunk;
+        return cc < n_chunks && pg < n_pages ? __ldg(indices + first + pg) : 0;
     }
     // An index outside the pool is recorded and replaced by page 0.
-    __device__ __forceinline__ int check(int v) const {
-        const bool bad = v < 0 || static_cast<int64_t>(v) >= qp->d.num_pages;
+    __device__ __forceinline__ int check(const DecodeParams& p, int i, int lane) const {
+        const bool bad = i < 0 || static_cast<int64_t>(i) >= p.num_pages;
         if (__any_sync(0xffffffffu, bad) && lane == 0)
-            record_status(qp->d.status, qp->d.epoch, kDeviceBadPage);
-        return bad ? 0 : v;
+            record_status(p.status, p.epoch, kDeviceBadPage);
+        return bad ? 0 : i;
     }
-    __device__ __forceinline__ void load_next_item() {
+    __device__ __forceinline__ void enter(const QuantDecodeParams& qp, const int4* units,
+                                          const int4 it, bool have_win, int warp, int lane) {
+        const DecodeParams& p = qp.d;
+        const Unit u = decode_unit(p, it);
+        n_pages = u.n_pages;
+        n_chunks = u.n_chunks;
+        first = u.first;
+        c = win_c = warp;
+        const int h = u.ok ? u.h : 0;
+        const size_t row = row_index(p.layout, 0, (lane >> 2) % C::kPs, h, p.num_kv_heads, C::kPs);
+        k = qp.k_codes + row * kCodeBytes + (lane & 3) * 16;
+        v = qp.v_codes + row * kCodeBytes + (lane & 3) * 16;
+        const int st = 2 * (lane & 15) % C::kPs;
+        sc = reinterpret_cast<const uint8_t*>((lane < 16 ? qp.k_scales : qp.v_scales) +
+                                              scale_index(0, st, h, p.num_kv_heads, C::kPs));
+        win = check(p, have_win ? nx_win : load_window(p.indices, warp, lane), lane);
+        ahead = load_window(p.indices, warp + kWarps * C::kRun, lane);
         if (unit + 1 < u_end) nx_it = __ldg(units + unit + 1);
         nx_have = false;
     }
-    __device__ __forceinline__ void load_next_window() {
-        nx_win = unit + 1 < u_end ? load_window(decode_unit(qp->d, nx_it), 0) : 0;
+    __device__ __forceinline__ void load_next_window(const DecodeParams& p, int warp, int lane) {
+        nx_win = 0;
+        if (unit + 1 < u_end) {
+            const Unit x = decode_unit(p, nx_it);
+            const int cc = warp + kWarps * (lane / C::kPagesPerChunk);
+            const int pg = cc * kQuantChunk / C::kPs + lane % C::kPagesPerChunk;
+            if (cc < x.n_chunks && pg < x.n_pages) nx_win = __ldg(p.indices + x.first + pg);
+        }
         nx_have = true;
     }
-    __device__ __forceinline__ void begin(int u_begin) {
-        unit = u_begin;
-        issued = 0;
-        k = 0;
-        u.ok = false;
-        u.n_chunks = 0;
-        if (unit < u_end) {
-            u = decode_unit(qp->d, __ldg(units + unit));
-            win = check(load_window(u, 0));
-            ahead = load_window(u, run);
-            win_k = 0;
-            load_next_item();
-        }
-    }
-    // Issues the next chunk's copies into its slot, if there is one.
-    __device__ __forceinline__ void refill() {
-        while (unit < u_end && warp + kWarps * k >= u.n_chunks) {
-            if (!nx_have) load_next_window();
+    // Issues the next chunk's copies into `slot`, if there is one; always one
+    // more copy group. `slot` is the shared address, dst / sdst this lane's
+    // offsets in it. Pages past the unit's last are read as page 0.
+    __device__ __forceinline__ void refill(const QuantDecodeParams& qp, const int4* units,
+                                           uint32_t slot, uint32_t dst, uint32_t sdst, int warp,
+                                           int lane) {
+        const DecodeParams& p = qp.d;
+        while (unit < u_end && c >= n_chunks) {
+            if (!nx_have) load_next_window(p, warp, lane);
             ++unit;
-            if (unit < u_end) {
-                u = decode_unit(qp->d, nx_it);
-                win = check(nx_win);
-                ahead = load_window(u, run);
-                win_k = 0;
-                k = 0;
-                load_next_item();
+            if (unit < u_end) enter(qp, units, nx_it, true, warp, lane);
+        }
+        if (unit < u_end) {
+            if (c - win_c >= kWarps * C::kRun) {
+                win = check(p, ahead, lane);
+                win_c += kWarps * C::kRun;
+                ahead = load_window(p.indices, win_c + kWarps * C::kRun, lane);
             }
-        }
-        if (unit >= u_end) return;
-        if (k - win_k >= run) {
-            win = check(ahead);
-            win_k += run;
-            ahead = load_window(u, win_k + run);
-        }
-        const DecodeParams& p = qp->d;
-        const int ps = p.page_size;
-        const int c = warp + kWarps * k;
-        const int pg0 = (c * kQuantChunk) / ps;
-        const int npg = min(ppc, u.n_pages - pg0);
-        const int t0 = ps > kQuantChunk ? (c & 1) * kQuantChunk : 0;
-        const int s = issued % C::kStages;
-        const uint32_t slot = ring + s * C::kSlotBytes;
-        uint64_t* bar = bar_ptr(s);
-        if (lane == 0)
-            mbar_arrive_expect_tx(bar, npg * rows * 2 * (kCodeBytes + kScaleBytes));
-        __syncwarp();
-        // lane 4 j + o: copy o (K codes, V codes, K scales, V scales) of page j
-        const int j = lane >> 2, o = lane & 3;
-        const int page = __shfl_sync(0xffffffffu, win, ((k - win_k) * ppc + j) & 31);
-        if (j < npg) {
-            if (o < 2) {
-                tma_load_4d(slot + (o ? C::kVOff : 0) + j * rows * kCodeBytes, o ? map_v : map_k, bar, 0,
-                            p.layout == 0 ? u.h : t0, p.layout == 0 ? t0 : u.h, page);
-            } else {
-                const uint16_t* src = (o == 2 ? qp->k_scales : qp->v_scales) +
-                                      scale_index(page, t0, u.h, p.num_kv_heads, ps);
-                bulk_load(slot + (o == 2 ? C::kKsOff : C::kVsOff) + j * rows * kScaleBytes, src,
-                          rows * kScaleBytes, bar);
+            const int w0 = (c - win_c) / kWarps * C::kPagesPerChunk;
+            // bytes of one token and of a page
+            const uint32_t tok = p.layout == 0 ? p.num_kv_heads * kCodeBytes : kCodeBytes;
+            const uint32_t page_bytes = p.num_kv_heads * (C::kPs * kCodeBytes);
+            const uint32_t half = C::kPs > kQuantChunk ? (c & 1) * kQuantChunk : 0;
+#pragma unroll
+            for (int i = 0; i < kQuantChunk / 8; ++i) {  // eight tokens of K and of V
+                const uint32_t page = __shfl_sync(0xffffffffu, win, w0 + i * 8 / C::kPs);
+                const size_t off = static_cast<size_t>(page) * page_bytes +
+                                   (half + i * 8 % C::kPs) * tok;
+                cp_async16(slot + dst + i * 8 * kCodeBytes, k + off);
+                cp_async16(slot + dst + C::kVOff + i * 8 * kCodeBytes, v + off);
             }
+            const uint32_t page =
+                __shfl_sync(0xffffffffu, win, w0 + 2 * (lane & 15) / C::kPs);
+            cp_async16(slot + sdst, sc + static_cast<size_t>(page) * (page_bytes / 8) +
+                                        half * kScaleBytes);
+            c += kWarps;
+            if (!nx_have) load_next_window(p, warp, lane);
         }
-        ++issued;
-        ++k;
-        if (!nx_have) load_next_window();
+        cp_async_commit();
     }
-    const CUtensorMap* map_k;
-    const CUtensorMap* map_v;
-    uint64_t* bar_base;
-    __device__ __forceinline__ uint64_t* bar_ptr(int s) const { return bar_base + s; }
 };
 
 template <class C>
 struct State {
     uint32_t q[C::kNT][8][2];  // B fragments of the query rows, one pair per 16 columns
-    float sc[C::kNT][2];       // logit scale (log2) of heads 2 tq, 2 tq + 1
+    float sc[C::kNT][2];       // logit scale (log2) of heads 2 tq, 2 tq + 1, positive
     float m[C::kNT][2], l[C::kNT][2];
     float acc[C::kNT][8][4];
+    // This lane's offsets in a slot: its ldmatrix row and 16-byte chunk (chunk
+    // c + 2 is 32 bytes away in the XOR), its K scales, and the codes and
+    // scales of its two V tokens of an 8-token block. Eight tokens on, the
+    // swizzle repeats, so everything else is a constant.
+    uint32_t k_off, ks_off, v_off[2], vs_off[2];
 
+    __device__ __forceinline__ void set_lane(int lane) {
+        const int g = lane >> 2, tq = lane & 3;
+        const int kt = ((lane >> 3) & 1) * 8 + row_token(lane & 7);
+        k_off = kt * kCodeBytes + (((lane >> 4) ^ ((kt >> 1) & 3)) << 4);
+        ks_off = C::kKsOff + row_token(g) * kScaleBytes;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = row_token(2 * tq + i);
+            v_off[i] = C::kVOff + t * kCodeBytes + (((g >> 1) ^ ((t >> 1) & 3)) << 4) + (g & 1) * 8;
+            vs_off[i] = C::kVsOff + t * kScaleBytes + (g >> 1) * 2;
+        }
+    }
+
+    // A negative scale's sign goes into q, and a scale of zero becomes the
+    // smallest normal number (logits below 2^-100), so a masked score of -inf
+    // stays one.
     // Columns 32 c + 8 tq .. + 8 of head g feed the two k steps of group c, in
     // the order the codes of a token leave its word. q is scaled by a power of
     // two so that the head's largest size lies in [1, 2) (f16's range).
@@ -296,7 +330,7 @@ struct State {
             // exponent field of the largest size, kept where 2^+-exponent is a
             // normal float
             const uint32_t e = min(max(top >> 7, 1u), 253u);
-            const float f = __uint_as_float((254u - e) << 23);
+            const float f = copysignf(__uint_as_float((254u - e) << 23), scale_log2);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 q[n][i >> 1][i & 1] = pack_f16x2(__uint_as_float(w[i] << 16) * f,
@@ -304,7 +338,7 @@ struct State {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const uint32_t eh = __shfl_sync(0xffffffffu, e, (2 * tq + j) * 4);
-                sc[n][j] = scale_log2 * __uint_as_float(eh << 23);
+                sc[n][j] = fmaxf(fabsf(scale_log2) * __uint_as_float(eh << 23), 1.17549435e-38f);
                 m[n][j] = -INFINITY;
                 l[n][j] = 0.f;
             }
@@ -314,19 +348,17 @@ struct State {
         }
     }
 
-    // One chunk: tokens [u0, u0 + 32) of the unit, in `slot`.
-    __device__ __forceinline__ void consume(uint32_t slot, int u0, int valid, int lane) {
-        const int g = lane >> 2, tq = lane & 3;
-        const int pg = row_token(g);
+    // One chunk of 32 tokens at `chunk`, of which the first `left` are there.
+    template <bool kPartial>
+    __device__ __forceinline__ void consume(uint32_t chunk, int left, int lane) {
+        const int tq = lane & 3;
+        const int pg = row_token(lane >> 2);
         // ---- S^T = K Q^T
         float s[2][C::kNT][4];
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
-            const int tok = tb * 16 + ((lane >> 3) & 1) * 8 + row_token(lane & 7);
-            const uint32_t row = slot + tok * kCodeBytes;
-            const uint32_t sw = (tok >> 1) & 3;
-            const uint2 k0 = lds64(slot + C::kKsOff + (tb * 16 + pg) * kScaleBytes);
-            const uint2 k1 = lds64(slot + C::kKsOff + (tb * 16 + 8 + pg) * kScaleBytes);
+            const uint2 k0 = lds64(chunk + ks_off + tb * 16 * kScaleBytes);
+            const uint2 k1 = lds64(chunk + ks_off + (tb * 16 + 8) * kScaleBytes);
             const float2 s01 = f16x2_floats(k0.x), s23 = f16x2_floats(k0.y);
             const float2 t01 = f16x2_floats(k1.x), t23 = f16x2_floats(k1.y);
             const float ks0[4] = {s01.x, s01.y, s23.x, s23.y};
@@ -334,7 +366,7 @@ struct State {
 #pragma unroll
             for (int c = 0; c < 4; c += 2) {
                 uint32_t w[4];
-                ldsm_x4(row + (((c + (lane >> 4)) ^ sw) << 4), w);
+                ldsm_x4(chunk + (k_off ^ (c << 4)) + tb * 16 * kCodeBytes, w);
 #pragma unroll
                 for (int cc = 0; cc < 2; ++cc) {
                     uint32_t a[4], b[4];
@@ -343,8 +375,8 @@ struct State {
                     const int grp = c + cc;
 #pragma unroll
                     for (int n = 0; n < C::kNT; ++n) {
-                        float t[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma_f16(t, a[0], b[0], a[1], b[1], q[n][2 * grp][0], q[n][2 * grp][1]);
+                        float t[4];
+                        mma_f16_zero(t, a[0], b[0], a[1], b[1], q[n][2 * grp][0], q[n][2 * grp][1]);
                         mma_f16(t, a[2], b[2], a[3], b[3], q[n][2 * grp + 1][0],
                                 q[n][2 * grp + 1][1]);
                         if (grp == 0) {
@@ -362,26 +394,22 @@ struct State {
                 }
             }
         }
-        // ---- online softmax in the log2 domain
-        const bool partial = u0 + kQuantChunk > valid;
+        // ---- online softmax in the log2 domain: score s counts as s * sc
         bool raise = false;
         float mx[C::kNT][2];
 #pragma unroll
         for (int n = 0; n < C::kNT; ++n) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
+                if constexpr (kPartial) {
 #pragma unroll
-                for (int tb = 0; tb < 2; ++tb) {
-                    s[tb][n][j] *= sc[n][j];
-                    s[tb][n][2 + j] *= sc[n][j];
-                    if (partial) {
-                        const int t = u0 + tb * 16 + pg;
-                        if (t >= valid) s[tb][n][j] = -INFINITY;
-                        if (t + 8 >= valid) s[tb][n][2 + j] = -INFINITY;
+                    for (int tb = 0; tb < 2; ++tb) {
+                        if (tb * 16 + pg >= left) s[tb][n][j] = -INFINITY;
+                        if (tb * 16 + 8 + pg >= left) s[tb][n][2 + j] = -INFINITY;
                     }
                 }
                 mx[n][j] = fmaxf(fmaxf(s[0][n][j], s[0][n][2 + j]),
-                                 fmaxf(s[1][n][j], s[1][n][2 + j]));
+                                 fmaxf(s[1][n][j], s[1][n][2 + j])) * sc[n][j];
                 raise = raise || mx[n][j] > m[n][j] + kLazy;
             }
         }
@@ -414,11 +442,11 @@ struct State {
         for (int n = 0; n < C::kNT; ++n) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float mu = m[n][j] == -INFINITY ? 0.f : m[n][j] - kPOffset;
+                const float mu = m[n][j] == -INFINITY ? 0.f : kPOffset - m[n][j];
 #pragma unroll
                 for (int tb = 0; tb < 2; ++tb) {
-                    s[tb][n][j] = fast_exp2(s[tb][n][j] - mu);
-                    s[tb][n][2 + j] = fast_exp2(s[tb][n][2 + j] - mu);
+                    s[tb][n][j] = fast_exp2(fmaf(s[tb][n][j], sc[n][j], mu));
+                    s[tb][n][2 + j] = fast_exp2(fmaf(s[tb][n][2 + j], sc[n][j], mu));
                 }
                 l[n][j] += (s[0][n][j] + s[0][n][2 + j]) + (s[1][n][j] + s[1][n][2 + j]);
             }
@@ -436,12 +464,11 @@ struct State {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 // MMA columns 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9
-                const int tok = tb * 16 + (i >> 1) * 8 + ((2 * tq + (i & 1)) ^ (tq & 1));
-                x[i] = lds64(slot + C::kVOff + tok * kCodeBytes +
-                             ((((g >> 1) ^ (tok >> 1)) & 3) << 4) + (g & 1) * 8);
-                vs[i] = lds16(slot + C::kVsOff + tok * kScaleBytes + (g >> 1) * 2);
+                const int t = tb * 16 + (i >> 1) * 8;
+                x[i] = lds64(chunk + v_off[i & 1] + t * kCodeBytes);
+                vs[i] = lds16(chunk + vs_off[i & 1] + t * kScaleBytes);
                 // rows past the last token may hold anything, NaN scales too
-                if (partial && u0 + tok >= valid) vs[i] = 0u;
+                if (kPartial && t + row_token(2 * tq + (i & 1)) >= left) vs[i] = 0u;
             }
             const uint32_t sa = vs[0] | (vs[1] << 16), sb = vs[2] | (vs[3] << 16);
             constexpr uint32_t kLow = 0x0f0f0f0fu;
@@ -496,34 +523,21 @@ struct State {
 
 template <class C, class WL>
 __global__ void __launch_bounds__(kThreads, C::kCtas)
-    quant_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
-                        const __grid_constant__ CUtensorMap tmap_v,
-                        const __grid_constant__ QuantDecodeParams qp,
+    quant_decode_kernel(const __grid_constant__ QuantDecodeParams qp,
                         const __grid_constant__ WL work) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 511) &
-                                               ~static_cast<uintptr_t>(511));
+    extern __shared__ __align__(128) uint8_t base[];
     const DecodeParams& p = qp.d;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kBarOff);
     float* red_m = reinterpret_cast<float*>(base + C::kRedOff);
     float* red_l = red_m + kWarps * 8;
-    volatile int* flags = reinterpret_cast<volatile int*>(base + C::kFlagOff);  // [0] abort
-    volatile int* dump_slot = flags + 1;  // [warp]: the slot its state is dumped in, or -1
+    volatile int* dump_slot = reinterpret_cast<volatile int*>(base + C::kFlagOff);  // [warp] or -1
+    volatile int* range = dump_slot + kWarps;  // first unit, end unit
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kWarps * C::kStages; ++i) mbar_init(bars + i, 1);
-        flags[0] = 0;
-        fence_mbar_init();
-        prefetch_tmap(&tmap_k);
-        prefetch_tmap(&tmap_v);
-    }
     // as a programmatic dependent: nothing in global memory before this
     grid_dependency_wait();
     // This CTA's units, from the parameter buffer or the workspace; one thread
     // reads the range, so every warp passes the same number of barriers.
     const int4* units = p.units;
-    volatile int* range = flags + 1;  // (first, end), before the dump slots are used
     if (threadIdx.x == 0) {
         if (blockIdx.x == 0) {
             *p.last_epoch = p.epoch;
@@ -556,33 +570,26 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     }
     __syncthreads();
     const int u_begin = range[0], u_end = range[1];
-    __syncthreads();
 
+    uint8_t* ring = base + warp * C::kStages * C::kSlotBytes;
+    const uint32_t ring_addr = smem_addr(ring);
+    const uint32_t dst =
+        (lane >> 2) * kCodeBytes + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+    const uint32_t sdst = (lane < 16 ? C::kKsOff : C::kVsOff) + (lane & 15) * 16;
     Stream<C> in;
-    in.qp = &qp;
-    in.units = units;
     in.u_end = u_end;
-    in.warp = warp;
-    in.lane = lane;
-    in.ring = smem_addr(base) + warp * C::kStages * C::kSlotBytes;
-    in.bar_base = bars + warp * C::kStages;
-    in.map_k = &tmap_k;
-    in.map_v = &tmap_v;
-    in.rows = min(p.page_size, kQuantChunk);
-    in.ppc = kQuantChunk / in.rows;
-    in.run = 32 / in.ppc;
-    in.begin(u_begin);
-    for (int i = 0; i < C::kStages; ++i) in.refill();
+    in.unit = u_begin;
+    if (u_begin < u_end) in.enter(qp, units, __ldg(units + u_begin), false, warp, lane);
+    for (int i = 0; i < C::kStages; ++i)
+        in.refill(qp, units, ring_addr + i * C::kSlotBytes, dst, sdst, warp, lane);
 
     State<C> st;
-    bool dead = false;   // a wait of this warp ran out
-    int taken = 0;       // chunks consumed
+    st.set_lane(lane);
+    int slot = 0;  // of the next chunk
     const int G = p.group;
-    int4 it = u_begin < u_end ? __ldg(units + u_begin) : make_int4(0, 0, 0, 0);
     for (int ui = u_begin; ui < u_end; ++ui) {
-        const int4 it_now = it;
-        const Unit u = decode_unit(p, it_now);
-        if (ui + 1 < u_end) it = __ldg(units + ui + 1);
+        const int4 it = __ldg(units + ui);
+        const Unit u = decode_unit(p, it);
         const int nrows = min(G - u.row0, C::kRows);
         const size_t row_base =
             static_cast<size_t>(u.b) * p.num_qo_heads + u.h * G + u.row0;
@@ -590,41 +597,38 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
             if (!u.ok) {
                 record_status(p.status, p.epoch, kDevicePlanMismatch);
             } else {
-                const int last_len = (it_now.y >> kUnitPagesBits) & 0x7f;
-                if ((it_now.y < 0 && p.indptr[u.b] != it_now.x) ||
-                    (last_len && (p.indptr[u.b + 1] != it_now.x + u.n_pages ||
+                const int last_len = (it.y >> kUnitPagesBits) & 0x7f;
+                if ((it.y < 0 && p.indptr[u.b] != it.x) ||
+                    (last_len && (p.indptr[u.b + 1] != it.x + u.n_pages ||
                                   p.last_page_len[u.b] != last_len)))
                     record_status(p.status, p.epoch, kDevicePlanMismatch);
             }
         }
         int held = -1;  // the slot of the warp's last chunk, not refilled yet
         if (warp < u.n_chunks) st.init(p.q + row_base * kHeadDim, nrows, p.scale_log2, lane);
-        for (int c = warp; c < u.n_chunks && !dead; c += kWarps) {
-            const int s = taken % C::kStages;
-            const bool got = mbar_wait(in.bar_ptr(s), (taken / C::kStages) & 1, flags, p.wait_ns);
-            if (!__all_sync(0xffffffffu, got)) {
-                dead = true;
-                if (lane == 0) {
-                    flags[0] = 1;
-                    record_status(p.status, p.epoch, kDeviceWaitTimeout);
-                }
-                break;
-            }
-            ++taken;
-            st.consume(in.ring + s * C::kSlotBytes, c * kQuantChunk, u.valid, lane);
+        for (int c = warp; c < u.n_chunks; c += kWarps) {
+            cp_async_wait<C::kStages - 1>();
+            __syncwarp();  // every lane's copies of the chunk have landed
+            const uint32_t chunk = ring_addr + slot * C::kSlotBytes;
+            const int left = u.valid - c * kQuantChunk;
+            if (left >= kQuantChunk)
+                st.template consume<false>(chunk, left, lane);
+            else
+                st.template consume<true>(chunk, left, lane);
             __syncwarp();
             if (c + kWarps < u.n_chunks)
-                in.refill();
+                in.refill(qp, units, chunk, dst, sdst, warp, lane);
             else
-                held = s;
+                held = slot;
+            slot = slot + 1 == C::kStages ? 0 : slot + 1;
         }
-        // ---- merge the warps' states, eight rows at a time
+        // ---- merge the warps' states, eight rows at a time, each through the
+        // slot its warp read last
 #pragma unroll
         for (int n = 0; n < C::kNT; ++n) {
             if (lane == 0) dump_slot[warp] = held;
             if (held >= 0)
-                st.dump(n,
-                        reinterpret_cast<float*>(base + (warp * C::kStages + held) * C::kSlotBytes),
+                st.dump(n, reinterpret_cast<float*>(ring + held * C::kSlotBytes),
                         red_m + warp * 8, red_l + warp * 8, lane);
             __syncthreads();
             const int rows = u.ok ? min(8, nrows - n * 8) : 0;
@@ -672,18 +676,10 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
             }
             __syncthreads();
         }
-        if (held >= 0) {
-            // the dump was written and read by plain accesses; the next copy
-            // into the slot comes from the async proxy
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            in.refill();
-        }
+        if (held >= 0)
+            in.refill(qp, units, ring_addr + held * C::kSlotBytes, dst, sdst, warp, lane);
     }
-    // Copies in flight (after a wait ran out, or issued from a list that changed
-    // meanwhile) land before the CTA leaves.
-    for (; taken < in.issued; ++taken)
-        mbar_wait(in.bar_ptr(taken % C::kStages), (taken / C::kStages) & 1, nullptr, kWaitTimeoutNs);
+    cp_async_wait<0>();
 }
 
 template <class C, class WL>
@@ -701,8 +697,8 @@ cudaError_t ensure_smem() {
 }
 
 template <class C, class WL>
-cudaError_t launch_ex(const CUtensorMap& tk, const CUtensorMap& tv, const QuantDecodeParams& p,
-                      const WL& w, int grid, cudaStream_t stream, bool pdl) {
+cudaError_t launch_ex(const QuantDecodeParams& p, const WL& w, int grid, cudaStream_t stream,
+                      bool pdl) {
     const cudaError_t e = ensure_smem<C, WL>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -715,14 +711,26 @@ cudaError_t launch_ex(const CUtensorMap& tk, const CUtensorMap& tv, const QuantD
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, quant_decode_kernel<C, WL>, tk, tv, p, w);
+    return cudaLaunchKernelEx(&cfg, quant_decode_kernel<C, WL>, p, w);
 }
 
 template <class C>
-cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const QuantDecodeParams& p,
-                   const WorkList* w, int grid, cudaStream_t stream, bool pdl) {
-    if (w != nullptr) return launch_ex<C>(tk, tv, p, *w, grid, stream, pdl);
-    return launch_ex<C>(tk, tv, p, NoList{0}, grid, stream, pdl);
+cudaError_t launch(const QuantDecodeParams& p, const WorkList* w, int grid, cudaStream_t stream,
+                   bool pdl) {
+    if (w != nullptr) return launch_ex<C>(p, *w, grid, stream, pdl);
+    return launch_ex<C>(p, NoList{0}, grid, stream, pdl);
+}
+
+template <template <int> class C>
+cudaError_t launch_ps(const QuantDecodeParams& p, const WorkList* w, int grid, cudaStream_t stream,
+                      bool pdl) {
+    switch (p.d.page_size) {
+        case 8: return launch<C<8>>(p, w, grid, stream, pdl);
+        case 16: return launch<C<16>>(p, w, grid, stream, pdl);
+        case 32: return launch<C<32>>(p, w, grid, stream, pdl);
+        case 64: return launch<C<64>>(p, w, grid, stream, pdl);
+    }
+    return cudaErrorInvalidValue;
 }
 
 template <class C>
@@ -733,23 +741,27 @@ cudaError_t occupancy(int* n) {
                                                          kThreads, C::kSmemBytes);
 }
 
+template <class C>
+VariantShape shape() {
+    return {kThreads, kWarps * kQuantChunk, C::kStages, C::kSmemBytes};
+}
+
 }  // namespace
 
+// The page size changes neither the registers (capped by the launch bound) nor
+// the shared memory.
 VariantShape quant_shape(int variant) {
-    if (variant == kVariantQuant8)
-        return {kThreads, kWarps * kQuantChunk, CfgQ8::kStages, CfgQ8::kSmemBytes};
-    return {kThreads, kWarps * kQuantChunk, CfgQ16::kStages, CfgQ16::kSmemBytes};
+    return variant == kVariantQuant8 ? shape<CfgQ8<16>>() : shape<CfgQ16<16>>();
 }
 
 cudaError_t quant_occupancy(int variant, int* n) {
-    return variant == kVariantQuant8 ? occupancy<CfgQ8>(n) : occupancy<CfgQ16>(n);
+    return variant == kVariantQuant8 ? occupancy<CfgQ8<16>>(n) : occupancy<CfgQ16<16>>(n);
 }
 
-cudaError_t launch_decode_quant(int variant, const CUtensorMap& tk, const CUtensorMap& tv,
-                                const QuantDecodeParams& p, const WorkList* w, int grid,
-                                cudaStream_t stream, bool pdl) {
-    if (variant == kVariantQuant8) return launch<CfgQ8>(tk, tv, p, w, grid, stream, pdl);
-    return launch<CfgQ16>(tk, tv, p, w, grid, stream, pdl);
+cudaError_t launch_decode_quant(int variant, const QuantDecodeParams& p, const WorkList* w,
+                                int grid, cudaStream_t stream, bool pdl) {
+    if (variant == kVariantQuant8) return launch_ps<CfgQ8>(p, w, grid, stream, pdl);
+    return launch_ps<CfgQ16>(p, w, grid, stream, pdl);
 }
 
 }  // namespace oxd

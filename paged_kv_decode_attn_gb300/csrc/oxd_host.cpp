@@ -154,27 +154,6 @@ bool encode_pool(CUtensorMap* map, const void* pool, const oxd_paged_decode_desc
     return encode_kv_pool(map, pool, d.layout, d.page_size, d.num_kv_heads, d.num_pages);
 }
 
-// 4-D map over a pool of 4-bit codes: (byte, A, B, page) with (A, B) = (head,
-// token) for NHD and (token, head) for HND; a box is the 64 code bytes of up to
-// 32 tokens of one page and head, stored with the 64-byte swizzle.
-bool encode_code_pool(CUtensorMap* map, const void* pool, const oxd_paged_decode_desc& d) {
-    EncodeTiledFn enc = get_encoder();
-    if (enc == nullptr) return false;
-    const cuuint64_t ps = static_cast<cuuint64_t>(d.page_size);
-    const cuuint64_t H = static_cast<cuuint64_t>(d.num_kv_heads);
-    const cuuint32_t rows = static_cast<cuuint32_t>(std::min(d.page_size, kQuantChunk));
-    const bool nhd = d.layout == OXD_LAYOUT_NHD;
-    const cuuint64_t dims[4] = {kCodeBytes, nhd ? H : ps, nhd ? ps : H,
-                                static_cast<cuuint64_t>(d.num_pages)};
-    const cuuint64_t strides[3] = {kCodeBytes, (nhd ? H : ps) * kCodeBytes, ps * H * kCodeBytes};
-    const cuuint32_t box[4] = {kCodeBytes, nhd ? 1u : rows, nhd ? rows : 1u, 1u};
-    const cuuint32_t elem[4] = {1, 1, 1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pool), dims, strides,
-                     box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
 // 2-D map over q as [B*Hq rows][128] for the tcgen05 variant: a box is 32
 // rows x 64 columns with the 128-byte swizzle its score MMA reads; rows past
 // the end read as zeros.
@@ -1139,10 +1118,6 @@ oxd_status oxd_quant_decode_run(oxd_plan plan, const void* q, const oxd_kv_pools
     const oxd_status chk = check_run(plan, q, pools, 4, indptr, indices, last_page_len, sm_scale,
                                      out, lse, workspace, workspace_bytes);
     if (chk != OXD_OK) return chk;
-    CUtensorMap tk, tv;
-    if (!encode_code_pool(&tk, cache->k, d) || !encode_code_pool(&tv, cache->v, d))
-        return OXD_ERR_CUDA;
-
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const bool bound = plan->bound_ws.load() == workspace;
@@ -1158,8 +1133,8 @@ oxd_status oxd_quant_decode_run(oxd_plan plan, const void* q, const oxd_kv_pools
     if (plan->ev_before != nullptr && cudaEventRecord(plan->ev_before, s) != cudaSuccess)
         return OXD_ERR_CUDA;
     const bool pdl = d.pdl != 0 && plan->ev_before == nullptr && !(!bound && plan->upload);
-    if (launch_decode_quant(plan->variant, tk, tv, p, in_ws ? nullptr : plan->work, plan->grid, s,
-                            pdl) != cudaSuccess)
+    if (launch_decode_quant(plan->variant, p, in_ws ? nullptr : plan->work, plan->grid, s, pdl) !=
+        cudaSuccess)
         return OXD_ERR_CUDA;
     if (plan->ev_after != nullptr && cudaEventRecord(plan->ev_after, s) != cudaSuccess)
         return OXD_ERR_CUDA;

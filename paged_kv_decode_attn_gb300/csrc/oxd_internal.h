@@ -187,8 +187,7 @@ cudaError_t wide_occupancy(int* ctas_per_sm);
 cudaError_t launch_decode_wide(const CUtensorMap& tk, const CUtensorMap& tv,
                                const CUtensorMap& tq, const DecodeParams& p, const WorkList* w,
                                int grid, cudaStream_t stream, bool pdl);
-// Decode over a 4-bit cache (oxd_decode_quant.cu). tk, tv: maps over the code
-// pools (64-byte swizzle, boxes of up to kQuantChunk tokens).
+// Decode over a 4-bit cache (oxd_decode_quant.cu).
 constexpr int kCodeBytes = 64;   // 4-bit codes of one (token, head) row
 constexpr int kScaleBytes = 8;   // its four f16 scales
 constexpr int kQuantChunk = 32;  // tokens a consumer warp takes at a time
@@ -201,9 +200,8 @@ struct QuantDecodeParams {
 };
 VariantShape quant_shape(int variant);
 cudaError_t quant_occupancy(int variant, int* ctas_per_sm);
-cudaError_t launch_decode_quant(int variant, const CUtensorMap& tk, const CUtensorMap& tv,
-                                const QuantDecodeParams& p, const WorkList* w, int grid,
-                                cudaStream_t stream, bool pdl);
+cudaError_t launch_decode_quant(int variant, const QuantDecodeParams& p, const WorkList* w,
+                                int grid, cudaStream_t stream, bool pdl);
 
 // RoPE with position axes + paged append, into bf16 or 4-bit pages
 // (oxd_append_axes.cu).
