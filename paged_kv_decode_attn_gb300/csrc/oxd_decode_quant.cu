@@ -151,17 +151,18 @@ struct Unit {
     bool ok;
 };
 
-__device__ __forceinline__ Unit decode_unit(const DecodeParams& p, const int4 it) {
+__device__ __forceinline__ Unit decode_unit(const QuantDecodeParams& qp, const int4 it) {
+    const DecodeParams& p = qp.d;
     Unit u;
     u.first = it.x;
     u.n_pages = it.y & ((1 << kUnitPagesBits) - 1);
     const int last_len = (it.y >> kUnitPagesBits) & 0x7f;  // 0: not the request's last page
     u.b = it.z & ((1 << kUnitBBits) - 1);
     u.row0 = ((it.z >> kUnitBBits) & 1) * 16;
-    u.h = static_cast<int>(static_cast<uint32_t>(it.z) >> (kUnitBBits + 1));
+    u.h = static_cast<int>(static_cast<uint32_t>(it.z) >> (kUnitBBits + 1)) * qp.heads;
     u.slot = it.w;
     u.ok = u.n_pages >= 1 && it.x >= 0 && static_cast<int64_t>(it.x) + u.n_pages <= p.nnz &&
-           u.b < p.batch && u.h < p.num_kv_heads && u.row0 < p.group && it.w >= -1 &&
+           u.b < p.batch && u.h + qp.heads <= p.num_kv_heads && u.row0 < p.group && it.w >= -1 &&
            it.w < p.n_slots && last_len <= p.page_size;
     u.valid = last_len ? (u.n_pages - 1) * p.page_size + last_len : u.n_pages * p.page_size;
     u.n_chunks = u.ok ? (u.valid + kQuantChunk - 1) / kQuantChunk : 0;
@@ -169,12 +170,15 @@ __device__ __forceinline__ Unit decode_unit(const DecodeParams& p, const int4 it
 }
 
 // One warp's stream of chunks: the refilling side, up to kStages chunks ahead
-// of the consuming one. The warp takes every fourth chunk of a unit. The page
+// of the consuming one. The warp takes every fourth chunk of a unit (every
+// second one where a unit covers two heads). The page
 // indices of a run of its chunks sit in the lanes (`win`, the next run in
 // `ahead`), and the next unit's entry and first indices are read while the
 // current unit's chunks are still being issued.
 template <class C>
 struct Stream {
+    int wl2;                     // log2 of the warps that share a head
+    int w, head;                 // this warp's place among them, and which head
     int u_end, unit;             // unit being issued
     int n_pages, n_chunks, first;
     int c;                       // this warp's next chunk of it
@@ -190,7 +194,7 @@ struct Stream {
     const uint8_t* sc;
 
     __device__ __forceinline__ int load_window(const int32_t* indices, int c0, int lane) const {
-        const int cc = c0 + kWarps * (lane / C::kPagesPerChunk);
+        const int cc = c0 + ((lane / C::kPagesPerChunk) << wl2);
         const int pg = cc * kQuantChunk / C::kPs + lane % C::kPagesPerChunk;
         return cc < n_chunks && pg < n_pages ? __ldg(indices + first + pg) : 0;
     }
@@ -202,32 +206,32 @@ struct Stream {
         return bad ? 0 : i;
     }
     __device__ __forceinline__ void enter(const QuantDecodeParams& qp, const int4* units,
-                                          const int4 it, bool have_win, int warp, int lane) {
+                                          const int4 it, bool have_win, int lane) {
         const DecodeParams& p = qp.d;
-        const Unit u = decode_unit(p, it);
+        const Unit u = decode_unit(qp, it);
         n_pages = u.n_pages;
         n_chunks = u.n_chunks;
         first = u.first;
-        c = win_c = warp;
-        const int h = u.ok ? u.h : 0;
+        c = win_c = w;
+        const int h = u.ok ? u.h + head : 0;
         const size_t row = row_index(p.layout, 0, (lane >> 2) % C::kPs, h, p.num_kv_heads, C::kPs);
         k = qp.k_codes + row * kCodeBytes + (lane & 3) * 16;
         v = qp.v_codes + row * kCodeBytes + (lane & 3) * 16;
         const int st = 2 * (lane & 15) % C::kPs;
         sc = reinterpret_cast<const uint8_t*>((lane < 16 ? qp.k_scales : qp.v_scales) +
                                               scale_index(0, st, h, p.num_kv_heads, C::kPs));
-        win = check(p, have_win ? nx_win : load_window(p.indices, warp, lane), lane);
-        ahead = load_window(p.indices, warp + kWarps * C::kRun, lane);
+        win = check(p, have_win ? nx_win : load_window(p.indices, w, lane), lane);
+        ahead = load_window(p.indices, w + (C::kRun << wl2), lane);
         if (unit + 1 < u_end) nx_it = __ldg(units + unit + 1);
         nx_have = false;
     }
-    __device__ __forceinline__ void load_next_window(const DecodeParams& p, int warp, int lane) {
+    __device__ __forceinline__ void load_next_window(const QuantDecodeParams& qp, int lane) {
         nx_win = 0;
         if (unit + 1 < u_end) {
-            const Unit x = decode_unit(p, nx_it);
-            const int cc = warp + kWarps * (lane / C::kPagesPerChunk);
+            const Unit x = decode_unit(qp, nx_it);
+            const int cc = w + ((lane / C::kPagesPerChunk) << wl2);
             const int pg = cc * kQuantChunk / C::kPs + lane % C::kPagesPerChunk;
-            if (cc < x.n_chunks && pg < x.n_pages) nx_win = __ldg(p.indices + x.first + pg);
+            if (cc < x.n_chunks && pg < x.n_pages) nx_win = __ldg(qp.d.indices + x.first + pg);
         }
         nx_have = true;
     }
@@ -235,21 +239,21 @@ struct Stream {
     // more copy group. `slot` is the shared address, dst / sdst this lane's
     // offsets in it. Pages past the unit's last are read as page 0.
     __device__ __forceinline__ void refill(const QuantDecodeParams& qp, const int4* units,
-                                           uint32_t slot, uint32_t dst, uint32_t sdst, int warp,
+                                           uint32_t slot, uint32_t dst, uint32_t sdst,
                                            int lane) {
         const DecodeParams& p = qp.d;
         while (unit < u_end && c >= n_chunks) {
-            if (!nx_have) load_next_window(p, warp, lane);
+            if (!nx_have) load_next_window(qp, lane);
             ++unit;
-            if (unit < u_end) enter(qp, units, nx_it, true, warp, lane);
+            if (unit < u_end) enter(qp, units, nx_it, true, lane);
         }
         if (unit < u_end) {
-            if (c - win_c >= kWarps * C::kRun) {
+            if (c - win_c >= C::kRun << wl2) {
                 win = check(p, ahead, lane);
-                win_c += kWarps * C::kRun;
-                ahead = load_window(p.indices, win_c + kWarps * C::kRun, lane);
+                win_c += C::kRun << wl2;
+                ahead = load_window(p.indices, win_c + (C::kRun << wl2), lane);
             }
-            const int w0 = (c - win_c) / kWarps * C::kPagesPerChunk;
+            const int w0 = ((c - win_c) >> wl2) * C::kPagesPerChunk;
             // bytes of one token and of a page
             const uint32_t tok = p.layout == 0 ? p.num_kv_heads * kCodeBytes : kCodeBytes;
             const uint32_t page_bytes = p.num_kv_heads * (C::kPs * kCodeBytes);
@@ -266,8 +270,8 @@ struct Stream {
                 __shfl_sync(0xffffffffu, win, w0 + 2 * (lane & 15) / C::kPs);
             cp_async16(slot + sdst, sc + static_cast<size_t>(page) * (page_bytes / 8) +
                                         half * kScaleBytes);
-            c += kWarps;
-            if (!nx_have) load_next_window(p, warp, lane);
+            c += 1 << wl2;
+            if (!nx_have) load_next_window(qp, lane);
         }
         cp_async_commit();
     }
@@ -577,11 +581,14 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         (lane >> 2) * kCodeBytes + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
     const uint32_t sdst = (lane < 16 ? C::kKsOff : C::kVsOff) + (lane & 15) * 16;
     Stream<C> in;
+    in.wl2 = qp.heads == 2 ? 1 : 2;
+    in.w = warp & ((1 << in.wl2) - 1);
+    in.head = warp >> in.wl2;
     in.u_end = u_end;
     in.unit = u_begin;
-    if (u_begin < u_end) in.enter(qp, units, __ldg(units + u_begin), false, warp, lane);
+    if (u_begin < u_end) in.enter(qp, units, __ldg(units + u_begin), false, lane);
     for (int i = 0; i < C::kStages; ++i)
-        in.refill(qp, units, ring_addr + i * C::kSlotBytes, dst, sdst, warp, lane);
+        in.refill(qp, units, ring_addr + i * C::kSlotBytes, dst, sdst, lane);
 
     State<C> st;
     st.set_lane(lane);
@@ -589,8 +596,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     const int G = p.group;
     for (int ui = u_begin; ui < u_end; ++ui) {
         const int4 it = __ldg(units + ui);
-        const Unit u = decode_unit(p, it);
+        const Unit u = decode_unit(qp, it);
         const int nrows = min(G - u.row0, C::kRows);
+        // first query row of the unit's first head; the next head's are G on
         const size_t row_base =
             static_cast<size_t>(u.b) * p.num_qo_heads + u.h * G + u.row0;
         if (threadIdx.x == 0) {
@@ -605,8 +613,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
             }
         }
         int held = -1;  // the slot of the warp's last chunk, not refilled yet
-        if (warp < u.n_chunks) st.init(p.q + row_base * kHeadDim, nrows, p.scale_log2, lane);
-        for (int c = warp; c < u.n_chunks; c += kWarps) {
+        if (in.w < u.n_chunks)
+            st.init(p.q + (row_base + in.head * G) * kHeadDim, nrows, p.scale_log2, lane);
+        for (int c = in.w; c < u.n_chunks; c += 1 << in.wl2) {
             cp_async_wait<C::kStages - 1>();
             __syncwarp();  // every lane's copies of the chunk have landed
             const uint32_t chunk = ring_addr + slot * C::kSlotBytes;
@@ -616,8 +625,8 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
             else
                 st.template consume<true>(chunk, left, lane);
             __syncwarp();
-            if (c + kWarps < u.n_chunks)
-                in.refill(qp, units, chunk, dst, sdst, warp, lane);
+            if (c + (1 << in.wl2) < u.n_chunks)
+                in.refill(qp, units, chunk, dst, sdst, lane);
             else
                 held = slot;
             slot = slot + 1 == C::kStages ? 0 : slot + 1;
@@ -631,18 +640,20 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
                 st.dump(n, reinterpret_cast<float*>(ring + held * C::kSlotBytes),
                         red_m + warp * 8, red_l + warp * 8, lane);
             __syncthreads();
-            const int rows = u.ok ? min(8, nrows - n * 8) : 0;
-            for (int i = threadIdx.x; i < rows * (kHeadDim / 4); i += kThreads) {
-                const int r = i / (kHeadDim / 4), c4 = i % (kHeadDim / 4);
+            const int rows = u.ok ? max(0, min(8, nrows - n * 8)) : 0;
+            const int per_head = rows * (kHeadDim / 4);
+            for (int i = threadIdx.x; i < per_head * qp.heads; i += kThreads) {
+                const int hd = i >= per_head ? 1 : 0;
+                const int r = (i - hd * per_head) / (kHeadDim / 4), c4 = i % (kHeadDim / 4);
+                // the states of the head's warps
+                const int w_begin = hd << in.wl2, w_end = w_begin + (1 << in.wl2);
                 float M = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w)
+                for (int w = w_begin; w < w_end; ++w)
                     if (dump_slot[w] >= 0) M = fmaxf(M, red_m[w * 8 + r]);
                 const float mu = M == -INFINITY ? 0.f : M;
                 float L = 0.f;
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
+                for (int w = w_begin; w < w_end; ++w) {
                     const int sl = dump_slot[w];
                     if (sl < 0) continue;
                     const float f = fast_exp2(red_m[w * 8 + r] - mu);
@@ -661,15 +672,18 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
                 o.z *= inv;
                 o.w *= inv;
                 const float lse2 = L != 0.f ? M - kPOffset + log2f(L) : -INFINITY;
+                const int row_in_unit = hd * G + n * 8 + r;
                 if (u.slot < 0) {
-                    const size_t row = row_base + n * 8 + r;
+                    const size_t row = row_base + row_in_unit;
                     uint2 v;
                     v.x = pack_bf16x2(o.x, o.y);
                     v.y = pack_bf16x2(o.z, o.w);
                     *reinterpret_cast<uint2*>(p.out + row * kHeadDim + c4 * 4) = v;
                     if (c4 == 0 && p.lse != nullptr) p.lse[row] = lse2 * kLn2;
                 } else {
-                    const size_t row = static_cast<size_t>(u.slot) * G + u.row0 + n * 8 + r;
+                    // partial states are [slot][heads * G][128]
+                    const size_t row = static_cast<size_t>(u.slot) * G * qp.heads + u.row0 +
+                                       row_in_unit;
                     *reinterpret_cast<float4*>(p.part_o + row * kHeadDim + c4 * 4) = o;
                     if (c4 == 0) p.part_lse[row] = lse2;
                 }
@@ -677,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
             __syncthreads();
         }
         if (held >= 0)
-            in.refill(qp, units, ring_addr + held * C::kSlotBytes, dst, sdst, warp, lane);
+            in.refill(qp, units, ring_addr + held * C::kSlotBytes, dst, sdst, lane);
     }
     cp_async_wait<0>();
 }

@@ -36,6 +36,7 @@ struct oxd_plan_s {
     int device;  // -1 for a host-only plan (desc.num_sms given)
     bool quant;  // for a 4-bit cache (oxd_quant_decode_run), else for bf16 pools
     int group;
+    int heads;   // KV heads a work unit covers (1; 2 for a 4-bit NHD cache)
     int variant;
     int n_items;
     int n_slots;
@@ -342,7 +343,12 @@ oxd_status plan_decode(const oxd_paged_decode_desc* desc, const int32_t* indptr,
     // prefix attend the prefix together (one prefill-kernel tile per chunk of
     // up to 128 / G consecutive such requests and KV head) and decode only
     // their pages after it.
-    const int H = d.num_kv_heads;
+    // Streams per request and query rows per stream: one KV head each, but in a
+    // 4-bit NHD cache, where a head's codes of a token are half a 128-byte line,
+    // two (for an even number of heads), so that whole lines are read at once.
+    const int heads = quant && d.layout == OXD_LAYOUT_NHD && d.num_kv_heads % 2 == 0 ? 2 : 1;
+    const int H = d.num_kv_heads / heads;
+    const int R = G * heads;
     const int prefix_pages = d.shared_prefix_tokens / ps;  // 0 without cascade
     std::vector<int> start_page(B, 0);
     struct Chunk {
@@ -384,7 +390,7 @@ oxd_status plan_decode(const oxd_paged_decode_desc* desc, const int32_t* indptr,
     // same pages). A piece is a run of consecutive pages of one stream; a
     // stream cut into several pieces is "split" and gets one partial-state
     // slot per piece.
-    const int pps = std::max(1, vs.stage_tokens / ps);  // pages per pipeline stage
+    const int pps = std::max(1, vs.stage_tokens / heads / ps);  // pages per pipeline stage
     // Groups of more than 16 query heads run every piece on a pair of CTAs,
     // one per 16-row half, side by side (the second read of each page is
     // then served by L2); the partition below is over CTA pairs.
@@ -607,12 +613,12 @@ oxd_status plan_decode(const oxd_paged_decode_desc* desc, const int32_t* indptr,
                       [&](int a, int x) { return pieces[a].p0 < pieces[x].p0; });
             if (casc_K > 0) {
                 const int blk = (h * B + b) * casc_K;
-                split_tab.push_back(make_int4(b * d.num_qo_heads + h * G, casc ? blk : blk + 1,
+                split_tab.push_back(make_int4(b * d.num_qo_heads + h * R, casc ? blk : blk + 1,
                                               static_cast<int>(v.size()) + (casc ? 1 : 0), 0));
                 int k = blk + 1;
                 for (int i : v) slot[i] = k++;
             } else {
-                split_tab.push_back(make_int4(b * d.num_qo_heads + h * G, n_slots,
+                split_tab.push_back(make_int4(b * d.num_qo_heads + h * R, n_slots,
                                               static_cast<int>(v.size()), 0));
                 for (int i : v) slot[i] = n_slots++;
             }
@@ -685,6 +691,7 @@ oxd_status plan_decode(const oxd_paged_decode_desc* desc, const int32_t* indptr,
     P->device = plan_device;
     P->quant = quant;
     P->group = G;
+    P->heads = heads;
     P->variant = variant;
     P->n_items = n_units;
     P->n_slots = n_slots;
@@ -713,8 +720,8 @@ oxd_status plan_decode(const oxd_paged_decode_desc* desc, const int32_t* indptr,
     P->meta_bytes = align_up(P->off_punits + sizeof(PrefillUnit) * punits.size(), 256);
     P->off_part_o = P->meta_bytes;
     P->off_part_lse =
-        align_up(P->off_part_o + static_cast<size_t>(n_slots) * G * kHeadDim * 4, 256);
-    P->ws_bytes = align_up(P->off_part_lse + static_cast<size_t>(n_slots) * G * 4, 256);
+        align_up(P->off_part_o + static_cast<size_t>(n_slots) * R * kHeadDim * 4, 256);
+    P->ws_bytes = align_up(P->off_part_lse + static_cast<size_t>(n_slots) * R * 4, 256);
 
     P->work = new (std::nothrow) WorkList();
     P->splits = new (std::nothrow) SplitList();
@@ -885,11 +892,12 @@ oxd_status merge_run(oxd_plan plan, const DecodeParams& p, uint8_t* ws, bool in_
     mp.ws_stamp = p.ws_stamp;
     mp.stamp = p.stamp;
     mp.n_rows = static_cast<int64_t>(d.batch) * d.num_qo_heads;
-    mp.n_states = static_cast<int64_t>(plan->n_slots) * plan->group;
+    const int rows = plan->group * plan->heads;
+    mp.n_states = static_cast<int64_t>(plan->n_slots) * rows;
     mp.uniform = 0;
     mp.n = plan->n_split;
     mp.S = 0;
-    mp.R = plan->group;
+    mp.R = rows;
     mp.D = kHeadDim;
     mp.s_to_ln = 0.693147180559945309f;  // partial LSEs are log2
     mp.max_count = plan->max_chunks + (plan->casc_units > 0 ? 1 : 0);
@@ -1126,6 +1134,7 @@ oxd_status oxd_quant_decode_run(oxd_plan plan, const void* q, const oxd_kv_pools
     if (up != OXD_OK) return up;
     QuantDecodeParams p{};
     p.d = decode_params(plan, ws, bound, q, indptr, indices, last_page_len, sm_scale, out, lse);
+    p.heads = plan->heads;
     p.k_codes = static_cast<const uint8_t*>(cache->k);
     p.v_codes = static_cast<const uint8_t*>(cache->v);
     p.k_scales = static_cast<const uint16_t*>(cache->k_scales);

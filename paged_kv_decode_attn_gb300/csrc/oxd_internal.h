@@ -197,6 +197,7 @@ struct QuantDecodeParams {
     const uint8_t* v_codes;
     const uint16_t* k_scales;    // f16 [num_pages][Hkv][page_size][4]
     const uint16_t* v_scales;
+    int32_t heads;               // KV heads a unit covers: its h counts such groups
 };
 VariantShape quant_shape(int variant);
 cudaError_t quant_occupancy(int variant, int* ctas_per_sm);
