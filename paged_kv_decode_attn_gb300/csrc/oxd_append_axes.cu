@@ -1,10 +1,25 @@
 // Rotary embedding with position axes + paged KV append for sm_103a, into
 // bf16 pages (oxd_rope_axes_append) or 4-bit pages (oxd_quant_rope_append).
 //
-// One warp per row: the K and V rows of a (token, KV head), or a query row.
-// Lane l owns columns 2l, 2l + 1 and 64 + 2l, 65 + 2l, the two rotary pairs
-// 2l and 2l + 1. Angles and rotation in double; the K row of a 4-bit cache is
-// the bf16 number nearest to the rotated value.
+//   angle of pair i = rope_positions[axis_i][t] * theta^(-2i/128)
+//   y_i = x_i cos - x_{i+64} sin,  y_{i+64} = x_{i+64} cos + x_i sin
+//
+// A call reads q, k and v once and writes q_out and the page rows once, so
+// bytes bound it (long calls) or the chain position -> page -> refcount (a
+// decode step). A block of eight warps takes one, two or four tokens. Its
+// threads form the tokens' 64 cosines and sines each, one pair a thread,
+// which all of a token's heads share (formed per row in double, they were
+// the whole cost); then each warp takes rows of one token, four at a time,
+// eight lanes a row: lane s of a row holds columns 8s .. 8s + 7 and 64 + 8s ..
+// (two 16-byte loads), so a rotation pairs values of one lane, a 4-bit group
+// of 32 is four lanes, and a row's 8 cosines stay in registers.
+//
+// Which code a K value of a 4-bit row gets is a comparison, so there the
+// rotated value is formed to about 2^-32 of the pair (cosines, sines and
+// products as sums of two floats) before it is rounded to bf16: the codes are
+// those of the exactly rotated row but for about one value in 10^9, where
+// float arithmetic would flip one in 10^6 and some groups' scales. Everything
+// else rotates in float.
 #include <cuda_bf16.h>
 
 #include "oxd_e2m1.cuh"
@@ -15,119 +30,314 @@ namespace oxd {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kRowsPerTask = 4;  // rows (heads) a warp takes at a time
+constexpr int kBatch = 2;        // tasks of query rows in flight a warp
+constexpr int kPairs = kHeadDim / 2;
 
-struct Row {
-    uint32_t lo, hi;  // columns (2l, 2l + 1) and (64 + 2l, 65 + 2l), bf16 pairs
+// a + b = s + e exactly.
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+    s = __fadd_rn(a, b);
+    const float t = __fadd_rn(s, -a);
+    e = __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -t)), __fadd_rn(b, -t));
+}
+
+// a * b = p + e exactly.
+__device__ __forceinline__ void two_prod(float a, float b, float& p, float& e) {
+    p = __fmul_rn(a, b);
+    e = fmaf(a, b, -p);
+}
+
+// cos and sin of pos * g turns, each as a sum of two floats good to about
+// 2^-32. g.x + g.y + g.z is the frequency in turns; pos < 2^24. The product is
+// kept exactly, whole quarter turns are taken off, and what is left, at most
+// an eighth of a turn, goes through the Taylor series with its leading terms
+// in two floats (the others are below 2^-11 of the result, so their float
+// roundings stay below 2^-32).
+__device__ __forceinline__ float4 cos_sin(int pos, float4 g) {
+    const float P = static_cast<float>(pos);
+    float h1, e1, h2, e2, s, a, b;
+    two_prod(P, g.x, h1, e1);
+    two_prod(P, g.y, h2, e2);
+    two_sum(h1 - rintf(h1), e1, s, a);
+    two_sum(s, h2, s, b);
+    float lo = (a + b) + (e2 + P * g.z);
+    two_sum(s, lo, s, lo);
+    const float quarter = rintf(4.f * s);
+    s = fmaf(-0.25f, quarter, s);  // exact
+    two_sum(s, lo, s, lo);
+    // z = 2 pi s
+    constexpr float kTwoPiHi = 6.2831854820251465f, kTwoPiLo = -1.7484556000744883e-7f;
+    float zh, zl;
+    two_prod(s, kTwoPiHi, zh, zl);
+    zl = fmaf(s, kTwoPiLo, fmaf(lo, kTwoPiHi, zl));
+    // u = z^2, q = u^2
+    float uh, ul, q, qe;
+    two_prod(zh, zh, uh, ul);
+    ul = fmaf(2.f * zh, zl, ul);
+    two_prod(uh, uh, q, qe);
+    qe = fmaf(2.f * uh, ul, qe);
+    // sin z = z (1 + t), t = -u/6 + u^2/120 - u^3/5040 + ...
+    constexpr float k6Hi = -1.f / 6.f, k6Lo = 4.967053731e-9f;       // -1/6 = Hi + Lo
+    constexpr float k120Hi = 1.f / 120.f, k120Lo = -4.346172015e-10f;     // 1/120
+    float m, me, n, ne, t, te, w, we;
+    two_prod(uh, k6Hi, m, me);
+    me = fmaf(uh, k6Lo, fmaf(ul, k6Hi, me));
+    two_prod(q, k120Hi, n, ne);
+    ne = fmaf(q, k120Lo, fmaf(qe, k120Hi, ne));
+    float v = fmaf(uh, -2.5052108e-8f, 2.7557319e-6f);  // -1/11!, 1/9!
+    v = q * uh * fmaf(uh, v, -1.9841270e-4f);             // -1/7!
+    two_sum(m, n, t, te);
+    te += me + (ne + v);
+    two_prod(zh, t, w, we);
+    we = fmaf(zh, te, fmaf(zl, t, we));
+    float sn, snl;
+    two_sum(zh, w, sn, snl);
+    snl += zl + we;
+    // cos z = 1 - u/2 + u^2/24 - u^3/720 + ...
+    constexpr float k24Hi = 1.f / 24.f, k24Lo = -1.241763433e-9f;    // 1/24
+    float y, ye;
+    two_prod(q, k24Hi, y, ye);
+    ye = fmaf(q, k24Lo, fmaf(qe, k24Hi, ye));
+    float r = fmaf(uh, 2.0876757e-9f, -2.7557319e-7f);  // 1/12!, -1/10!
+    r = fmaf(uh, r, 2.4801587e-5f);                       // 1/8!
+    r = q * uh * fmaf(uh, r, -1.3888889e-3f);             // -1/6!
+    float cs, csl, x, xe;
+    two_sum(1.f, -0.5f * uh, cs, csl);
+    two_sum(cs, y, x, xe);
+    csl += xe + (ye + r) - 0.5f * ul;
+    two_sum(x, csl, cs, csl);
+    two_sum(sn, snl, sn, snl);
+    const int k = static_cast<int>(quarter) & 3;  // sin, cos of z + k quarter turns
+    float4 o = (k & 1) ? make_float4(-sn, cs, -snl, csl) : make_float4(cs, sn, csl, snl);
+    if (k & 2) o = make_float4(-o.x, -o.y, -o.z, -o.w);
+    return o;  // cos, sin, their low parts
+}
+
+// A bf16 number from hi + lo (hi the nearest float): hi rounds the right way
+// by itself unless it lies exactly between two bf16 numbers.
+__device__ __forceinline__ float nudge_tie(float hi, float lo) {
+    uint32_t b = __float_as_uint(hi);
+    if ((b & 0xffffu) == 0x8000u && lo != 0.f) b += ((lo > 0.f) == (hi > 0.f)) ? 1u : ~0u;
+    return __uint_as_float(b);
+}
+
+// a c - b s (c, s with low parts cl, sl), rounded to bf16 once.
+__device__ __forceinline__ float exact_turn(float a, float c, float cl, float b, float s,
+                                            float sl) {
+    float p, pe, q, qe, d, de;
+    two_prod(a, c, p, pe);
+    two_prod(-b, s, q, qe);
+    two_sum(p, q, d, de);
+    const float rest = fmaf(a, cl, fmaf(-b, sl, (pe + qe) + de));
+    const float hi = __fadd_rn(d, rest);
+    return nudge_tie(hi, __fadd_rn(rest, -__fadd_rn(hi, -d)));
+}
+
+// The lane's 16 columns of a row: eight below 64 and their partners.
+struct Slice {
+    uint4 lo, hi;
 };
 
-__device__ __forceinline__ Row load_row(const uint16_t* src, int lane) {
-    return {*reinterpret_cast<const uint32_t*>(src + 2 * lane),
-            *reinterpret_cast<const uint32_t*>(src + 64 + 2 * lane)};
+__device__ __forceinline__ Slice load_slice(const uint16_t* row, int s) {
+    return {*reinterpret_cast<const uint4*>(row + 8 * s),
+            *reinterpret_cast<const uint4*>(row + 64 + 8 * s)};
+}
+__device__ __forceinline__ void store_slice(uint16_t* row, int s, const Slice& x) {
+    *reinterpret_cast<uint4*>(row + 8 * s) = x.lo;
+    *reinterpret_cast<uint4*>(row + 64 + 8 * s) = x.hi;
+}
+__device__ __forceinline__ float low_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// cs: the token's cosines and sines in shared memory, the lane's pair j at 8 j.
+template <bool kExact>
+__device__ __forceinline__ Slice rotate(const Slice& x, const float4* cs) {
+    const uint32_t* a = &x.lo.x;
+    const uint32_t* b = &x.hi.x;
+    Slice y;
+    uint32_t* ya = &y.lo.x;
+    uint32_t* yb = &y.hi.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a0 = low_f(a[i]), a1 = high_f(a[i]), b0 = low_f(b[i]), b1 = high_f(b[i]);
+        const float4 t0 = cs[8 * (2 * i)], t1 = cs[8 * (2 * i + 1)];
+        if constexpr (kExact) {
+            ya[i] = pack_bf16x2(exact_turn(a0, t0.x, t0.z, b0, t0.y, t0.w),
+                                exact_turn(a1, t1.x, t1.z, b1, t1.y, t1.w));
+            yb[i] = pack_bf16x2(exact_turn(b0, t0.x, t0.z, -a0, t0.y, t0.w),
+                                exact_turn(b1, t1.x, t1.z, -a1, t1.y, t1.w));
+        } else {
+            ya[i] = pack_bf16x2(a0 * t0.x - b0 * t0.y, a1 * t1.x - b1 * t1.y);
+            yb[i] = pack_bf16x2(b0 * t0.x + a0 * t0.y, b1 * t1.x + a1 * t1.y);
+        }
+    }
+    return y;
 }
 
-__device__ __forceinline__ Row rotate(Row x, const double (&c)[2], const double (&s)[2]) {
-    const float a0 = __uint_as_float(x.lo << 16), a1 = __uint_as_float(x.lo & 0xffff0000u);
-    const float b0 = __uint_as_float(x.hi << 16), b1 = __uint_as_float(x.hi & 0xffff0000u);
-    __nv_bfloat162 lo, hi;
-    lo.x = __double2bfloat16(a0 * c[0] - b0 * s[0]);
-    lo.y = __double2bfloat16(a1 * c[1] - b1 * s[1]);
-    hi.x = __double2bfloat16(b0 * c[0] + a0 * s[0]);
-    hi.y = __double2bfloat16(b1 * c[1] + a1 * s[1]);
-    return {*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi)};
-}
-
-__device__ __forceinline__ void store_row(uint16_t* dst, Row x, int lane) {
-    *reinterpret_cast<uint32_t*>(dst + 2 * lane) = x.lo;
-    *reinterpret_cast<uint32_t*>(dst + 64 + 2 * lane) = x.hi;
-}
-
-// Holds a row in 4 bits: columns below 64 are groups 0 (lanes 0..15) and 1
-// (lanes 16..31), the others groups 2 and 3.
-__device__ __forceinline__ void hold_row(uint8_t* codes, uint16_t* scales, Row x, int lane) {
-    const uint32_t w[2] = {x.lo, x.hi};
+// Holds a row in 4 bits. Lanes 0..3 (4..7) of a row have group 0 (1) in their
+// low and group 2 (3) in their high columns. Every lane of the warp calls it;
+// `live` lanes store.
+__device__ __forceinline__ void hold_slice(uint8_t* codes, uint16_t* scales, const Slice& x, int s,
+                                           bool live) {
+    const uint4 w[2] = {x.lo, x.hi};
+    uint32_t sc[2], code[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const float x0 = __uint_as_float(w[j] << 16), x1 = __uint_as_float(w[j] & 0xffff0000u);
-        float amax = fmaxf(fabsf(x0), fabsf(x1));
+        const uint32_t v[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+        float amax = 0.f;
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const uint16_t s = group_scale(amax);
-        codes[32 * j + lane] = static_cast<uint8_t>(code_pair(x0, x1, scale_inverse(s)));
-        if ((lane & 15) == 0) scales[2 * j + lane / 16] = s;
+        for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(low_f(v[i])), fabsf(high_f(v[i]))));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        sc[j] = group_scale(amax);
+        const float inv = scale_inverse(static_cast<uint16_t>(sc[j]));
+        code[j] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) code[j] |= code_pair(low_f(v[i]), high_f(v[i]), inv) << (8 * i);
+    }
+    const uint32_t far0 = __shfl_xor_sync(0xffffffffu, sc[0], 4);
+    const uint32_t far1 = __shfl_xor_sync(0xffffffffu, sc[1], 4);
+    if (live) {
+        *reinterpret_cast<uint32_t*>(codes + 4 * s) = code[0];
+        *reinterpret_cast<uint32_t*>(codes + 32 + 4 * s) = code[1];
+        if (s == 0)
+            *reinterpret_cast<uint2*>(scales) = make_uint2(sc[0] | (far0 << 16), sc[1] | (far1 << 16));
     }
 }
 
-template <bool k4>
-__global__ void __launch_bounds__(kWarps * 32) axes_append_kernel(const AxesAppendParams p) {
+// kTokens: tokens a block takes; its warps are divided among them.
+template <bool k4, int kTokens>
+__global__ void __launch_bounds__(kWarps * 32, k4 ? 3 : 4)
+    axes_append_kernel(const __grid_constant__ AxesAppendParams p) {
+    constexpr int kTokenWarps = kWarps / kTokens;
+    __shared__ float4 cs_all[kTokens][kPairs];
+    __shared__ int bad_rope[kTokens];
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.last_epoch = p.epoch;
-    const int lane = threadIdx.x & 31;
-    const long long gw = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int heads = p.Hkv + p.Hq;
-    if (gw >= static_cast<long long>(p.T) * heads) return;
-    const int t = static_cast<int>(gw / heads), h = static_cast<int>(gw % heads);
-    double c[2], s[2];
-    bool ok_rope = true;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int pos = p.rope_positions[static_cast<size_t>(p.pair_axis[2 * lane + j]) * p.T + t];
-        ok_rope = ok_rope && pos >= 0 && pos < (1 << 24);
-        const double turns = (pos & ((1 << 24) - 1)) * p.turns[2 * lane + j];
-        sincospi(2.0 * (turns - rint(turns)), &s[j], &c[j]);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = lane & 7, sub = lane >> 3;  // columns of the row, row of the task
+    const int local = warp / kTokenWarps, wi = warp % kTokenWarps;
+    const long long t_all = static_cast<long long>(blockIdx.x) * kTokens + local;
+    const bool have = t_all < p.T;
+    const int t = have ? static_cast<int>(t_all) : 0;
+    const int kv_tasks = (p.Hkv + kRowsPerTask - 1) / kRowsPerTask;
+    const int q_tasks = (p.Hq + kRowsPerTask - 1) / kRowsPerTask;
+
+    // The first rows and the page walk are under way while the angles are
+    // formed. KV tasks go to the token's first warps.
+    const bool kv_warp = have && wi < kv_tasks;
+    Slice k0, v0;
+    if (kv_warp && wi * kRowsPerTask + sub < p.Hkv) {
+        const size_t row = (static_cast<size_t>(t) * p.Hkv + wi * kRowsPerTask + sub) * kHeadDim;
+        k0 = load_slice(p.k + row, s);
+        v0 = load_slice(p.v + row, s);
     }
-    ok_rope = __all_sync(0xffffffffu, ok_rope);
-    if (h >= p.Hkv) {
-        const size_t row = (static_cast<size_t>(t) * p.Hq + h - p.Hkv) * kHeadDim;
-        store_row(p.q_out + row, rotate(load_row(p.q + row, lane), c, s), lane);
-        return;
+    int b = -1, pos = -1;
+    if (kv_warp) {
+        b = p.token_request[t];
+        pos = p.positions[t];
     }
-    const int b = p.token_request[t], pos = p.positions[t];
-    int code = 0, lo = 0, hi = 0;
+    if (threadIdx.x < kTokens) bad_rope[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTokens * kPairs; i += kWarps * 32) {
+        const long long ti = static_cast<long long>(blockIdx.x) * kTokens + i / kPairs;
+        if (ti < p.T) {
+            const float4 g = p.turns[i % kPairs];
+            const int rp = p.rope_positions[static_cast<size_t>(__float_as_int(g.w)) * p.T + ti];
+            if (rp < 0 || rp >= (1 << 24)) bad_rope[i / kPairs] = 1;
+            // pair 8 s + j at 8 j + s: the eight lanes of a row read a line
+            cs_all[i / kPairs][(i % 8) * 8 + i % kPairs / 8] = cos_sin(rp & ((1 << 24) - 1), g);
+        }
+    }
+    int code = 0;
     int64_t page = -1;
-    if (b >= 0 && b < p.B) {
-        lo = p.indptr[b];
-        hi = p.indptr[b + 1];
+    if (kv_warp) {
+        int lo = 0, hi = 0;
+        if (b >= 0 && b < p.B) {
+            lo = p.indptr[b];
+            hi = p.indptr[b + 1];
+        }
+        if (b < 0 || b >= p.B || lo < 0 || hi < lo || hi > p.num_indices || pos < 0 ||
+            pos >= (1 << 24) ||
+            static_cast<int64_t>(pos) >= static_cast<int64_t>(hi - lo) * p.page_size) {
+            code = kDeviceBadPosition;
+        } else {
+            page = p.indices[lo + pos / p.page_size];
+            if (page < 0 || page >= p.num_pages)
+                code = kDeviceBadPage;
+            else if (p.refcount[page] != 1)
+                code = kDeviceSharedPage;
+        }
     }
-    if (b < 0 || b >= p.B || lo < 0 || hi < lo || hi > p.num_indices || pos < 0 ||
-        pos >= (1 << 24) || !ok_rope ||
-        static_cast<int64_t>(pos) >= static_cast<int64_t>(hi - lo) * p.page_size) {
-        code = kDeviceBadPosition;
-    } else {
-        page = p.indices[lo + pos / p.page_size];
-        if (page < 0 || page >= p.num_pages)
-            code = kDeviceBadPage;
-        else if (p.refcount[page] != 1)
-            code = kDeviceSharedPage;
+    __syncthreads();
+    if (!have) return;
+    const float4* cs = cs_all[local] + s;
+
+    if (kv_warp) {
+        if (code == 0 && bad_rope[local]) code = kDeviceBadPosition;
+        if (code != 0 && wi == 0 && lane == 0) record_status(p.status, p.epoch, code);
+        const int slot = code == 0 ? pos % p.page_size : 0;
+        for (int task = wi; task < kv_tasks && code == 0; task += kTokenWarps) {
+            const int h = task * kRowsPerTask + sub;
+            const bool live = h < p.Hkv;
+            if (task != wi && live) {
+                const size_t row = (static_cast<size_t>(t) * p.Hkv + h) * kHeadDim;
+                k0 = load_slice(p.k + row, s);
+                v0 = load_slice(p.v + row, s);
+            }
+            if (!live) k0 = v0 = Slice{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            const Slice k = rotate<k4>(k0, cs);
+            const int hd = live ? h : 0;
+            const size_t dst = row_index(p.layout, page, slot, hd, p.Hkv, p.page_size);
+            if constexpr (k4) {
+                const size_t sc = scale_index(page, slot, hd, p.Hkv, p.page_size);
+                hold_slice(static_cast<uint8_t*>(p.k_pages) + dst * kCodeBytes, p.k_scales + sc, k,
+                           s, live);
+                hold_slice(static_cast<uint8_t*>(p.v_pages) + dst * kCodeBytes, p.v_scales + sc,
+                           v0, s, live);
+            } else if (live) {
+                store_slice(static_cast<uint16_t*>(p.k_pages) + dst * kHeadDim, s, k);
+                store_slice(static_cast<uint16_t*>(p.v_pages) + dst * kHeadDim, s, v0);
+            }
+        }
     }
-    if (code != 0) {
-        if (h == 0 && lane == 0) record_status(p.status, p.epoch, code);
-        return;
+    // Query rows, a batch of tasks' loads ahead of its stores (q_out may be q).
+    // The warps are taken from the last on, behind the KV warps.
+    for (int task = kTokenWarps - 1 - wi; task < q_tasks; task += kTokenWarps * kBatch) {
+        Slice x[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int h = (task + j * kTokenWarps) * kRowsPerTask + sub;
+            if (h < p.Hq)
+                x[j] = load_slice(p.q + (static_cast<size_t>(t) * p.Hq + h) * kHeadDim, s);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int h = (task + j * kTokenWarps) * kRowsPerTask + sub;
+            if (h < p.Hq)
+                store_slice(p.q_out + (static_cast<size_t>(t) * p.Hq + h) * kHeadDim, s,
+                            rotate<false>(x[j], cs));
+        }
     }
-    const size_t src = (static_cast<size_t>(t) * p.Hkv + h) * kHeadDim;
-    const Row k = rotate(load_row(p.k + src, lane), c, s), v = load_row(p.v + src, lane);
-    const int slot = pos % p.page_size;
-    const size_t dst = row_index(p.layout, page, slot, h, p.Hkv, p.page_size);
-    if constexpr (k4) {
-        const size_t sc = scale_index(page, slot, h, p.Hkv, p.page_size);
-        hold_row(static_cast<uint8_t*>(p.k_pages) + dst * kCodeBytes, p.k_scales + sc, k, lane);
-        hold_row(static_cast<uint8_t*>(p.v_pages) + dst * kCodeBytes, p.v_scales + sc, v, lane);
-    } else {
-        store_row(static_cast<uint16_t*>(p.k_pages) + dst * kHeadDim, k, lane);
-        store_row(static_cast<uint16_t*>(p.v_pages) + dst * kHeadDim, v, lane);
-    }
+}
+
+template <bool k4, int kTokens>
+cudaError_t launch(const AxesAppendParams& p, cudaStream_t stream) {
+    const long long blocks = (static_cast<long long>(p.T) + kTokens - 1) / kTokens;
+    axes_append_kernel<k4, kTokens>
+        <<<static_cast<unsigned>(blocks), kWarps * 32, 0, stream>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_axes_append(const AxesAppendParams& p, cudaStream_t stream) {
-    const long long warps = static_cast<long long>(p.T) * (p.Hkv + p.Hq);
-    const long long blocks = (warps + kWarps - 1) / kWarps;
-    if (p.T < 1 || blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (p.k_scales != nullptr)
-        axes_append_kernel<true><<<static_cast<unsigned>(blocks), kWarps * 32, 0, stream>>>(p);
-    else
-        axes_append_kernel<false><<<static_cast<unsigned>(blocks), kWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    if (p.T < 1) return cudaErrorInvalidConfiguration;
+    // Four tokens a block form their angles with every thread; a call of few
+    // tokens spreads each over a block of its own.
+    const bool k4 = p.k_scales != nullptr;
+    if (p.T <= 152 * 4) return k4 ? launch<true, 1>(p, stream) : launch<false, 1>(p, stream);
+    return k4 ? launch<true, 4>(p, stream) : launch<false, 4>(p, stream);
 }
 
 }  // namespace oxd

@@ -224,10 +224,11 @@ struct AxesAppendParams {
     unsigned long long* status;
     uint32_t* last_epoch;
     uint32_t epoch;
-    int32_t T, B, Hq, Hkv, page_size, layout, num_indices, num_axes;
+    int32_t T, B, Hq, Hkv, page_size, layout, num_indices;
     int64_t num_pages;
-    double turns[kHeadDim / 2];     // theta^(-2i/128) / (2 pi)
-    uint8_t pair_axis[kHeadDim / 2];
+    // Per pair: theta^(-2i/128) / (2 pi) as the sum of three floats, and its
+    // axis as the bits of an int.
+    float4 turns[kHeadDim / 2];
 };
 cudaError_t launch_axes_append(const AxesAppendParams& p, cudaStream_t stream);
 

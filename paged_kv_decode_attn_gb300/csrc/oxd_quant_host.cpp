@@ -130,11 +130,16 @@ oxd_status axes_append(const oxd_axes_append_desc* desc, const void* q, const vo
     p.page_size = d.page_size;
     p.layout = d.layout;
     p.num_indices = d.num_indices;
-    p.num_axes = rope_positions != nullptr ? d.num_axes : 1;
     p.num_pages = d.num_pages;
     for (int i = 0; i < kHeadDim / 2; ++i) {
-        p.pair_axis[i] = rope_positions != nullptr ? d.pair_axis[i] : 0;
-        p.turns[i] = std::pow(d.rope_theta, -2.0 * i / kHeadDim) / 6.283185307179586476925286766559;
+        const double g = std::pow(d.rope_theta, -2.0 * i / kHeadDim) /
+                         6.283185307179586476925286766559;
+        const int32_t axis = rope_positions != nullptr ? d.pair_axis[i] : 0;
+        float4& f = p.turns[i];
+        f.x = static_cast<float>(g);
+        f.y = static_cast<float>(g - f.x);
+        f.z = static_cast<float>(g - f.x - f.y);
+        std::memcpy(&f.w, &axis, sizeof(axis));
     }
     if (launch_axes_append(p, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return OXD_ERR_CUDA;
