@@ -2,7 +2,14 @@
 // between equal formats, held in 4 bits from bf16 rows, or written back as
 // bf16 from 4-bit rows (oxd_copy_pages).
 //
-// One warp per (pair, tensor, token, head) row.
+// Bytes bound it: every row is read once and written once. The work is cut
+// into slices of one (pair, tensor): 32 rows of 128 columns that eight warps
+// take four at a time, eight lanes a row (16 columns of a lane: 8s .. 8s + 7
+// and 64 + 8s ..), so every access is 16 bytes of bf16 or 4 bytes of codes and
+// a 4-bit group of 32 columns is four lanes. Rows are counted in the
+// destination's order, so its writes are contiguous; with equal layouts the
+// reads are too. Equal formats and layouts need no rows: a page is one run of
+// bytes, copied 16 bytes a lane.
 #include <cuda_bf16.h>
 
 #include "oxd_e2m1.cuh"
@@ -12,93 +19,226 @@
 namespace oxd {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 256;
 
-template <bool kSrc4, bool kDst4>
-__global__ void __launch_bounds__(kWarps * 32) copy_pages_kernel(const CopyPagesParams p) {
+// The pages of pair i, or false with the error (or the skipped pair) dealt with.
+__device__ __forceinline__ bool pair_pages(const CopyPagesParams& p, int i, bool first, int* src,
+                                           int* dst) {
+    const int s = p.src_pages[i], d = p.dst_pages[i];
+    *src = s;
+    *dst = d;
+    if (s == -1) return false;
+    int code = 0;
+    if (s < 0 || s >= p.src.num_pages || d < 0 || d >= p.dst.num_pages)
+        code = kDeviceBadPage;
+    else if (p.refcount != nullptr && p.refcount[d] != 1)
+        code = kDeviceSharedPage;
+    if (code != 0 && first && threadIdx.x == 0) record_status(p.status, p.epoch, code);
+    return code == 0;
+}
+
+// Equal formats and layouts: kPieces 16-byte pieces a thread.
+template <bool k4>
+__global__ void __launch_bounds__(kThreads) copy_pages_kernel(const CopyPagesParams p, int slices) {
+    constexpr int kPieces = 4;
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.last_epoch = p.epoch;
-    const int lane = threadIdx.x & 31;
-    const long long rows = static_cast<long long>(p.n) * 2 * p.page_size * p.H;
-    for (long long r = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); r < rows;
-         r += static_cast<long long>(gridDim.x) * kWarps) {
-        long long x = r;
-        const int h = static_cast<int>(x % p.H);
-        x /= p.H;
-        const int t = static_cast<int>(x % p.page_size);
-        x /= p.page_size;
-        const int tensor = static_cast<int>(x & 1);
-        const int i = static_cast<int>(x >> 1);
-        const int src = p.src_pages[i], dst = p.dst_pages[i];
-        if (src == -1) continue;
-        int code = 0;
-        if (src < 0 || src >= p.src.num_pages || dst < 0 || dst >= p.dst.num_pages)
-            code = kDeviceBadPage;
-        else if (p.refcount != nullptr && p.refcount[dst] != 1)
-            code = kDeviceSharedPage;
-        if (code != 0) {
-            if (lane == 0 && t == 0 && h == 0) record_status(p.status, p.epoch, code);
-            continue;
+    const int page_rows = p.page_size * p.H;
+    const int row_pieces = (k4 ? kCodeBytes : kHeadDim * 2) / 16;
+    const int data = page_rows * row_pieces;                     // pieces of a page's rows
+    const int all = data + (k4 ? page_rows * kScaleBytes / 16 : 0);  // and of its scales
+    const long long work = static_cast<long long>(p.n) * 2 * slices;
+    for (long long x = blockIdx.x; x < work; x += gridDim.x) {
+        const int slice = static_cast<int>(x % slices);
+        const int tensor = static_cast<int>(x / slices) & 1;
+        const int i = static_cast<int>(x / slices >> 1);
+        int src, dst;
+        if (!pair_pages(p, i, slice == 0 && tensor == 0, &src, &dst)) continue;
+        const uint4* from = reinterpret_cast<const uint4*>(p.src.data[tensor]) +
+                            static_cast<size_t>(src) * data;
+        uint4* to = reinterpret_cast<uint4*>(p.dst.data[tensor]) + static_cast<size_t>(dst) * data;
+        uint4 v[kPieces];
+        const int c0 = slice * kThreads * kPieces + threadIdx.x;
+        const uint4* from_s = nullptr;
+        uint4* to_s = nullptr;
+        if constexpr (k4) {
+            from_s = reinterpret_cast<const uint4*>(p.src.scales[tensor]) +
+                     static_cast<size_t>(src) * (all - data) - data;
+            to_s = reinterpret_cast<uint4*>(p.dst.scales[tensor]) +
+                   static_cast<size_t>(dst) * (all - data) - data;
         }
-        const size_t from = row_index(p.src.layout, src, t, h, p.H, p.page_size);
-        const size_t to = row_index(p.dst.layout, dst, t, h, p.H, p.page_size);
-        const size_t from_s = scale_index(src, t, h, p.H, p.page_size);
-        const size_t to_s = scale_index(dst, t, h, p.H, p.page_size);
-        if constexpr (kSrc4 && kDst4) {
-            reinterpret_cast<uint16_t*>(p.dst.data[tensor] + to * kCodeBytes)[lane] =
-                reinterpret_cast<const uint16_t*>(p.src.data[tensor] + from * kCodeBytes)[lane];
-            if (lane < kRowScales)
-                p.dst.scales[tensor][to_s + lane] = p.src.scales[tensor][from_s + lane];
-        } else {
-            // lane: columns [4 lane, 4 lane + 4), group lane / 8
-            uint2 v;
-            if constexpr (kSrc4) {
-                const uint32_t w = reinterpret_cast<const uint16_t*>(p.src.data[tensor] +
-                                                                     from * kCodeBytes)[lane];
-                const float s = __half2float(
-                    __ushort_as_half(p.src.scales[tensor][from_s + lane / 8]));
-                uint32_t c[4];
-                codes_to_f16(w, c);
-                const float2 a = f16x2_floats(c[0]), b = f16x2_floats(c[1]);
-                v.x = pack_bf16x2(a.x * s, a.y * s);
-                v.y = pack_bf16x2(b.x * s, b.y * s);
-            } else {
-                v = reinterpret_cast<const uint2*>(p.src.data[tensor] + from * kHeadDim * 2)[lane];
-            }
-            if constexpr (kDst4) {
-                const float x0 = __uint_as_float(v.x << 16), x1 = __uint_as_float(v.x & 0xffff0000u);
-                const float x2 = __uint_as_float(v.y << 16), x3 = __uint_as_float(v.y & 0xffff0000u);
-                float amax = fmaxf(fmaxf(fabsf(x0), fabsf(x1)), fmaxf(fabsf(x2), fabsf(x3)));
 #pragma unroll
-                for (int o = 1; o < 8; o <<= 1)
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                const uint16_t s = group_scale(amax);
-                const float inv = scale_inverse(s);
-                reinterpret_cast<uint16_t*>(p.dst.data[tensor] + to * kCodeBytes)[lane] =
-                    static_cast<uint16_t>(code_pair(x0, x1, inv) | (code_pair(x2, x3, inv) << 8));
-                if ((lane & 7) == 0) p.dst.scales[tensor][to_s + lane / 8] = s;
-            } else {
-                reinterpret_cast<uint2*>(p.dst.data[tensor] + to * kHeadDim * 2)[lane] = v;
+        for (int j = 0; j < kPieces; ++j) {
+            const int c = c0 + j * kThreads;
+            if (c < all) v[j] = k4 && c >= data ? from_s[c] : from[c];
+        }
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            const int c = c0 + j * kThreads;
+            if (c < all) {
+                if (k4 && c >= data)
+                    to_s[c] = v[j];
+                else
+                    to[c] = v[j];
             }
         }
     }
 }
 
+__device__ __forceinline__ float low_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// What a lane holds of a row: as bf16 pairs, or as codes and the scales of its
+// two groups.
+template <bool k4>
+struct Piece;
+template <>
+struct Piece<false> {
+    uint4 lo, hi;
+    __device__ __forceinline__ void load(const PagePools& c, int tensor, size_t row, size_t, int s) {
+        const uint4* r = reinterpret_cast<const uint4*>(c.data[tensor] + row * kHeadDim * 2);
+        lo = r[s];
+        hi = r[8 + s];
+    }
+    __device__ __forceinline__ void store(const PagePools& c, int tensor, size_t row, size_t, int s,
+                                          bool live) const {
+        uint4* r = reinterpret_cast<uint4*>(c.data[tensor] + row * kHeadDim * 2);
+        if (live) {
+            r[s] = lo;
+            r[8 + s] = hi;
+        }
+    }
+};
+template <>
+struct Piece<true> {
+    uint32_t lo, hi;      // codes of columns 8s .. 8s + 7 and 64 + 8s ..
+    uint32_t s_lo, s_hi;  // f16 scales of the groups they lie in
+    __device__ __forceinline__ void load(const PagePools& c, int tensor, size_t row, size_t sc,
+                                         int s) {
+        const uint32_t* r = reinterpret_cast<const uint32_t*>(c.data[tensor] + row * kCodeBytes);
+        lo = r[s];
+        hi = r[8 + s];
+        s_lo = c.scales[tensor][sc + s / 4];
+        s_hi = c.scales[tensor][sc + 2 + s / 4];
+    }
+    // Every lane of the warp calls it; `live` lanes store.
+    __device__ __forceinline__ void store(const PagePools& c, int tensor, size_t row, size_t sc,
+                                          int s, bool live) const {
+        const uint32_t a = __shfl_xor_sync(0xffffffffu, s_lo, 4);
+        const uint32_t b = __shfl_xor_sync(0xffffffffu, s_hi, 4);
+        if (live) {
+            uint32_t* r = reinterpret_cast<uint32_t*>(c.data[tensor] + row * kCodeBytes);
+            r[s] = lo;
+            r[8 + s] = hi;
+            if (s == 0)
+                *reinterpret_cast<uint2*>(c.scales[tensor] + sc) =
+                    make_uint2(s_lo | (a << 16), s_hi | (b << 16));
+        }
+    }
+};
+
+// Eight bf16 values in 4 bits, and their group's scale; the group's other
+// values are in the lanes next to this one.
+__device__ __forceinline__ void hold(const uint4& x, uint32_t& code, uint32_t& scale) {
+    const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(low_f(v[i])), fabsf(high_f(v[i]))));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    scale = group_scale(amax);
+    const float inv = scale_inverse(static_cast<uint16_t>(scale));
+    code = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) code |= code_pair(low_f(v[i]), high_f(v[i]), inv) << (8 * i);
+}
+
+__device__ __forceinline__ uint4 unhold(uint32_t code, uint32_t scale) {
+    const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(scale)));
+    uint32_t h[4], o[4];
+    codes_to_f16(code, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = f16x2_floats(h[i]);
+        o[i] = pack_bf16x2(f.x * s, f.y * s);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__device__ __forceinline__ void convert(const Piece<false>& a, Piece<false>& b) { b = a; }
+__device__ __forceinline__ void convert(const Piece<true>& a, Piece<true>& b) { b = a; }
+__device__ __forceinline__ void convert(const Piece<false>& a, Piece<true>& b) {
+    hold(a.lo, b.lo, b.s_lo);
+    hold(a.hi, b.hi, b.s_hi);
+}
+__device__ __forceinline__ void convert(const Piece<true>& a, Piece<false>& b) {
+    b.lo = unhold(a.lo, a.s_lo);
+    b.hi = unhold(a.hi, a.s_hi);
+}
+
+// Other formats or layouts: kRows rows a thread's eight lanes take.
+template <bool kSrc4, bool kDst4>
+__global__ void __launch_bounds__(kThreads) convert_pages_kernel(const CopyPagesParams p,
+                                                                 int slices) {
+    constexpr int kRows = 2;
+    constexpr int kSliceRows = kThreads / 8 * kRows;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.last_epoch = p.epoch;
+    const int s = threadIdx.x & 7;
+    const int page_rows = p.page_size * p.H;
+    const long long work = static_cast<long long>(p.n) * 2 * slices;
+    for (long long x = blockIdx.x; x < work; x += gridDim.x) {
+        const int slice = static_cast<int>(x % slices);
+        const int tensor = static_cast<int>(x / slices) & 1;
+        const int i = static_cast<int>(x / slices >> 1);
+        int src, dst;
+        if (!pair_pages(p, i, slice == 0 && tensor == 0, &src, &dst)) continue;
+        Piece<kSrc4> a[kRows];
+        size_t to[kRows], to_s[kRows];
+        bool live[kRows];
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+            const int r = slice * kSliceRows + j * (kThreads / 8) + (threadIdx.x >> 3);
+            live[j] = r < page_rows;
+            const int rr = live[j] ? r : 0;
+            const int t = p.dst.layout == 0 ? rr / p.H : rr % p.page_size;
+            const int h = p.dst.layout == 0 ? rr % p.H : rr / p.page_size;
+            a[j].load(p.src, tensor, row_index(p.src.layout, src, t, h, p.H, p.page_size),
+                      scale_index(src, t, h, p.H, p.page_size), s);
+            to[j] = row_index(p.dst.layout, dst, t, h, p.H, p.page_size);
+            to_s[j] = scale_index(dst, t, h, p.H, p.page_size);
+        }
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+            Piece<kDst4> b;
+            convert(a[j], b);
+            b.store(p.dst, tensor, to[j], to_s[j], s, live[j]);
+        }
+    }
+}
+
+template <class F>
+cudaError_t launch(F kernel, const CopyPagesParams& p, int slices, cudaStream_t stream) {
+    const long long work = static_cast<long long>(p.n) * 2 * slices;
+    const unsigned grid = static_cast<unsigned>(work < 1 ? 1 : work > (1 << 20) ? (1 << 20) : work);
+    kernel<<<grid, kThreads, 0, stream>>>(p, slices);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_copy_pages(const CopyPagesParams& p, cudaStream_t stream) {
-    const long long rows = static_cast<long long>(p.n) * 2 * p.page_size * p.H;
-    const long long blocks = (rows + kWarps - 1) / kWarps;
-    const unsigned grid = static_cast<unsigned>(blocks < 1 ? 1 : blocks > 152 * 8 ? 152 * 8 : blocks);
     const bool s4 = p.src.scales[0] != nullptr, d4 = p.dst.scales[0] != nullptr;
-    if (s4 && d4)
-        copy_pages_kernel<true, true><<<grid, kWarps * 32, 0, stream>>>(p);
-    else if (s4)
-        copy_pages_kernel<true, false><<<grid, kWarps * 32, 0, stream>>>(p);
-    else if (d4)
-        copy_pages_kernel<false, true><<<grid, kWarps * 32, 0, stream>>>(p);
-    else
-        copy_pages_kernel<false, false><<<grid, kWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    const long long rows = static_cast<long long>(p.page_size) * p.H;
+    if (s4 == d4 && p.src.layout == p.dst.layout) {
+        const long long pieces = rows * (s4 ? kCodeBytes + kScaleBytes : kHeadDim * 2) / 16;
+        const int slices = static_cast<int>((pieces + kThreads * 4 - 1) / (kThreads * 4));
+        return s4 ? launch(copy_pages_kernel<true>, p, slices, stream)
+                  : launch(copy_pages_kernel<false>, p, slices, stream);
+    }
+    const int slices = static_cast<int>((rows + kThreads / 4 - 1) / (kThreads / 4));
+    if (s4 && d4) return launch(convert_pages_kernel<true, true>, p, slices, stream);
+    if (s4) return launch(convert_pages_kernel<true, false>, p, slices, stream);
+    if (d4) return launch(convert_pages_kernel<false, true>, p, slices, stream);
+    return launch(convert_pages_kernel<false, false>, p, slices, stream);
 }
 
 }  // namespace oxd
