@@ -279,6 +279,8 @@ def make_rope_append_desc(num_tokens, batch, num_qo_heads, num_kv_heads, page_si
 def lib():
     """The loaded liboxd.so with its signatures declared."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -336,25 +338,36 @@ def lib():
 # ------------------------------------------------------------------ marshalling helpers
 
 def _addr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
+    except AttributeError:
+        pass
+    if x is None or isinstance(x, int):
+        return x
     if isinstance(x, np.ndarray):
         return x.ctypes.data
     raise TypeError(f"cannot take the address of {type(x).__name__}")
 
 
+_current_stream = None  # device index -> torch's current stream there, as an integer
+
+
+def _torch_stream(device):
+    """torch's current stream on a device, without making a Stream object where torch offers
+    that (a call's marshalling is most of the host time of a small launch)."""
+    global _current_stream
+    if _current_stream is None:
+        import torch
+
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _current_stream = raw or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _current_stream(device)
+
+
 def _stream(stream, like=None):
     if stream is None:
-        try:
-            import torch
-        except ImportError:
-            return None
-        if like is not None and hasattr(like, "device") and like.device.type == "cuda":
-            return torch.cuda.current_stream(like.device).cuda_stream
+        if like is not None and getattr(like, "is_cuda", False):
+            return _torch_stream(like.get_device())
         return None
     if isinstance(stream, int):
         return stream
@@ -449,7 +462,7 @@ def oxd_paged_decode_run(plan, q, k_pages, v_pages, indptr, indices, last_page_l
                          out, lse, workspace, workspace_bytes=None, stream=None) -> None:
     """Enqueue one decode step (see ``oxd_paged_decode_run`` in include/oxd.h)."""
     if workspace_bytes is None:
-        workspace_bytes = workspace.numel() * workspace.element_size()
+        workspace_bytes = workspace.nbytes
     st = lib().oxd_paged_decode_run(
         _handle(plan), _addr(q), _addr(k_pages), _addr(v_pages), _addr(indptr), _addr(indices),
         _addr(last_page_len), float(sm_scale), _addr(out), _addr(lse), _addr(workspace),
@@ -462,7 +475,7 @@ def oxd_plan_bind_workspace(plan, workspace, workspace_bytes=None, stream=None) 
     the plan on that workspace copy nothing and launch with small parameter
     blocks (see ``oxd_plan_bind_workspace`` in include/oxd.h)."""
     if workspace_bytes is None:
-        workspace_bytes = workspace.numel() * workspace.element_size()
+        workspace_bytes = workspace.nbytes
     st = lib().oxd_plan_bind_workspace(_handle(plan), _addr(workspace), int(workspace_bytes),
                                        _stream(stream, workspace))
     _check("oxd_plan_bind_workspace", st)
@@ -548,7 +561,7 @@ def oxd_rope_append(desc: RopeAppendDesc, q, k, v, token_request, positions, ind
     """Enqueue a fused rotary embedding + paged KV append (see ``oxd_rope_append``
     in include/oxd.h)."""
     if workspace_bytes is None:
-        workspace_bytes = workspace.numel() * workspace.element_size()
+        workspace_bytes = workspace.nbytes
     st = lib().oxd_rope_append(ctypes.byref(desc), _addr(q), _addr(k), _addr(v),
                                _addr(token_request), _addr(positions), _addr(indptr),
                                _addr(indices), _addr(page_refcount), _addr(q_out),
@@ -609,7 +622,7 @@ def oxd_paged_prefill_run(plan, q, k_pages, v_pages, qo_indptr, indptr, indices,
                           stream=None) -> None:
     """Enqueue one causal prefill (see ``oxd_paged_prefill_run`` in include/oxd.h)."""
     if workspace_bytes is None:
-        workspace_bytes = workspace.numel() * workspace.element_size()
+        workspace_bytes = workspace.nbytes
     st = lib().oxd_paged_prefill_run(
         _handle(plan), _addr(q), _addr(k_pages), _addr(v_pages), _addr(qo_indptr),
         _addr(indptr), _addr(indices), _addr(last_page_len), float(sm_scale), _addr(out),
@@ -620,7 +633,7 @@ def oxd_paged_prefill_run(plan, q, k_pages, v_pages, qo_indptr, indptr, indices,
 def oxd_prefill_plan_bind_workspace(plan, workspace, workspace_bytes=None, stream=None) -> None:
     """Enqueue the copy of the prefill plan's work list into ``workspace``."""
     if workspace_bytes is None:
-        workspace_bytes = workspace.numel() * workspace.element_size()
+        workspace_bytes = workspace.nbytes
     st = lib().oxd_prefill_plan_bind_workspace(_handle(plan), _addr(workspace),
                                                int(workspace_bytes), _stream(stream, workspace))
     _check("oxd_prefill_plan_bind_workspace", st)
@@ -653,7 +666,7 @@ def oxd_quant_decode_run(plan, q, cache: KvPools, indptr, indices, last_page_len
     """Enqueue one decode step over a 4-bit cache (see ``oxd_quant_decode_run`` in
     include/oxd.h)."""
     if workspace_bytes is None:
-        workspace_bytes = workspace.numel() * workspace.element_size()
+        workspace_bytes = workspace.nbytes
     st = lib().oxd_quant_decode_run(
         _handle(plan), _addr(q), ctypes.byref(cache.struct), _addr(indptr), _addr(indices),
         _addr(last_page_len), float(sm_scale), _addr(out), _addr(lse), _addr(workspace),
@@ -667,7 +680,7 @@ def oxd_rope_axes_append(desc: AxesAppendDesc, q, k, v, token_request, positions
     """Enqueue a rotary embedding with position axes + paged KV append (see
     ``oxd_rope_axes_append`` in include/oxd.h)."""
     if workspace_bytes is None:
-        workspace_bytes = workspace.numel() * workspace.element_size()
+        workspace_bytes = workspace.nbytes
     st = lib().oxd_rope_axes_append(
         ctypes.byref(desc), _addr(q), _addr(k), _addr(v), _addr(token_request), _addr(positions),
         _addr(rope_positions), _addr(indptr), _addr(indices), _addr(page_refcount), _addr(q_out),
@@ -681,7 +694,7 @@ def oxd_quant_rope_append(desc: AxesAppendDesc, q, k, v, token_request, position
     """Enqueue a rotary embedding + append into a 4-bit cache (see
     ``oxd_quant_rope_append`` in include/oxd.h)."""
     if workspace_bytes is None:
-        workspace_bytes = workspace.numel() * workspace.element_size()
+        workspace_bytes = workspace.nbytes
     st = lib().oxd_quant_rope_append(
         ctypes.byref(desc), _addr(q), _addr(k), _addr(v), _addr(token_request), _addr(positions),
         _addr(rope_positions), _addr(indptr), _addr(indices), _addr(page_refcount), _addr(q_out),
@@ -693,7 +706,7 @@ def oxd_copy_pages(desc: CopyPagesDesc, src: KvPools, dst: KvPools, src_pages, d
                    dst_refcount, workspace, workspace_bytes=None, stream=None) -> None:
     """Enqueue page copies between caches (see ``oxd_copy_pages`` in include/oxd.h)."""
     if workspace_bytes is None:
-        workspace_bytes = workspace.numel() * workspace.element_size()
+        workspace_bytes = workspace.nbytes
     st = lib().oxd_copy_pages(
         ctypes.byref(desc), ctypes.byref(src.struct), ctypes.byref(dst.struct), _addr(src_pages),
         _addr(dst_pages), _addr(dst_refcount), _addr(workspace), int(workspace_bytes),

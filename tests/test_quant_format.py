@@ -52,7 +52,7 @@ def test_decode_of_one_token_is_its_value_row():
     rng = np.random.default_rng(2)
     k, v = rng.normal(size=(2, 8, 2, 128)), rng.normal(size=(2, 8, 2, 128))
     q = rng.normal(size=(1, 4, 128))
-    out, lse, _, _ = R.decode(q, k, v, [0, 1], np.array([1]), [1], "NHD", 0.1)
+    out, lse, _, _, _ = R.decode(q, k, v, [0, 1], np.array([1]), [1], "NHD", 0.1)
     np.testing.assert_allclose(out[0], np.repeat(v[1, 0], 2, 0))
     np.testing.assert_allclose(lse[0, :2], q[0, :2] @ k[1, 0, 0] * 0.1)
 
