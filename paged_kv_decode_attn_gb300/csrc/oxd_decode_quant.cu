@@ -27,7 +27,7 @@
 //     the largest weight.
 // A unit's warp states are merged through the chunks the warps last read;
 // split streams leave F32 partial states for the merge kernel, as in the bf16
-// decode. The only waits are for a warp's own loads and the CTA's barriers.
+// decode.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -45,6 +45,8 @@ constexpr float kPOffset = 10.f; // log2 of the weight a score at the running ma
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+
+constexpr int kListed = 32;  // of a CTA's units, the ones held decoded in shared memory
 
 // kNT: 8-head tiles a warp holds. kCtas: resident CTAs a SM, which caps the
 // registers at 65536 / (kThreads * kCtas). kPs: page size.
@@ -64,12 +66,22 @@ struct QCfg {
     static constexpr int kVsOff = kKsOff + kQuantChunk * kScaleBytes;
     static constexpr int kSlotBytes = kVsOff + kQuantChunk * kScaleBytes;
     static_assert(8 * kHeadDim * 4 <= kSlotBytes, "a dumped 8-row state fits a slot");
-    static constexpr int kRedOff = kWarps * kStages * kSlotBytes;
-    static constexpr int kFlagOff = kRedOff + 2 * kWarps * 8 * 4;
-    static constexpr int kSmemBytes = kFlagOff + 32;  // dump slot of each warp, unit range
+    // query fragments of up to two heads: [head][group c][tile][lane] 16 bytes,
+    // and the next unit's query rows as they come from memory
+    static constexpr int kQOff = kWarps * kStages * kSlotBytes;
+    static constexpr int kQHeadBytes = kRows * kHeadDim * 2;
+    static constexpr int kRawOff = kQOff + 2 * kQHeadBytes;
+    static constexpr int kBarOff = kRawOff + 2 * kQHeadBytes;      // their mbarrier
+    static constexpr int kScOff = kBarOff + 16;                    // logit scales [head][kRows]
+    static constexpr int kRedOff = kScOff + 2 * kRows * 4;
+    static constexpr int kFlagOff = kRedOff + 2 * kWarps * 8 * 4;  // dump offset of each warp, units
+    static constexpr int kListOff = kFlagOff + 32;
+    static constexpr int kSmemBytes = kListOff + kListed * 32;
+    static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "the CTAs fit a SM");
 };
-template <int kPs> using CfgQ8 = QCfg<1, 3, 4, kPs>;
-template <int kPs> using CfgQ16 = QCfg<2, 4, 3, kPs>;
+template <int kPs> using CfgQ8 = QCfg<1, 2, 4, kPs>;
+template <int kPs> using CfgQ16 = QCfg<2, 3, 3, kPs>;
+template <int kPs> using CfgQ32 = QCfg<4, 4, 2, kPs>;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -86,6 +98,14 @@ __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
 }
 
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
@@ -141,15 +161,15 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 // different banks.
 __device__ __forceinline__ int row_token(int r) { return r ^ ((r >> 1) & 1); }
 
-// A work unit, checked against the plan.
+// A work unit, checked against the plan: no chunks if it is not one of it.
 struct Unit {
-    int first;    // offset of its first page in `indices`
+    int first;     // offset of its first page in `indices`
     int n_pages;
-    int b, h, row0, slot;
-    int valid;    // tokens
+    int valid;     // tokens
     int n_chunks;
-    bool ok;
+    int b, h, slot, reserved;
 };
+static_assert(sizeof(Unit) == 32, "two 16-byte loads");
 
 __device__ __forceinline__ Unit decode_unit(const QuantDecodeParams& qp, const int4 it) {
     const DecodeParams& p = qp.d;
@@ -158,23 +178,43 @@ __device__ __forceinline__ Unit decode_unit(const QuantDecodeParams& qp, const i
     u.n_pages = it.y & ((1 << kUnitPagesBits) - 1);
     const int last_len = (it.y >> kUnitPagesBits) & 0x7f;  // 0: not the request's last page
     u.b = it.z & ((1 << kUnitBBits) - 1);
-    u.row0 = ((it.z >> kUnitBBits) & 1) * 16;
     u.h = static_cast<int>(static_cast<uint32_t>(it.z) >> (kUnitBBits + 1)) * qp.heads;
     u.slot = it.w;
-    u.ok = u.n_pages >= 1 && it.x >= 0 && static_cast<int64_t>(it.x) + u.n_pages <= p.nnz &&
-           u.b < p.batch && u.h + qp.heads <= p.num_kv_heads && u.row0 < p.group && it.w >= -1 &&
-           it.w < p.n_slots && last_len <= p.page_size;
+    u.reserved = 0;
+    const bool ok = u.n_pages >= 1 && it.x >= 0 &&
+                    static_cast<int64_t>(it.x) + u.n_pages <= p.nnz && u.b < p.batch &&
+                    u.h + qp.heads <= p.num_kv_heads && it.w >= -1 && it.w < p.n_slots &&
+                    last_len <= p.page_size;
     u.valid = last_len ? (u.n_pages - 1) * p.page_size + last_len : u.n_pages * p.page_size;
-    u.n_chunks = u.ok ? (u.valid + kQuantChunk - 1) / kQuantChunk : 0;
+    u.n_chunks = ok ? (u.valid + kQuantChunk - 1) / kQuantChunk : 0;
     return u;
 }
+
+// Whether the device's block tables say what the unit's plan was made from.
+__device__ __forceinline__ bool tables_match(const DecodeParams& p, const Unit& u, const int4 it) {
+    const int last_len = (it.y >> kUnitPagesBits) & 0x7f;
+    return u.n_chunks > 0 && (it.y >= 0 || p.indptr[u.b] == u.first) &&
+           (last_len == 0 || (p.indptr[u.b + 1] == u.first + u.n_pages &&
+                              p.last_page_len[u.b] == last_len));
+}
+
+// A CTA's units: the first kListed decoded in shared memory, others from the list.
+struct UnitList {
+    const Unit* shared;
+    const int4* list;
+    int first;
+    __device__ __forceinline__ Unit get(const QuantDecodeParams& qp, int i) const {
+        if (i - first < kListed) return shared[i - first];
+        return decode_unit(qp, __ldg(list + i));
+    }
+};
 
 // One warp's stream of chunks: the refilling side, up to kStages chunks ahead
 // of the consuming one. The warp takes every fourth chunk of a unit (every
 // second one where a unit covers two heads). The page
 // indices of a run of its chunks sit in the lanes (`win`, the next run in
-// `ahead`), and the next unit's entry and first indices are read while the
-// current unit's chunks are still being issued.
+// `ahead`), and the next unit's first indices are read while the current
+// unit's chunks are still being issued.
 template <class C>
 struct Stream {
     int wl2;                     // log2 of the warps that share a head
@@ -183,9 +223,7 @@ struct Stream {
     int n_pages, n_chunks, first;
     int c;                       // this warp's next chunk of it
     int win_c, win, ahead;       // indices of the chunks from win_c on, and of the next run
-    int4 nx_it;
-    int nx_win;
-    bool nx_have;                // nx_win holds unit + 1's first indices
+    int nx_win;                  // unit + 1's first indices
     // this lane's addresses in page 0 of the unit's head: the 16-byte piece
     // lane % 4 of token lane / 4 of K and V, and the scales of tokens
     // 2 (lane % 16), + 1 of K (lanes 0..15) or V
@@ -193,10 +231,11 @@ struct Stream {
     const uint8_t* v;
     const uint8_t* sc;
 
-    __device__ __forceinline__ int load_window(const int32_t* indices, int c0, int lane) const {
+    __device__ __forceinline__ int load_window(const int32_t* indices, int x_first, int x_chunks,
+                                               int x_pages, int c0, int lane) const {
         const int cc = c0 + ((lane / C::kPagesPerChunk) << wl2);
         const int pg = cc * kQuantChunk / C::kPs + lane % C::kPagesPerChunk;
-        return cc < n_chunks && pg < n_pages ? __ldg(indices + first + pg) : 0;
+        return cc < x_chunks && pg < x_pages ? __ldg(indices + x_first + pg) : 0;
     }
     // An index outside the pool is recorded and replaced by page 0.
     __device__ __forceinline__ int check(const DecodeParams& p, int i, int lane) const {
@@ -205,53 +244,49 @@ struct Stream {
             record_status(p.status, p.epoch, kDeviceBadPage);
         return bad ? 0 : i;
     }
-    __device__ __forceinline__ void enter(const QuantDecodeParams& qp, const int4* units,
-                                          const int4 it, bool have_win, int lane) {
+    // Enters `unit`, whose first indices are in nx_win.
+    __device__ __forceinline__ void enter(const QuantDecodeParams& qp, const UnitList& units,
+                                          int lane) {
         const DecodeParams& p = qp.d;
-        const Unit u = decode_unit(qp, it);
+        const Unit u = units.get(qp, unit);
         n_pages = u.n_pages;
         n_chunks = u.n_chunks;
         first = u.first;
         c = win_c = w;
-        const int h = u.ok ? u.h + head : 0;
+        const int h = u.n_chunks > 0 ? u.h + head : 0;
         const size_t row = row_index(p.layout, 0, (lane >> 2) % C::kPs, h, p.num_kv_heads, C::kPs);
         k = qp.k_codes + row * kCodeBytes + (lane & 3) * 16;
         v = qp.v_codes + row * kCodeBytes + (lane & 3) * 16;
         const int st = 2 * (lane & 15) % C::kPs;
         sc = reinterpret_cast<const uint8_t*>((lane < 16 ? qp.k_scales : qp.v_scales) +
                                               scale_index(0, st, h, p.num_kv_heads, C::kPs));
-        win = check(p, have_win ? nx_win : load_window(p.indices, w, lane), lane);
-        ahead = load_window(p.indices, w + (C::kRun << wl2), lane);
-        if (unit + 1 < u_end) nx_it = __ldg(units + unit + 1);
-        nx_have = false;
+        win = check(p, nx_win, lane);
+        ahead = load_window(p.indices, first, n_chunks, n_pages, w + (C::kRun << wl2), lane);
+        load_next_window(qp, units, lane);
     }
-    __device__ __forceinline__ void load_next_window(const QuantDecodeParams& qp, int lane) {
-        nx_win = 0;
+    __device__ __forceinline__ void load_next_window(const QuantDecodeParams& qp,
+                                                     const UnitList& units, int lane) {
         if (unit + 1 < u_end) {
-            const Unit x = decode_unit(qp, nx_it);
-            const int cc = w + ((lane / C::kPagesPerChunk) << wl2);
-            const int pg = cc * kQuantChunk / C::kPs + lane % C::kPagesPerChunk;
-            if (cc < x.n_chunks && pg < x.n_pages) nx_win = __ldg(qp.d.indices + x.first + pg);
+            const Unit x = units.get(qp, unit + 1);
+            nx_win = load_window(qp.d.indices, x.first, x.n_chunks, x.n_pages, w, lane);
         }
-        nx_have = true;
     }
     // Issues the next chunk's copies into `slot`, if there is one; always one
     // more copy group. `slot` is the shared address, dst / sdst this lane's
     // offsets in it. Pages past the unit's last are read as page 0.
-    __device__ __forceinline__ void refill(const QuantDecodeParams& qp, const int4* units,
+    __device__ __forceinline__ void refill(const QuantDecodeParams& qp, const UnitList& units,
                                            uint32_t slot, uint32_t dst, uint32_t sdst,
                                            int lane) {
         const DecodeParams& p = qp.d;
         while (unit < u_end && c >= n_chunks) {
-            if (!nx_have) load_next_window(qp, lane);
             ++unit;
-            if (unit < u_end) enter(qp, units, nx_it, true, lane);
+            if (unit < u_end) enter(qp, units, lane);
         }
         if (unit < u_end) {
             if (c - win_c >= C::kRun << wl2) {
                 win = check(p, ahead, lane);
                 win_c += C::kRun << wl2;
-                ahead = load_window(p.indices, win_c + (C::kRun << wl2), lane);
+                ahead = load_window(p.indices, first, n_chunks, n_pages, win_c + (C::kRun << wl2), lane);
             }
             const int w0 = ((c - win_c) >> wl2) * C::kPagesPerChunk;
             // bytes of one token and of a page
@@ -271,7 +306,6 @@ struct Stream {
             cp_async16(slot + sdst, sc + static_cast<size_t>(page) * (page_bytes / 8) +
                                         half * kScaleBytes);
             c += 1 << wl2;
-            if (!nx_have) load_next_window(qp, lane);
         }
         cp_async_commit();
     }
@@ -279,7 +313,7 @@ struct Stream {
 
 template <class C>
 struct State {
-    uint32_t q[C::kNT][8][2];  // B fragments of the query rows, one pair per 16 columns
+    uint32_t q;                // this lane's query fragments: [group c][tile] 512 bytes apart
     float sc[C::kNT][2];       // logit scale (log2) of heads 2 tq, 2 tq + 1, positive
     float m[C::kNT][2], l[C::kNT][2];
     float acc[C::kNT][8][4];
@@ -302,50 +336,16 @@ struct State {
         }
     }
 
-    // A negative scale's sign goes into q, and a scale of zero becomes the
-    // smallest normal number (logits below 2^-100), so a masked score of -inf
-    // stays one.
-    // Columns 32 c + 8 tq .. + 8 of head g feed the two k steps of group c, in
-    // the order the codes of a token leave its word. q is scaled by a power of
-    // two so that the head's largest size lies in [1, 2) (f16's range).
-    __device__ __forceinline__ void init(const uint16_t* q_rows, int nrows, float scale_log2,
-                                         int lane) {
-        const int g = lane >> 2, tq = lane & 3;
+    // q_addr, sc_row: the head's fragments and logit scales in shared memory.
+    __device__ __forceinline__ void init(uint32_t q_addr, const float* sc_row, int lane) {
+        q = q_addr + lane * 16;
 #pragma unroll
         for (int n = 0; n < C::kNT; ++n) {
-            uint32_t w[16];
-            const bool have = n * 8 + g < nrows;
-            const uint4* src =
-                reinterpret_cast<const uint4*>(q_rows + static_cast<size_t>(n * 8 + g) * kHeadDim);
-            uint32_t top = 0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint4 x = have ? __ldg(src + c * 4 + tq) : make_uint4(0, 0, 0, 0);
-                w[4 * c] = x.x;
-                w[4 * c + 1] = x.y;
-                w[4 * c + 2] = x.z;
-                w[4 * c + 3] = x.w;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // exponent field of the largest size, kept where 2^+-exponent is a
-            // normal float
-            const uint32_t e = min(max(top >> 7, 1u), 253u);
-            const float f = copysignf(__uint_as_float((254u - e) << 23), scale_log2);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                q[n][i >> 1][i & 1] = pack_f16x2(__uint_as_float(w[i] << 16) * f,
-                                                 __uint_as_float(w[i] & 0xffff0000u) * f);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t eh = __shfl_sync(0xffffffffu, e, (2 * tq + j) * 4);
-                sc[n][j] = fmaxf(fabsf(scale_log2) * __uint_as_float(eh << 23), 1.17549435e-38f);
-                m[n][j] = -INFINITY;
-                l[n][j] = 0.f;
-            }
+            const float2 f = *reinterpret_cast<const float2*>(sc_row + n * 8 + 2 * (lane & 3));
+            sc[n][0] = f.x;
+            sc[n][1] = f.y;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
@@ -359,41 +359,45 @@ struct State {
         const int pg = row_token(lane >> 2);
         // ---- S^T = K Q^T
         float s[2][C::kNT][4];
+        uint2 ks[2][2];  // [token block][row g, g + 8]: the four groups' f16 scales
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
-            const uint2 k0 = lds64(chunk + ks_off + tb * 16 * kScaleBytes);
-            const uint2 k1 = lds64(chunk + ks_off + (tb * 16 + 8) * kScaleBytes);
-            const float2 s01 = f16x2_floats(k0.x), s23 = f16x2_floats(k0.y);
-            const float2 t01 = f16x2_floats(k1.x), t23 = f16x2_floats(k1.y);
-            const float ks0[4] = {s01.x, s01.y, s23.x, s23.y};
-            const float ks1[4] = {t01.x, t01.y, t23.x, t23.y};
+            ks[tb][0] = lds64(chunk + ks_off + tb * 16 * kScaleBytes);
+            ks[tb][1] = lds64(chunk + ks_off + (tb * 16 + 8) * kScaleBytes);
+        }
 #pragma unroll
-            for (int c = 0; c < 4; c += 2) {
-                uint32_t w[4];
-                ldsm_x4(chunk + (k_off ^ (c << 4)) + tb * 16 * kCodeBytes, w);
+        for (int c = 0; c < 4; c += 2) {
+            uint32_t w[2][4];
 #pragma unroll
-                for (int cc = 0; cc < 2; ++cc) {
-                    uint32_t a[4], b[4];
-                    codes_to_f16(w[2 * cc], a);
-                    codes_to_f16(w[2 * cc + 1], b);
-                    const int grp = c + cc;
+            for (int tb = 0; tb < 2; ++tb)
+                ldsm_x4(chunk + (k_off ^ (c << 4)) + tb * 16 * kCodeBytes, w[tb]);
 #pragma unroll
-                    for (int n = 0; n < C::kNT; ++n) {
+            for (int cc = 0; cc < 2; ++cc) {
+                const int grp = c + cc;
+                uint32_t a[2][4], b[2][4];
+                float f[2][2];
+#pragma unroll
+                for (int tb = 0; tb < 2; ++tb) {
+                    codes_to_f16(w[tb][2 * cc], a[tb]);
+                    codes_to_f16(w[tb][2 * cc + 1], b[tb]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float2 two = f16x2_floats(c ? ks[tb][j].y : ks[tb][j].x);
+                        f[tb][j] = cc ? two.y : two.x;
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < C::kNT; ++n) {
+                    const uint4 qf = lds128(q + (grp * C::kNT + n) * 512);
+#pragma unroll
+                    for (int tb = 0; tb < 2; ++tb) {
                         float t[4];
-                        mma_f16_zero(t, a[0], b[0], a[1], b[1], q[n][2 * grp][0], q[n][2 * grp][1]);
-                        mma_f16(t, a[2], b[2], a[3], b[3], q[n][2 * grp + 1][0],
-                                q[n][2 * grp + 1][1]);
-                        if (grp == 0) {
-                            s[tb][n][0] = t[0] * ks0[0];
-                            s[tb][n][1] = t[1] * ks0[0];
-                            s[tb][n][2] = t[2] * ks1[0];
-                            s[tb][n][3] = t[3] * ks1[0];
-                        } else {
-                            s[tb][n][0] = fmaf(t[0], ks0[grp], s[tb][n][0]);
-                            s[tb][n][1] = fmaf(t[1], ks0[grp], s[tb][n][1]);
-                            s[tb][n][2] = fmaf(t[2], ks1[grp], s[tb][n][2]);
-                            s[tb][n][3] = fmaf(t[3], ks1[grp], s[tb][n][3]);
-                        }
+                        mma_f16_zero(t, a[tb][0], b[tb][0], a[tb][1], b[tb][1], qf.x, qf.y);
+                        mma_f16(t, a[tb][2], b[tb][2], a[tb][3], b[tb][3], qf.z, qf.w);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s[tb][n][e] = grp == 0 ? t[e] * f[tb][e >> 1]
+                                                   : fmaf(t[e], f[tb][e >> 1], s[tb][n][e]);
                     }
                 }
             }
@@ -525,6 +529,48 @@ struct State {
     }
 };
 
+// Turns a unit's query rows into f16 fragments: eight rows a pass, 16 threads a
+// row, a thread 8 columns (one lane's fragment of a group). A row is scaled by a
+// power of two so that its largest size lies in [1, 2) (f16's range); a negative
+// logit scale's sign goes into q, and a scale of zero becomes the smallest normal
+// number (logits below 2^-100), so a masked score of -inf stays one.
+template <class C>
+__device__ __forceinline__ void convert_query(const QuantDecodeParams& qp, uint8_t* base) {
+    float* sc = reinterpret_cast<float*>(base + C::kScOff);
+    const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
+    const int G = qp.d.group;
+    for (int i = 0; i < qp.heads * C::kNT; ++i) {
+        const int hd = i >= C::kNT ? 1 : 0, n = i - hd * C::kNT;
+        const int r = n * 8 + row;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < G)
+            x = *reinterpret_cast<const uint4*>(base + C::kRawOff + (hd * G + r) * (kHeadDim * 2) +
+                                                col * 16);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[j] & 0x7fff7fffu);
+        top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // exponent field of the largest size, kept where 2^+-exponent is a
+        // normal float
+        const uint32_t e = min(max(top >> 7, 1u), 253u);
+        const float f = copysignf(__uint_as_float((254u - e) << 23), qp.d.scale_log2);
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            h[j] = pack_f16x2(__uint_as_float(w[j] << 16) * f,
+                              __uint_as_float(w[j] & 0xffff0000u) * f);
+        *reinterpret_cast<uint4*>(base + C::kQOff + hd * C::kQHeadBytes +
+                                  ((col >> 2) * C::kNT + n) * 512 + (row * 4 + (col & 3)) * 16) =
+            make_uint4(h[0], h[1], h[2], h[3]);
+        if (col == 0)
+            sc[hd * C::kRows + r] =
+                fmaxf(fabsf(qp.d.scale_log2) * __uint_as_float(e << 23), 1.17549435e-38f);
+    }
+}
+
 template <class C, class WL>
 __global__ void __launch_bounds__(kThreads, C::kCtas)
     quant_decode_kernel(const __grid_constant__ QuantDecodeParams qp,
@@ -533,88 +579,124 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     const DecodeParams& p = qp.d;
     float* red_m = reinterpret_cast<float*>(base + C::kRedOff);
     float* red_l = red_m + kWarps * 8;
-    volatile int* dump_slot = reinterpret_cast<volatile int*>(base + C::kFlagOff);  // [warp] or -1
-    volatile int* range = dump_slot + kWarps;  // first unit, end unit
+    volatile int* dump_at = reinterpret_cast<volatile int*>(base + C::kFlagOff);  // [warp]
+    volatile int* range = dump_at + kWarps;  // first unit, end unit
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    uint64_t* q_bar = reinterpret_cast<uint64_t*>(base + C::kBarOff);
+    if (threadIdx.x == 0) {
+        mbar_init(q_bar, 1);
+        fence_mbar_init();
+    }
     // as a programmatic dependent: nothing in global memory before this
     grid_dependency_wait();
-    // This CTA's units, from the parameter buffer or the workspace; one thread
-    // reads the range, so every warp passes the same number of barriers.
-    const int4* units = p.units;
+    // This CTA's units, from the parameter buffer or the workspace. Their range
+    // and first entries go through shared memory: every warp passes the same
+    // number of barriers, whatever happens to the list meanwhile.
+    const int4* list = p.units;
+    Unit* shared_list = reinterpret_cast<Unit*>(base + C::kListOff);
+    int a = 0, b = 0;
+    bool listed = false;
+    if constexpr (std::is_same<WL, WorkList>::value) {
+        if (list == nullptr) {
+            list = work.unit;
+            a = work.cta_begin[blockIdx.x];
+            b = work.cta_begin[blockIdx.x + 1];
+            listed = true;
+        }
+    }
+    if (!listed) {
+        const int4 r = __ldg(p.cta_rec + 2 * blockIdx.x);
+        a = r.x;
+        b = r.y;
+    }
+    const bool mine = (p.ws_stamp == nullptr || *p.ws_stamp == p.stamp) && a >= 0 &&
+                      b <= p.n_units && a <= b;
+    if (!mine) a = b = 0;
     if (threadIdx.x == 0) {
         if (blockIdx.x == 0) {
             *p.last_epoch = p.epoch;
             if (p.clear_stamp != nullptr) *p.clear_stamp = 0ull;
         }
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        int a = 0, b = 0;
-        bool listed = false;
-        if constexpr (std::is_same<WL, WorkList>::value) {
-            if (units == nullptr) {
-                a = work.cta_begin[blockIdx.x];
-                b = work.cta_begin[blockIdx.x + 1];
-                listed = true;
-            }
-        }
-        if (!listed) {
-            const int4 r = __ldg(p.cta_rec + 2 * blockIdx.x);
-            a = r.x;
-            b = r.y;
-        }
-        if ((p.ws_stamp != nullptr && *p.ws_stamp != p.stamp) || a < 0 || b > p.n_units || a > b) {
-            record_status(p.status, p.epoch, kDevicePlanMismatch);
-            a = b = 0;
-        }
+        if (!mine) record_status(p.status, p.epoch, kDevicePlanMismatch);
         range[0] = a;
         range[1] = b;
     }
-    if constexpr (std::is_same<WL, WorkList>::value) {
-        if (units == nullptr) units = work.unit;
+    // warp 0 decodes and checks the units in shared memory, the others' check
+    // comes when they are reached
+    Unit own;
+    int4 own_it = make_int4(0, 0, 0, 0);
+    const bool have = threadIdx.x < kListed && static_cast<int>(threadIdx.x) < b - a;
+    if (have) {
+        own_it = list[a + threadIdx.x];
+        own = decode_unit(qp, own_it);
+        shared_list[threadIdx.x] = own;
     }
     __syncthreads();
     const int u_begin = range[0], u_end = range[1];
+    if (u_begin >= u_end) return;
+    const UnitList units{shared_list, list, u_begin};
 
     uint8_t* ring = base + warp * C::kStages * C::kSlotBytes;
     const uint32_t ring_addr = smem_addr(ring);
     const uint32_t dst =
         (lane >> 2) * kCodeBytes + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
     const uint32_t sdst = (lane < 16 ? C::kKsOff : C::kVsOff) + (lane & 15) * 16;
+    // The query rows of a unit (contiguous) come as one bulk copy, a unit ahead;
+    // one that is not a unit of this plan has none.
+    const int G = p.group;
+    int q_issued = 0;  // copies issued, as every thread counts them
+    auto copy_query = [&](int i) {
+        if (i >= u_end) return;
+        const Unit u = units.get(qp, i);
+        if (u.n_chunks == 0) return;
+        if (threadIdx.x == 0) {
+            const uint32_t bytes = qp.heads * G * kHeadDim * 2;
+            mbar_arrive_expect_tx(q_bar, bytes);
+            bulk_load(smem_addr(base) + C::kRawOff,
+                      p.q + (static_cast<size_t>(u.b) * p.num_qo_heads + u.h * G) * kHeadDim, bytes,
+                      q_bar);
+        }
+        ++q_issued;
+    };
+    // Waits for the last of them and makes the fragments. Every thread waits.
+    auto take_query = [&](int i) {
+        if (i >= u_end || units.get(qp, i).n_chunks == 0) return;
+        const uint32_t parity = (q_issued - 1) & 1;
+        if (!mbar_wait(q_bar, parity, nullptr, p.wait_ns)) {
+            record_status(p.status, p.epoch, kDeviceWaitTimeout);
+            mbar_wait(q_bar, parity, nullptr, kWaitTimeoutNs);  // the copy still lands first
+        }
+        convert_query<C>(qp, base);
+    };
+    copy_query(u_begin);
     Stream<C> in;
     in.wl2 = qp.heads == 2 ? 1 : 2;
     in.w = warp & ((1 << in.wl2) - 1);
     in.head = warp >> in.wl2;
     in.u_end = u_end;
-    in.unit = u_begin;
-    if (u_begin < u_end) in.enter(qp, units, __ldg(units + u_begin), false, lane);
+    in.unit = u_begin - 1;
+    in.load_next_window(qp, units, lane);  // the first unit's
+    in.c = in.n_chunks = 0;
     for (int i = 0; i < C::kStages; ++i)
         in.refill(qp, units, ring_addr + i * C::kSlotBytes, dst, sdst, lane);
+    if (have && !tables_match(p, own, own_it)) record_status(p.status, p.epoch, kDevicePlanMismatch);
+    take_query(u_begin);
+    __syncthreads();
+    copy_query(u_begin + 1);
 
     State<C> st;
     st.set_lane(lane);
+    const uint32_t q_addr = smem_addr(base) + C::kQOff + in.head * C::kQHeadBytes;
+    const float* sc_row = reinterpret_cast<const float*>(base + C::kScOff) + in.head * C::kRows;
     int slot = 0;  // of the next chunk
-    const int G = p.group;
     for (int ui = u_begin; ui < u_end; ++ui) {
-        const int4 it = __ldg(units + ui);
-        const Unit u = decode_unit(qp, it);
-        const int nrows = min(G - u.row0, C::kRows);
-        // first query row of the unit's first head; the next head's are G on
-        const size_t row_base =
-            static_cast<size_t>(u.b) * p.num_qo_heads + u.h * G + u.row0;
-        if (threadIdx.x == 0) {
-            if (!u.ok) {
-                record_status(p.status, p.epoch, kDevicePlanMismatch);
-            } else {
-                const int last_len = (it.y >> kUnitPagesBits) & 0x7f;
-                if ((it.y < 0 && p.indptr[u.b] != it.x) ||
-                    (last_len && (p.indptr[u.b + 1] != it.x + u.n_pages ||
-                                  p.last_page_len[u.b] != last_len)))
-                    record_status(p.status, p.epoch, kDevicePlanMismatch);
-            }
-        }
+        const Unit u = units.get(qp, ui);
+        if (ui - u_begin >= kListed && threadIdx.x == 0 && !tables_match(p, u, __ldg(list + ui)))
+            record_status(p.status, p.epoch, kDevicePlanMismatch);
         int held = -1;  // the slot of the warp's last chunk, not refilled yet
-        if (in.w < u.n_chunks)
-            st.init(p.q + (row_base + in.head * G) * kHeadDim, nrows, p.scale_log2, lane);
+        st.init(q_addr, sc_row, lane);
         for (int c = in.w; c < u.n_chunks; c += 1 << in.wl2) {
             cp_async_wait<C::kStages - 1>();
             __syncwarp();  // every lane's copies of the chunk have landed
@@ -633,63 +715,74 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         }
         // ---- merge the warps' states, eight rows at a time, each through the
         // slot its warp read last
+        const int dump_off = (warp * C::kStages + held) * C::kSlotBytes;
+        if (lane == 0) dump_at[warp] = held >= 0 ? dump_off : -1;
 #pragma unroll
         for (int n = 0; n < C::kNT; ++n) {
-            if (lane == 0) dump_slot[warp] = held;
+            if (n * 8 >= G) break;
             if (held >= 0)
-                st.dump(n, reinterpret_cast<float*>(ring + held * C::kSlotBytes),
-                        red_m + warp * 8, red_l + warp * 8, lane);
+                st.dump(n, reinterpret_cast<float*>(base + dump_off), red_m + warp * 8,
+                        red_l + warp * 8, lane);
             __syncthreads();
-            const int rows = u.ok ? max(0, min(8, nrows - n * 8)) : 0;
-            const int per_head = rows * (kHeadDim / 4);
-            for (int i = threadIdx.x; i < per_head * qp.heads; i += kThreads) {
-                const int hd = i >= per_head ? 1 : 0;
-                const int r = (i - hd * per_head) / (kHeadDim / 4), c4 = i % (kHeadDim / 4);
-                // the states of the head's warps
-                const int w_begin = hd << in.wl2, w_end = w_begin + (1 << in.wl2);
-                float M = -INFINITY;
-                for (int w = w_begin; w < w_end; ++w)
-                    if (dump_slot[w] >= 0) M = fmaxf(M, red_m[w * 8 + r]);
+            const int rows = u.n_chunks > 0 ? min(8, G - n * 8) : 0;
+            // a warp takes whole rows: a lane four columns
+            for (int i = warp; i < rows * qp.heads; i += kWarps) {
+                const int hd = i >= rows ? 1 : 0, r = i - hd * rows;
+                const int w0 = hd << in.wl2;  // the head's first warp
+                float mw[kWarps], M = -INFINITY;
+                int at[kWarps];
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const bool there = w < 1 << in.wl2;
+                    at[w] = there ? dump_at[w0 + w] : -1;
+                    mw[w] = at[w] >= 0 ? red_m[(w0 + w) * 8 + r] : -INFINITY;
+                    M = fmaxf(M, mw[w]);
+                }
                 const float mu = M == -INFINITY ? 0.f : M;
                 float L = 0.f;
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int w = w_begin; w < w_end; ++w) {
-                    const int sl = dump_slot[w];
-                    if (sl < 0) continue;
-                    const float f = fast_exp2(red_m[w * 8 + r] - mu);
-                    const float4 a = *reinterpret_cast<const float4*>(
-                        base + (w * C::kStages + sl) * C::kSlotBytes +
-                        (r * kHeadDim + ((c4 ^ (r & 7)) * 4)) * 4);
-                    L += red_l[w * 8 + r] * f;
-                    o.x += a.x * f;
-                    o.y += a.y * f;
-                    o.z += a.z * f;
-                    o.w += a.w * f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    if (at[w] < 0) continue;
+                    const float f = fast_exp2(mw[w] - mu);
+                    const float4 v = *reinterpret_cast<const float4*>(
+                        base + at[w] + (r * kHeadDim + ((lane ^ (r & 7)) * 4)) * 4);
+                    L = fmaf(red_l[(w0 + w) * 8 + r], f, L);
+                    o.x = fmaf(v.x, f, o.x);
+                    o.y = fmaf(v.y, f, o.y);
+                    o.z = fmaf(v.z, f, o.z);
+                    o.w = fmaf(v.w, f, o.w);
                 }
-                const float inv = L != 0.f ? 1.f / L : 0.f;
+                const float inv = L != 0.f ? __fdividef(1.f, L) : 0.f;
                 o.x *= inv;
                 o.y *= inv;
                 o.z *= inv;
                 o.w *= inv;
-                const float lse2 = L != 0.f ? M - kPOffset + log2f(L) : -INFINITY;
                 const int row_in_unit = hd * G + n * 8 + r;
+                float* lse = nullptr;
+                float to_lse = 1.f;
                 if (u.slot < 0) {
-                    const size_t row = row_base + row_in_unit;
+                    const size_t row =
+                        static_cast<size_t>(u.b) * p.num_qo_heads + u.h * G + row_in_unit;
                     uint2 v;
                     v.x = pack_bf16x2(o.x, o.y);
                     v.y = pack_bf16x2(o.z, o.w);
-                    *reinterpret_cast<uint2*>(p.out + row * kHeadDim + c4 * 4) = v;
-                    if (c4 == 0 && p.lse != nullptr) p.lse[row] = lse2 * kLn2;
+                    *reinterpret_cast<uint2*>(p.out + row * kHeadDim + lane * 4) = v;
+                    if (p.lse != nullptr) lse = p.lse + row;
+                    to_lse = kLn2;
                 } else {
                     // partial states are [slot][heads * G][128]
-                    const size_t row = static_cast<size_t>(u.slot) * G * qp.heads + u.row0 +
-                                       row_in_unit;
-                    *reinterpret_cast<float4*>(p.part_o + row * kHeadDim + c4 * 4) = o;
-                    if (c4 == 0) p.part_lse[row] = lse2;
+                    const size_t row = static_cast<size_t>(u.slot) * G * qp.heads + row_in_unit;
+                    *reinterpret_cast<float4*>(p.part_o + row * kHeadDim + lane * 4) = o;
+                    lse = p.part_lse + row;
                 }
+                if (lane == 0 && lse != nullptr)
+                    *lse = L != 0.f ? (M - kPOffset + __log2f(L)) * to_lse : -INFINITY;
             }
+            if (n == 0) take_query(ui + 1);  // no warp reads this unit's any more
             __syncthreads();
         }
+        copy_query(ui + 2);
         if (held >= 0)
             in.refill(qp, units, ring_addr + held * C::kSlotBytes, dst, sdst, lane);
     }
@@ -765,17 +858,28 @@ VariantShape shape() {
 // The page size changes neither the registers (capped by the launch bound) nor
 // the shared memory.
 VariantShape quant_shape(int variant) {
-    return variant == kVariantQuant8 ? shape<CfgQ8<16>>() : shape<CfgQ16<16>>();
+    switch (variant) {
+        case kVariantQuant8: return shape<CfgQ8<16>>();
+        case kVariantQuant16: return shape<CfgQ16<16>>();
+        default: return shape<CfgQ32<16>>();
+    }
 }
 
 cudaError_t quant_occupancy(int variant, int* n) {
-    return variant == kVariantQuant8 ? occupancy<CfgQ8<16>>(n) : occupancy<CfgQ16<16>>(n);
+    switch (variant) {
+        case kVariantQuant8: return occupancy<CfgQ8<16>>(n);
+        case kVariantQuant16: return occupancy<CfgQ16<16>>(n);
+        default: return occupancy<CfgQ32<16>>(n);
+    }
 }
 
 cudaError_t launch_decode_quant(int variant, const QuantDecodeParams& p, const WorkList* w,
                                 int grid, cudaStream_t stream, bool pdl) {
-    if (variant == kVariantQuant8) return launch_ps<CfgQ8>(p, w, grid, stream, pdl);
-    return launch_ps<CfgQ16>(p, w, grid, stream, pdl);
+    switch (variant) {
+        case kVariantQuant8: return launch_ps<CfgQ8>(p, w, grid, stream, pdl);
+        case kVariantQuant16: return launch_ps<CfgQ16>(p, w, grid, stream, pdl);
+        default: return launch_ps<CfgQ32>(p, w, grid, stream, pdl);
+    }
 }
 
 }  // namespace oxd

@@ -394,7 +394,7 @@ oxd_status plan_decode(const oxd_paged_decode_desc* desc, const int32_t* indptr,
     // Groups of more than 16 query heads run every piece on a pair of CTAs,
     // one per 16-row half, side by side (the second read of each page is
     // then served by L2); the partition below is over CTA pairs.
-    const int copies = variant == kVariantMma32 || variant == kVariantQuant32 ? 2 : 1;
+    const int copies = variant == kVariantMma32 ? 2 : 1;
     const int64_t resident = static_cast<int64_t>(num_sms) * ctas_per_sm / copies;
     auto tokens_to = [&](int b, int k) {  // tokens in pages [0, k) of request b
         const int P = indptr[b + 1] - indptr[b];

@@ -24,7 +24,7 @@ enum Variant : int {
     kVariantWide = 5,    // 17 <= G <= 32: tcgen05 (TMEM accumulators), one CTA per piece
     kVariantQuant8 = 6,  // 4-bit cache (oxd_decode_quant.cu), G <= 8
     kVariantQuant16 = 7, // 9 <= G <= 16
-    kVariantQuant32 = 8, // 17 <= G <= 32: each piece runs on a pair of 16-row CTAs
+    kVariantQuant32 = 8, // 17 <= G <= 32
     kNumVariants = 9
 };
 
