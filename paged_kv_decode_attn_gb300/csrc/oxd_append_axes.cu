@@ -146,11 +146,7 @@ __device__ __forceinline__ void store_slice(uint16_t* row, int s, const Slice& x
     *reinterpret_cast<uint4*>(row + 8 * s) = x.lo;
     *reinterpret_cast<uint4*>(row + 64 + 8 * s) = x.hi;
 }
-__device__ __forceinline__ float low_f(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float high_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
 // cs: the token's cosines and sines in shared memory, the lane's pair j at 8 j.
-template <bool kExact>
 __device__ __forceinline__ Slice rotate(const Slice& x, const float4* cs) {
     const uint32_t* a = &x.lo.x;
     const uint32_t* b = &x.hi.x;
@@ -159,16 +155,51 @@ __device__ __forceinline__ Slice rotate(const Slice& x, const float4* cs) {
     uint32_t* yb = &y.hi.x;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a0 = low_f(a[i]), a1 = high_f(a[i]), b0 = low_f(b[i]), b1 = high_f(b[i]);
+        const float a0 = bf16_low(a[i]), a1 = bf16_high(a[i]);
+        const float b0 = bf16_low(b[i]), b1 = bf16_high(b[i]);
         const float4 t0 = cs[8 * (2 * i)], t1 = cs[8 * (2 * i + 1)];
-        if constexpr (kExact) {
+        ya[i] = pack_bf16x2(a0 * t0.x - b0 * t0.y, a1 * t1.x - b1 * t1.y);
+        yb[i] = pack_bf16x2(b0 * t0.x + a0 * t0.y, b1 * t1.x + a1 * t1.y);
+    }
+    return y;
+}
+
+// The same with the bf16 numbers nearest to the exact rotation. The float
+// result y is within 2^-21 (|a| + |b|) of it (cosine and sine rounded once, two
+// products, a sum): where both ends of that range round alike, that is it. A
+// lane with a value where they do not (about one in 200) forms its slice anew
+// with the low parts.
+__device__ __forceinline__ Slice rotate_exact(const Slice& x, const float4* cs) {
+    const uint32_t* a = &x.lo.x;
+    const uint32_t* b = &x.hi.x;
+    Slice y;
+    uint32_t* ya = &y.lo.x;
+    uint32_t* yb = &y.hi.x;
+    constexpr float kErr = 4.76837158e-7f;  // 2^-21
+    uint32_t differ = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a0 = bf16_low(a[i]), a1 = bf16_high(a[i]);
+        const float b0 = bf16_low(b[i]), b1 = bf16_high(b[i]);
+        const float4 t0 = cs[8 * (2 * i)], t1 = cs[8 * (2 * i + 1)];
+        const float n0 = fabsf(a0) + fabsf(b0), n1 = fabsf(a1) + fabsf(b1);
+        const float u0 = a0 * t0.x - b0 * t0.y, u1 = a1 * t1.x - b1 * t1.y;
+        const float v0 = b0 * t0.x + a0 * t0.y, v1 = b1 * t1.x + a1 * t1.y;
+        ya[i] = pack_bf16x2(fmaf(n0, kErr, u0), fmaf(n1, kErr, u1));
+        yb[i] = pack_bf16x2(fmaf(n0, kErr, v0), fmaf(n1, kErr, v1));
+        differ |= ya[i] ^ pack_bf16x2(fmaf(n0, -kErr, u0), fmaf(n1, -kErr, u1));
+        differ |= yb[i] ^ pack_bf16x2(fmaf(n0, -kErr, v0), fmaf(n1, -kErr, v1));
+    }
+    if (differ != 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a0 = bf16_low(a[i]), a1 = bf16_high(a[i]);
+            const float b0 = bf16_low(b[i]), b1 = bf16_high(b[i]);
+            const float4 t0 = cs[8 * (2 * i)], t1 = cs[8 * (2 * i + 1)];
             ya[i] = pack_bf16x2(exact_turn(a0, t0.x, t0.z, b0, t0.y, t0.w),
                                 exact_turn(a1, t1.x, t1.z, b1, t1.y, t1.w));
             yb[i] = pack_bf16x2(exact_turn(b0, t0.x, t0.z, -a0, t0.y, t0.w),
                                 exact_turn(b1, t1.x, t1.z, -a1, t1.y, t1.w));
-        } else {
-            ya[i] = pack_bf16x2(a0 * t0.x - b0 * t0.y, a1 * t1.x - b1 * t1.y);
-            yb[i] = pack_bf16x2(b0 * t0.x + a0 * t0.y, b1 * t1.x + a1 * t1.y);
         }
     }
     return y;
@@ -179,22 +210,9 @@ __device__ __forceinline__ Slice rotate(const Slice& x, const float4* cs) {
 // `live` lanes store.
 __device__ __forceinline__ void hold_slice(uint8_t* codes, uint16_t* scales, const Slice& x, int s,
                                            bool live) {
-    const uint4 w[2] = {x.lo, x.hi};
     uint32_t sc[2], code[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const uint32_t v[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-        float amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(low_f(v[i])), fabsf(high_f(v[i]))));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        sc[j] = group_scale(amax);
-        const float inv = scale_inverse(static_cast<uint16_t>(sc[j]));
-        code[j] = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) code[j] |= code_pair(low_f(v[i]), high_f(v[i]), inv) << (8 * i);
-    }
+    hold_eight(x.lo, code[0], sc[0]);
+    hold_eight(x.hi, code[1], sc[1]);
     const uint32_t far0 = __shfl_xor_sync(0xffffffffu, sc[0], 4);
     const uint32_t far1 = __shfl_xor_sync(0xffffffffu, sc[1], 4);
     if (live) {
@@ -207,7 +225,7 @@ __device__ __forceinline__ void hold_slice(uint8_t* codes, uint16_t* scales, con
 
 // kTokens: tokens a block takes; its warps are divided among them.
 template <bool k4, int kTokens>
-__global__ void __launch_bounds__(kWarps * 32, k4 ? 3 : 4)
+__global__ void __launch_bounds__(kWarps * 32, 4)
     axes_append_kernel(const __grid_constant__ AxesAppendParams p) {
     constexpr int kTokenWarps = kWarps / kTokens;
     __shared__ float4 cs_all[kTokens][kPairs];
@@ -286,7 +304,7 @@ __global__ void __launch_bounds__(kWarps * 32, k4 ? 3 : 4)
                 v0 = load_slice(p.v + row, s);
             }
             if (!live) k0 = v0 = Slice{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-            const Slice k = rotate<k4>(k0, cs);
+            const Slice k = k4 ? rotate_exact(k0, cs) : rotate(k0, cs);
             const int hd = live ? h : 0;
             const size_t dst = row_index(p.layout, page, slot, hd, p.Hkv, p.page_size);
             if constexpr (k4) {
@@ -316,7 +334,7 @@ __global__ void __launch_bounds__(kWarps * 32, k4 ? 3 : 4)
             const int h = (task + j * kTokenWarps) * kRowsPerTask + sub;
             if (h < p.Hq)
                 store_slice(p.q_out + (static_cast<size_t>(t) * p.Hq + h) * kHeadDim, s,
-                            rotate<false>(x[j], cs));
+                            rotate(x[j], cs));
         }
     }
 }

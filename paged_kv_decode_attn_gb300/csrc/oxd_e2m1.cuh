@@ -18,37 +18,64 @@ constexpr int kRowScales = kHeadDim / kScaleGroup;
 constexpr float kMaxScale = 10912.f;
 
 // f16 scale bits of a group whose largest size is `amax` (a bf16 value): the
-// f16 number nearest to amax / 6. The f32 quotient rounds to the same f16
-// number as the exact one: amax has 8 significant bits, so amax / 6 either has
-// no more (a multiple of 3) or repeats in binary and stays clear of the
-// midpoints of 11-bit numbers by far more than f32 rounds.
-__device__ __forceinline__ uint16_t group_scale(float amax) {
-    return __half_as_ushort(__float2half_rn(fminf(__fdiv_rn(amax, 6.f), kMaxScale)));
+// f16 number nearest to amax / 6. The product with the f32 nearest to 1/6 is
+// within 2^-23 of the quotient, and rounds to the same f16 number: amax has 8
+// significant bits, so amax / 6 either has no more (a multiple of 3) or repeats
+// in binary, and stays clear of the midpoints of 11-bit numbers by far more.
+// Only below f16's normal range can a quotient be a midpoint; it is divided.
+__device__ __forceinline__ uint32_t group_scale(float amax) {
+    float q = amax * (1.f / 6.f);
+    if (q < 6.2e-5f) q = __fdiv_rn(amax, 6.f);
+    return __half_as_ushort(__float2half_rn(fminf(q, kMaxScale)));
 }
 
-// 1 / scale for code_pair; 0 for a group of zeros.
-__device__ __forceinline__ float scale_inverse(uint16_t scale) {
-    const float s = __half2float(__ushort_as_half(scale));
-    return s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
+// 1 / scale, to 2^-23; 0 for a group of zeros.
+__device__ __forceinline__ float scale_inverse(uint32_t scale) {
+    const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(scale)));
+    return s > 0.f ? __fdividef(1.f, s) : 0.f;
 }
 
-// Codes of two neighbouring columns (x0 in the low half of the byte), each the
-// e2m1 number nearest to x / s, ties to even. inv = 1 / s rounded, so x * inv
-// may miss a quotient that lies exactly between two codes by a rounding; the
-// quotient of an 8-bit by an 11-bit number that is no tie differs from one by
-// at least 2^-16 (a tie is at least 0.25 and t * s has 14 bits), so rounding
-// x * inv to a multiple of 2^-17, by adding and taking away 1.5 * 2^6, restores
-// ties and moves nothing across one.
-__device__ __forceinline__ uint32_t code_pair(float x0, float x1, float inv) {
+// x / s for its code, inv = 1 / s: x * inv may miss a quotient that lies exactly
+// between two codes by a rounding. The quotient of an 8-bit by an 11-bit number
+// that is no tie differs from one by at least 2^-16 (a tie is at least 0.25, and
+// tie * s has 14 bits), and x * inv is within 2^-19 of it up to 6, so rounding
+// it to a multiple of 2^-17, by adding and taking away 1.5 * 2^6, restores ties
+// and moves nothing across one.
+__device__ __forceinline__ float code_argument(float x, float inv) {
     constexpr float kGrid = 96.f;
-    const float y0 = __fadd_rn(fmaf(x0, inv, kGrid), -kGrid);
-    const float y1 = __fadd_rn(fmaf(x1, inv, kGrid), -kGrid);
+    return __fadd_rn(fmaf(x, inv, kGrid), -kGrid);
+}
+
+__device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Codes of eight columns (bf16 pairs): each the e2m1 number nearest to x / s,
+// ties to even, the first column in the lowest four bits.
+__device__ __forceinline__ uint32_t code_eight(const uint4& x, float inv) {
     uint32_t r;
-    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
-        "mov.b32 %0, {b, 0, 0, 0};\n\t}"
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
         : "=r"(r)
-        : "f"(y1), "f"(y0));
+        : "f"(code_argument(bf16_low(x.x), inv)), "f"(code_argument(bf16_high(x.x), inv)),
+          "f"(code_argument(bf16_low(x.y), inv)), "f"(code_argument(bf16_high(x.y), inv)),
+          "f"(code_argument(bf16_low(x.z), inv)), "f"(code_argument(bf16_high(x.z), inv)),
+          "f"(code_argument(bf16_low(x.w), inv)), "f"(code_argument(bf16_high(x.w), inv)));
     return r;
+}
+
+// Eight columns of a row in 4 bits, and their group's f16 scale. The group's
+// other columns are in the lanes next to this one (a multiple of four and its
+// three followers): every lane of the warp calls it.
+__device__ __forceinline__ void hold_eight(const uint4& x, uint32_t& code, uint32_t& scale) {
+    // sizes as the integers their bits are
+    uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                          __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    scale = group_scale(fmaxf(bf16_low(m), bf16_high(m)));
+    code = code_eight(x, scale_inverse(scale));
 }
 
 // The four code pairs of a 32-bit word as f16x2 (low half: the even column).

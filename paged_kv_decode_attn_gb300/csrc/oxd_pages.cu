@@ -39,20 +39,17 @@ __device__ __forceinline__ bool pair_pages(const CopyPagesParams& p, int i, bool
 
 // Equal formats and layouts: kPieces 16-byte pieces a thread.
 template <bool k4>
-__global__ void __launch_bounds__(kThreads) copy_pages_kernel(const CopyPagesParams p, int slices) {
+__global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_constant__ CopyPagesParams p) {
     constexpr int kPieces = 4;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.last_epoch = p.epoch;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.last_epoch = p.epoch;
     const int page_rows = p.page_size * p.H;
     const int row_pieces = (k4 ? kCodeBytes : kHeadDim * 2) / 16;
     const int data = page_rows * row_pieces;                     // pieces of a page's rows
     const int all = data + (k4 ? page_rows * kScaleBytes / 16 : 0);  // and of its scales
-    const long long work = static_cast<long long>(p.n) * 2 * slices;
-    for (long long x = blockIdx.x; x < work; x += gridDim.x) {
-        const int slice = static_cast<int>(x % slices);
-        const int tensor = static_cast<int>(x / slices) & 1;
-        const int i = static_cast<int>(x / slices >> 1);
+    const int slice = blockIdx.x >> 1, tensor = blockIdx.x & 1;
+    for (int i = blockIdx.y; i < p.n; i += gridDim.y) {
         int src, dst;
-        if (!pair_pages(p, i, slice == 0 && tensor == 0, &src, &dst)) continue;
+        if (!pair_pages(p, i, blockIdx.x == 0, &src, &dst)) continue;
         const uint4* from = reinterpret_cast<const uint4*>(p.src.data[tensor]) +
                             static_cast<size_t>(src) * data;
         uint4* to = reinterpret_cast<uint4*>(p.dst.data[tensor]) + static_cast<size_t>(dst) * data;
@@ -83,9 +80,6 @@ __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const CopyPagesPar
         }
     }
 }
-
-__device__ __forceinline__ float low_f(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float high_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // What a lane holds of a row: as bf16 pairs, or as codes and the scales of its
 // two groups.
@@ -136,22 +130,6 @@ struct Piece<true> {
     }
 };
 
-// Eight bf16 values in 4 bits, and their group's scale; the group's other
-// values are in the lanes next to this one.
-__device__ __forceinline__ void hold(const uint4& x, uint32_t& code, uint32_t& scale) {
-    const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(low_f(v[i])), fabsf(high_f(v[i]))));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    scale = group_scale(amax);
-    const float inv = scale_inverse(static_cast<uint16_t>(scale));
-    code = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) code |= code_pair(low_f(v[i]), high_f(v[i]), inv) << (8 * i);
-}
-
 __device__ __forceinline__ uint4 unhold(uint32_t code, uint32_t scale) {
     const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(scale)));
     uint32_t h[4], o[4];
@@ -167,8 +145,8 @@ __device__ __forceinline__ uint4 unhold(uint32_t code, uint32_t scale) {
 __device__ __forceinline__ void convert(const Piece<false>& a, Piece<false>& b) { b = a; }
 __device__ __forceinline__ void convert(const Piece<true>& a, Piece<true>& b) { b = a; }
 __device__ __forceinline__ void convert(const Piece<false>& a, Piece<true>& b) {
-    hold(a.lo, b.lo, b.s_lo);
-    hold(a.hi, b.hi, b.s_hi);
+    hold_eight(a.lo, b.lo, b.s_lo);
+    hold_eight(a.hi, b.hi, b.s_hi);
 }
 __device__ __forceinline__ void convert(const Piece<true>& a, Piece<false>& b) {
     b.lo = unhold(a.lo, a.s_lo);
@@ -176,21 +154,21 @@ __device__ __forceinline__ void convert(const Piece<true>& a, Piece<false>& b) {
 }
 
 // Other formats or layouts: kRows rows a thread's eight lanes take.
+constexpr int kRows = 2;
+constexpr int kSliceRows = kThreads / 8 * kRows;
+
 template <bool kSrc4, bool kDst4>
-__global__ void __launch_bounds__(kThreads) convert_pages_kernel(const CopyPagesParams p,
-                                                                 int slices) {
-    constexpr int kRows = 2;
-    constexpr int kSliceRows = kThreads / 8 * kRows;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.last_epoch = p.epoch;
+__global__ void __launch_bounds__(kThreads) convert_pages_kernel(const __grid_constant__
+                                                                 CopyPagesParams p) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.last_epoch = p.epoch;
     const int s = threadIdx.x & 7;
     const int page_rows = p.page_size * p.H;
-    const long long work = static_cast<long long>(p.n) * 2 * slices;
-    for (long long x = blockIdx.x; x < work; x += gridDim.x) {
-        const int slice = static_cast<int>(x % slices);
-        const int tensor = static_cast<int>(x / slices) & 1;
-        const int i = static_cast<int>(x / slices >> 1);
+    const int slice = blockIdx.x >> 1, tensor = blockIdx.x & 1;
+    // counting in the destination's order: (token, head) or (head, token)
+    const uint32_t inner = p.dst.layout == 0 ? p.H : p.page_size;
+    for (int i = blockIdx.y; i < p.n; i += gridDim.y) {
         int src, dst;
-        if (!pair_pages(p, i, slice == 0 && tensor == 0, &src, &dst)) continue;
+        if (!pair_pages(p, i, blockIdx.x == 0, &src, &dst)) continue;
         Piece<kSrc4> a[kRows];
         size_t to[kRows], to_s[kRows];
         bool live[kRows];
@@ -198,9 +176,9 @@ __global__ void __launch_bounds__(kThreads) convert_pages_kernel(const CopyPages
         for (int j = 0; j < kRows; ++j) {
             const int r = slice * kSliceRows + j * (kThreads / 8) + (threadIdx.x >> 3);
             live[j] = r < page_rows;
-            const int rr = live[j] ? r : 0;
-            const int t = p.dst.layout == 0 ? rr / p.H : rr % p.page_size;
-            const int h = p.dst.layout == 0 ? rr % p.H : rr / p.page_size;
+            const uint32_t rr = live[j] ? r : 0;
+            const uint32_t hi = rr / inner, lo = rr - hi * inner;
+            const int t = p.dst.layout == 0 ? hi : lo, h = p.dst.layout == 0 ? lo : hi;
             a[j].load(p.src, tensor, row_index(p.src.layout, src, t, h, p.H, p.page_size),
                       scale_index(src, t, h, p.H, p.page_size), s);
             to[j] = row_index(p.dst.layout, dst, t, h, p.H, p.page_size);
@@ -215,11 +193,12 @@ __global__ void __launch_bounds__(kThreads) convert_pages_kernel(const CopyPages
     }
 }
 
+// A row of blocks for every pair (the pairs in turn past 65535): K and V in
+// turn, slice by slice.
 template <class F>
-cudaError_t launch(F kernel, const CopyPagesParams& p, int slices, cudaStream_t stream) {
-    const long long work = static_cast<long long>(p.n) * 2 * slices;
-    const unsigned grid = static_cast<unsigned>(work < 1 ? 1 : work > (1 << 20) ? (1 << 20) : work);
-    kernel<<<grid, kThreads, 0, stream>>>(p, slices);
+cudaError_t launch(F kernel, const CopyPagesParams& p, long long slices, cudaStream_t stream) {
+    const dim3 grid(2 * static_cast<unsigned>(slices), p.n < 1 ? 1 : p.n > 65535 ? 65535 : p.n);
+    kernel<<<grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -230,11 +209,11 @@ cudaError_t launch_copy_pages(const CopyPagesParams& p, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.page_size) * p.H;
     if (s4 == d4 && p.src.layout == p.dst.layout) {
         const long long pieces = rows * (s4 ? kCodeBytes + kScaleBytes : kHeadDim * 2) / 16;
-        const int slices = static_cast<int>((pieces + kThreads * 4 - 1) / (kThreads * 4));
+        const long long slices = (pieces + kThreads * 4 - 1) / (kThreads * 4);
         return s4 ? launch(copy_pages_kernel<true>, p, slices, stream)
                   : launch(copy_pages_kernel<false>, p, slices, stream);
     }
-    const int slices = static_cast<int>((rows + kThreads / 4 - 1) / (kThreads / 4));
+    const long long slices = (rows + kSliceRows - 1) / kSliceRows;
     if (s4 && d4) return launch(convert_pages_kernel<true, true>, p, slices, stream);
     if (s4) return launch(convert_pages_kernel<true, false>, p, slices, stream);
     if (d4) return launch(convert_pages_kernel<false, true>, p, slices, stream);
