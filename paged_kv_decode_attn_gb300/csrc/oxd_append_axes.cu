@@ -146,8 +146,9 @@ __device__ __forceinline__ void store_slice(uint16_t* row, int s, const Slice& x
     *reinterpret_cast<uint4*>(row + 8 * s) = x.lo;
     *reinterpret_cast<uint4*>(row + 64 + 8 * s) = x.hi;
 }
-// cs: the token's cosines and sines in shared memory, the lane's pair j at 8 j.
-__device__ __forceinline__ Slice rotate(const Slice& x, const float4* cs) {
+// cs: the token's cosines and sines in shared memory, the lane's pair j at 8 j;
+// low: their low parts.
+__device__ __forceinline__ Slice rotate(const Slice& x, const float2* cs) {
     const uint32_t* a = &x.lo.x;
     const uint32_t* b = &x.hi.x;
     Slice y;
@@ -157,7 +158,7 @@ __device__ __forceinline__ Slice rotate(const Slice& x, const float4* cs) {
     for (int i = 0; i < 4; ++i) {
         const float a0 = bf16_low(a[i]), a1 = bf16_high(a[i]);
         const float b0 = bf16_low(b[i]), b1 = bf16_high(b[i]);
-        const float4 t0 = cs[8 * (2 * i)], t1 = cs[8 * (2 * i + 1)];
+        const float2 t0 = cs[8 * (2 * i)], t1 = cs[8 * (2 * i + 1)];
         ya[i] = pack_bf16x2(a0 * t0.x - b0 * t0.y, a1 * t1.x - b1 * t1.y);
         yb[i] = pack_bf16x2(b0 * t0.x + a0 * t0.y, b1 * t1.x + a1 * t1.y);
     }
@@ -168,8 +169,9 @@ __device__ __forceinline__ Slice rotate(const Slice& x, const float4* cs) {
 // result y is within 2^-21 (|a| + |b|) of it (cosine and sine rounded once, two
 // products, a sum): where both ends of that range round alike, that is it. A
 // lane with a value where they do not (about one in 200) forms its slice anew
-// with the low parts.
-__device__ __forceinline__ Slice rotate_exact(const Slice& x, const float4* cs) {
+// with the low parts, one pair of columns at a time.
+__device__ __forceinline__ Slice rotate_exact(const Slice& x, const float2* cs,
+                                              const float2* low) {
     const uint32_t* a = &x.lo.x;
     const uint32_t* b = &x.hi.x;
     Slice y;
@@ -181,7 +183,7 @@ __device__ __forceinline__ Slice rotate_exact(const Slice& x, const float4* cs) 
     for (int i = 0; i < 4; ++i) {
         const float a0 = bf16_low(a[i]), a1 = bf16_high(a[i]);
         const float b0 = bf16_low(b[i]), b1 = bf16_high(b[i]);
-        const float4 t0 = cs[8 * (2 * i)], t1 = cs[8 * (2 * i + 1)];
+        const float2 t0 = cs[8 * (2 * i)], t1 = cs[8 * (2 * i + 1)];
         const float n0 = fabsf(a0) + fabsf(b0), n1 = fabsf(a1) + fabsf(b1);
         const float u0 = a0 * t0.x - b0 * t0.y, u1 = a1 * t1.x - b1 * t1.y;
         const float v0 = b0 * t0.x + a0 * t0.y, v1 = b1 * t1.x + a1 * t1.y;
@@ -191,15 +193,27 @@ __device__ __forceinline__ Slice rotate_exact(const Slice& x, const float4* cs) 
         differ |= yb[i] ^ pack_bf16x2(fmaf(n0, -kErr, v0), fmaf(n1, -kErr, v1));
     }
     if (differ != 0) {
+        uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float a0 = bf16_low(a[i]), a1 = bf16_high(a[i]);
-            const float b0 = bf16_low(b[i]), b1 = bf16_high(b[i]);
-            const float4 t0 = cs[8 * (2 * i)], t1 = cs[8 * (2 * i + 1)];
-            ya[i] = pack_bf16x2(exact_turn(a0, t0.x, t0.z, b0, t0.y, t0.w),
-                                exact_turn(a1, t1.x, t1.z, b1, t1.y, t1.w));
-            yb[i] = pack_bf16x2(exact_turn(b0, t0.x, t0.z, -a0, t0.y, t0.w),
-                                exact_turn(b1, t1.x, t1.z, -a1, t1.y, t1.w));
+            w[i] = a[i];
+            w[4 + i] = b[i];
+        }
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const float a0 = bf16_low(w[i]), a1 = bf16_high(w[i]);
+            const float b0 = bf16_low(w[4 + i]), b1 = bf16_high(w[4 + i]);
+            const float2 t0 = cs[8 * (2 * i)], t1 = cs[8 * (2 * i + 1)];
+            const float2 l0 = low[8 * (2 * i)], l1 = low[8 * (2 * i + 1)];
+            w[i] = pack_bf16x2(exact_turn(a0, t0.x, l0.x, b0, t0.y, l0.y),
+                               exact_turn(a1, t1.x, l1.x, b1, t1.y, l1.y));
+            w[4 + i] = pack_bf16x2(exact_turn(b0, t0.x, l0.x, -a0, t0.y, l0.y),
+                                   exact_turn(b1, t1.x, l1.x, -a1, t1.y, l1.y));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ya[i] = w[i];
+            yb[i] = w[4 + i];
         }
     }
     return y;
@@ -228,7 +242,7 @@ template <bool k4, int kTokens>
 __global__ void __launch_bounds__(kWarps * 32, 4)
     axes_append_kernel(const __grid_constant__ AxesAppendParams p) {
     constexpr int kTokenWarps = kWarps / kTokens;
-    __shared__ float4 cs_all[kTokens][kPairs];
+    __shared__ float2 cs_all[kTokens][kPairs], low_all[k4 ? kTokens : 1][kPairs];
     __shared__ int bad_rope[kTokens];
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.last_epoch = p.epoch;
@@ -239,7 +253,6 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     const bool have = t_all < p.T;
     const int t = have ? static_cast<int>(t_all) : 0;
     const int kv_tasks = (p.Hkv + kRowsPerTask - 1) / kRowsPerTask;
-    const int q_tasks = (p.Hq + kRowsPerTask - 1) / kRowsPerTask;
 
     // The first rows and the page walk are under way while the angles are
     // formed. KV tasks go to the token's first warps.
@@ -264,7 +277,10 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
             const int rp = p.rope_positions[static_cast<size_t>(__float_as_int(g.w)) * p.T + ti];
             if (rp < 0 || rp >= (1 << 24)) bad_rope[i / kPairs] = 1;
             // pair 8 s + j at 8 j + s: the eight lanes of a row read a line
-            cs_all[i / kPairs][(i % 8) * 8 + i % kPairs / 8] = cos_sin(rp & ((1 << 24) - 1), g);
+            const int at = (i % 8) * 8 + i % kPairs / 8;
+            const float4 f = cos_sin(rp & ((1 << 24) - 1), g);
+            cs_all[i / kPairs][at] = make_float2(f.x, f.y);
+            if constexpr (k4) low_all[i / kPairs][at] = make_float2(f.z, f.w);
         }
     }
     int code = 0;
@@ -289,52 +305,56 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     }
     __syncthreads();
     if (!have) return;
-    const float4* cs = cs_all[local] + s;
+    const float2* cs = cs_all[local] + s;
 
     if (kv_warp) {
         if (code == 0 && bad_rope[local]) code = kDeviceBadPosition;
         if (code != 0 && wi == 0 && lane == 0) record_status(p.status, p.epoch, code);
-        const int slot = code == 0 ? pos % p.page_size : 0;
+        // the token's first row in the pools, and what a head's rows and scales
+        // are apart
+        const int slot = code == 0 ? pos & (p.page_size - 1) : 0;
+        const size_t row0 = row_index(p.layout, code == 0 ? page : 0, slot, 0, p.Hkv, p.page_size);
+        const int stride = p.layout == 0 ? 1 : p.page_size;
+        const uint16_t* k_in = p.k + static_cast<size_t>(t) * p.Hkv * kHeadDim;
+        const uint16_t* v_in = p.v + static_cast<size_t>(t) * p.Hkv * kHeadDim;
         for (int task = wi; task < kv_tasks && code == 0; task += kTokenWarps) {
             const int h = task * kRowsPerTask + sub;
             const bool live = h < p.Hkv;
             if (task != wi && live) {
-                const size_t row = (static_cast<size_t>(t) * p.Hkv + h) * kHeadDim;
-                k0 = load_slice(p.k + row, s);
-                v0 = load_slice(p.v + row, s);
+                k0 = load_slice(k_in + h * kHeadDim, s);
+                v0 = load_slice(v_in + h * kHeadDim, s);
             }
             if (!live) k0 = v0 = Slice{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-            const Slice k = k4 ? rotate_exact(k0, cs) : rotate(k0, cs);
             const int hd = live ? h : 0;
-            const size_t dst = row_index(p.layout, page, slot, hd, p.Hkv, p.page_size);
+            const size_t row = row0 + static_cast<size_t>(hd) * stride;
             if constexpr (k4) {
                 const size_t sc = scale_index(page, slot, hd, p.Hkv, p.page_size);
-                hold_slice(static_cast<uint8_t*>(p.k_pages) + dst * kCodeBytes, p.k_scales + sc, k,
+                hold_slice(static_cast<uint8_t*>(p.k_pages) + row * kCodeBytes, p.k_scales + sc,
+                           rotate_exact(k0, cs, low_all[local] + s), s, live);
+                hold_slice(static_cast<uint8_t*>(p.v_pages) + row * kCodeBytes, p.v_scales + sc, v0,
                            s, live);
-                hold_slice(static_cast<uint8_t*>(p.v_pages) + dst * kCodeBytes, p.v_scales + sc,
-                           v0, s, live);
             } else if (live) {
-                store_slice(static_cast<uint16_t*>(p.k_pages) + dst * kHeadDim, s, k);
-                store_slice(static_cast<uint16_t*>(p.v_pages) + dst * kHeadDim, s, v0);
+                store_slice(static_cast<uint16_t*>(p.k_pages) + row * kHeadDim, s, rotate(k0, cs));
+                store_slice(static_cast<uint16_t*>(p.v_pages) + row * kHeadDim, s, v0);
             }
         }
     }
     // Query rows, a batch of tasks' loads ahead of its stores (q_out may be q).
     // The warps are taken from the last on, behind the KV warps.
-    for (int task = kTokenWarps - 1 - wi; task < q_tasks; task += kTokenWarps * kBatch) {
+    const uint16_t* q_in = p.q + static_cast<size_t>(t) * p.Hq * kHeadDim;
+    uint16_t* q_to = p.q_out + static_cast<size_t>(t) * p.Hq * kHeadDim;
+    for (int h0 = (kTokenWarps - 1 - wi) * kRowsPerTask + sub; h0 - sub < p.Hq;
+         h0 += kTokenWarps * kRowsPerTask * kBatch) {
         Slice x[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            const int h = (task + j * kTokenWarps) * kRowsPerTask + sub;
-            if (h < p.Hq)
-                x[j] = load_slice(p.q + (static_cast<size_t>(t) * p.Hq + h) * kHeadDim, s);
+            const int h = h0 + j * kTokenWarps * kRowsPerTask;
+            if (h < p.Hq) x[j] = load_slice(q_in + h * kHeadDim, s);
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            const int h = (task + j * kTokenWarps) * kRowsPerTask + sub;
-            if (h < p.Hq)
-                store_slice(p.q_out + (static_cast<size_t>(t) * p.Hq + h) * kHeadDim, s,
-                            rotate(x[j], cs));
+            const int h = h0 + j * kTokenWarps * kRowsPerTask;
+            if (h < p.Hq) store_slice(q_to + h * kHeadDim, s, rotate(x[j], cs));
         }
     }
 }

@@ -248,6 +248,7 @@ struct CopyPagesParams {
     uint32_t* last_epoch;
     uint32_t epoch;
     int32_t n, H, page_size;
+    uint32_t inner_magic;    // for division by dst's inner count (heads or tokens), or 0
 };
 cudaError_t launch_copy_pages(const CopyPagesParams& p, cudaStream_t stream);
 

@@ -83,22 +83,37 @@ __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_const
 
 // What a lane holds of a row: as bf16 pairs, or as codes and the scales of its
 // two groups.
+// A page's rows of one tensor: where they and their scales begin.
+struct PageRows {
+    uint8_t* data;
+    uint16_t* scales;
+};
+
+template <bool k4>
+__device__ __forceinline__ PageRows page_rows_of(const PagePools& c, int tensor, int page,
+                                                 int rows) {
+    const size_t first = static_cast<size_t>(page) * rows;
+    return {c.data[tensor] + first * (k4 ? kCodeBytes : kHeadDim * 2),
+            k4 ? c.scales[tensor] + first * kRowScales : nullptr};
+}
+
+// row: in the pool's order; sc: in the order of scales (heads before tokens).
 template <bool k4>
 struct Piece;
 template <>
 struct Piece<false> {
     uint4 lo, hi;
-    __device__ __forceinline__ void load(const PagePools& c, int tensor, size_t row, size_t, int s) {
-        const uint4* r = reinterpret_cast<const uint4*>(c.data[tensor] + row * kHeadDim * 2);
-        lo = r[s];
-        hi = r[8 + s];
+    __device__ __forceinline__ void load(const PageRows& c, uint32_t row, uint32_t, int s) {
+        const uint4* r = reinterpret_cast<const uint4*>(c.data) + row * 16 + s;
+        lo = r[0];
+        hi = r[8];
     }
-    __device__ __forceinline__ void store(const PagePools& c, int tensor, size_t row, size_t, int s,
+    __device__ __forceinline__ void store(const PageRows& c, uint32_t row, uint32_t, int s,
                                           bool live) const {
-        uint4* r = reinterpret_cast<uint4*>(c.data[tensor] + row * kHeadDim * 2);
+        uint4* r = reinterpret_cast<uint4*>(c.data) + row * 16 + s;
         if (live) {
-            r[s] = lo;
-            r[8 + s] = hi;
+            r[0] = lo;
+            r[8] = hi;
         }
     }
 };
@@ -106,25 +121,24 @@ template <>
 struct Piece<true> {
     uint32_t lo, hi;      // codes of columns 8s .. 8s + 7 and 64 + 8s ..
     uint32_t s_lo, s_hi;  // f16 scales of the groups they lie in
-    __device__ __forceinline__ void load(const PagePools& c, int tensor, size_t row, size_t sc,
-                                         int s) {
-        const uint32_t* r = reinterpret_cast<const uint32_t*>(c.data[tensor] + row * kCodeBytes);
-        lo = r[s];
-        hi = r[8 + s];
-        s_lo = c.scales[tensor][sc + s / 4];
-        s_hi = c.scales[tensor][sc + 2 + s / 4];
+    __device__ __forceinline__ void load(const PageRows& c, uint32_t row, uint32_t sc, int s) {
+        const uint32_t* r = reinterpret_cast<const uint32_t*>(c.data) + row * 16 + s;
+        lo = r[0];
+        hi = r[8];
+        s_lo = c.scales[sc * kRowScales + s / 4];
+        s_hi = c.scales[sc * kRowScales + 2 + s / 4];
     }
     // Every lane of the warp calls it; `live` lanes store.
-    __device__ __forceinline__ void store(const PagePools& c, int tensor, size_t row, size_t sc,
-                                          int s, bool live) const {
+    __device__ __forceinline__ void store(const PageRows& c, uint32_t row, uint32_t sc, int s,
+                                          bool live) const {
         const uint32_t a = __shfl_xor_sync(0xffffffffu, s_lo, 4);
         const uint32_t b = __shfl_xor_sync(0xffffffffu, s_hi, 4);
         if (live) {
-            uint32_t* r = reinterpret_cast<uint32_t*>(c.data[tensor] + row * kCodeBytes);
-            r[s] = lo;
-            r[8 + s] = hi;
+            uint32_t* r = reinterpret_cast<uint32_t*>(c.data) + row * 16 + s;
+            r[0] = lo;
+            r[8] = hi;
             if (s == 0)
-                *reinterpret_cast<uint2*>(c.scales[tensor] + sc) =
+                *reinterpret_cast<uint2*>(c.scales + sc * kRowScales) =
                     make_uint2(s_lo | (a << 16), s_hi | (b << 16));
         }
     }
@@ -164,31 +178,34 @@ __global__ void __launch_bounds__(kThreads) convert_pages_kernel(const __grid_co
     const int s = threadIdx.x & 7;
     const int page_rows = p.page_size * p.H;
     const int slice = blockIdx.x >> 1, tensor = blockIdx.x & 1;
-    // counting in the destination's order: (token, head) or (head, token)
+    // Rows are counted in the destination's order, (token, head) or (head,
+    // token); `inner` counts the second.
     const uint32_t inner = p.dst.layout == 0 ? p.H : p.page_size;
+    const uint32_t outer = p.dst.layout == 0 ? p.page_size : p.H;
     for (int i = blockIdx.y; i < p.n; i += gridDim.y) {
         int src, dst;
         if (!pair_pages(p, i, blockIdx.x == 0, &src, &dst)) continue;
+        const PageRows from = page_rows_of<kSrc4>(p.src, tensor, src, page_rows);
+        const PageRows to = page_rows_of<kDst4>(p.dst, tensor, dst, page_rows);
         Piece<kSrc4> a[kRows];
-        size_t to[kRows], to_s[kRows];
+        uint32_t row[kRows], sc[kRows];
         bool live[kRows];
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
             const int r = slice * kSliceRows + j * (kThreads / 8) + (threadIdx.x >> 3);
             live[j] = r < page_rows;
-            const uint32_t rr = live[j] ? r : 0;
-            const uint32_t hi = rr / inner, lo = rr - hi * inner;
-            const int t = p.dst.layout == 0 ? hi : lo, h = p.dst.layout == 0 ? lo : hi;
-            a[j].load(p.src, tensor, row_index(p.src.layout, src, t, h, p.H, p.page_size),
-                      scale_index(src, t, h, p.H, p.page_size), s);
-            to[j] = row_index(p.dst.layout, dst, t, h, p.H, p.page_size);
-            to_s[j] = scale_index(dst, t, h, p.H, p.page_size);
+            row[j] = live[j] ? r : 0;
+            uint32_t hi = row[j];
+            if (inner > 1) hi = p.inner_magic ? __umulhi(row[j], p.inner_magic) : row[j] / inner;
+            const uint32_t other = (row[j] - hi * inner) * outer + hi;  // in the other order
+            sc[j] = p.dst.layout == 0 ? other : row[j];
+            a[j].load(from, p.src.layout == p.dst.layout ? row[j] : other, sc[j], s);
         }
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
             Piece<kDst4> b;
             convert(a[j], b);
-            b.store(p.dst, tensor, to[j], to_s[j], s, live[j]);
+            b.store(to, row[j], sc[j], s, live[j]);
         }
     }
 }

@@ -70,7 +70,8 @@ oxd_status axes_append(const oxd_axes_append_desc* desc, const void* q, const vo
     if (d.head_dim != kHeadDim || !page_size_ok(d.page_size)) return OXD_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(d.num_tokens) *
             (static_cast<int64_t>(d.num_qo_heads) + d.num_kv_heads) > (int64_t{1} << 33) ||
-        d.num_pages >= (int64_t{1} << 31))
+        d.num_pages >= (int64_t{1} << 31) || d.num_qo_heads > (1 << 20) ||
+        d.num_kv_heads > (1 << 20))
         return OXD_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
         !pools_aligned(pools) || !aligned(token_request, 4) || !aligned(positions, 4) ||
@@ -243,6 +244,11 @@ extern "C" oxd_status oxd_copy_pages(const oxd_copy_pages_desc* desc, const oxd_
     p.n = d.num_pairs;
     p.H = d.num_kv_heads;
     p.page_size = d.page_size;
+    // n / inner = the high word of n * magic for n < page_size * H, where that
+    // many times inner stays below 2^32
+    const uint64_t inner = d.dst_layout == OXD_LAYOUT_NHD ? d.num_kv_heads : d.page_size;
+    if (inner > 1 && static_cast<uint64_t>(d.num_kv_heads) * d.page_size * inner < (uint64_t{1} << 32))
+        p.inner_magic = static_cast<uint32_t>((uint64_t{1} << 32) / inner + 1);
     if (launch_copy_pages(p, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return OXD_ERR_CUDA;
     return OXD_OK;
