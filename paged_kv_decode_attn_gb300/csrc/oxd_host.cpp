@@ -352,7 +352,12 @@ oxd_status plan_decode(const oxd_paged_decode_desc* desc, const int32_t* indptr,
     // Streams per request and query rows per stream: one KV head each, but in a
     // 4-bit NHD cache, where a head's codes of a token are half a 128-byte line,
     // two (for an even number of heads), so that whole lines are read at once.
-    const int heads = quant && d.layout == OXD_LAYOUT_NHD && d.num_kv_heads % 2 == 0 ? 2 : 1;
+    // Below 512 tokens a resident CTA a call is short enough that the streams'
+    // number counts for more than the bytes.
+    const bool pairs = quant && d.layout == OXD_LAYOUT_NHD && d.num_kv_heads % 2 == 0 &&
+                       total_tokens * d.num_kv_heads >=
+                           int64_t{512} * num_sms * ctas_per_sm;
+    const int heads = pairs ? 2 : 1;
     const int H = d.num_kv_heads / heads;
     const int R = G * heads;
     const int prefix_pages = d.shared_prefix_tokens / ps;  // 0 without cascade
@@ -445,8 +450,12 @@ oxd_status plan_decode(const oxd_paged_decode_desc* desc, const int32_t* indptr,
         const int64_t line_grid = std::max<int64_t>(
             1, std::min<int64_t>(resident, std::max<int64_t>(streamed * H / stage_tokens, live)));
         const double share = static_cast<double>(streamed) * H / line_grid;
-        whole_streams = live <= resident && longest <= 2 * stage_tokens &&
-                        static_cast<double>(longest) <= share + 160.0;
+        // 4-bit: a stage of a lone CTA takes about 0.45 us and the merge launch
+        // 3.5, so a longest stream up to seven stages above the share runs whole.
+        whole_streams =
+            live <= resident &&
+            (quant ? static_cast<double>(longest) <= share + 7.0 * stage_tokens
+                   : longest <= 2 * stage_tokens && static_cast<double>(longest) <= share + 160.0);
         const int64_t n_streams = static_cast<int64_t>(B) * H;
         if (!whole_streams && prefix_pages == 0 && n_streams <= 64 &&
             (variant == kVariantFmaG1 || variant == kVariantFmaG2 || variant == kVariantMma8)) {

@@ -285,3 +285,33 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_run_is_right(G):
     assert (guard[0] == 7).all() and (guard[-1] == 7).all()
     assert run() == 0
     assert torch.equal(guard, out) and torch.equal(lse, l0)
+
+
+@pytest.mark.parametrize("G,Hkv,layout", [(1, 8, "NHD"), (4, 2, "HND"), (8, 3, "NHD")])
+def test_any_workspace_contents_and_two_plans_on_one(G, Hkv, layout):
+    """Split streams, whatever the workspace held before, replayed from an unbound capture, and with
+    another plan's run on the same workspace in between."""
+    c = Cache([512, 900, 64, 130], G, Hkv, 16, layout, seed=23)
+    plan, other = c.plan(force_splits=4), c.plan(force_splits=3)
+    ref = c.reference()
+    g = torch.Generator(device="cuda").manual_seed(2)
+    n = max(plan.workspace_bytes, other.workspace_bytes)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for fill in (torch.zeros(n, dtype=torch.uint8, device="cuda"),
+                 torch.randint(0, 256, (n,), dtype=torch.uint8, device="cuda", generator=g)):
+        ws.copy_(fill)
+        out, lse, _ = c.run(plan, ws=ws)
+        assert oxd.oxd_read_device_status(ws) == 0
+        assert_decode(out, lse, ref)
+        first, l0 = out.clone(), lse.clone()
+        c.run(other, ws=ws)
+        c.run(plan, ws=ws, out=out, lse=lse)
+        assert torch.equal(out, first) and torch.equal(lse, l0)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        c.run(plan, ws=ws, out=out, lse=lse)
+    for _ in range(5):
+        out.zero_(), lse.zero_()
+        graph.replay()
+        assert torch.equal(out, first) and torch.equal(lse, l0)
