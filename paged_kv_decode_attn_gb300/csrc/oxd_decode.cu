@@ -550,23 +550,6 @@ struct Smem {
 
 // ------------------------------------------------------------------ the kernel
 
-// Address in cluster rank 0 of the same shared-memory location.
-__device__ __forceinline__ uint32_t map_rank0(uint32_t local) {
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(local));
-    return remote;
-}
-
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x),
-                 "f"(v.y), "f"(v.z), "f"(v.w)
-                 : "memory");
-}
-
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
 // Rank 0 of a cluster merges row g of the cluster's n pieces from its own
 // shared memory (every lane holds all n log2-sums, so no shuffles): the
 // state merge of the "Single decode split-K" row, with natural-log weights

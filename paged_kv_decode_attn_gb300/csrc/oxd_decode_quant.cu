@@ -27,7 +27,8 @@
 //     the largest weight.
 // A unit's warp states are merged through the chunks the warps last read;
 // split streams leave F32 partial states for the merge kernel, as in the bf16
-// decode.
+// decode; a small batch is launched as clusters, one stream a cluster, whose
+// first CTA merges the pieces' states from its shared memory.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -77,6 +78,11 @@ struct QCfg {
     static constexpr int kFlagOff = kRedOff + 2 * kWarps * 8 * 4;  // dump offset of each warp, units
     static constexpr int kListOff = kFlagOff + 32;
     static constexpr int kSmemBytes = kListOff + kListed * 32;
+    // A cluster launch adds the pieces' states in rank 0: [rank][kRows][128]
+    // f32 values, then [rank][kRows] log2-sums.
+    static constexpr int kClusterOff = (kSmemBytes + 15) / 16 * 16;
+    static constexpr int kClusterSums = kClusterOff + kMaxClusterCtas * kRows * kHeadDim * 4;
+    static constexpr int kSmemBytesCluster = kClusterSums + kMaxClusterCtas * kRows * 4;
     static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "the CTAs fit a SM");
 };
 template <int kPs> using CfgQ8 = QCfg<1, 2, 4, kPs>;
@@ -571,7 +577,9 @@ __device__ __forceinline__ void convert_query(const QuantDecodeParams& qp, uint8
     }
 }
 
-template <class C, class WL>
+// kCluster: launched as clusters of p.cluster_c CTAs, one unit each (an
+// instantiation of its own, so its code does not weigh on the others).
+template <class C, class WL, bool kCluster>
 __global__ void __launch_bounds__(kThreads, C::kCtas)
     quant_decode_kernel(const __grid_constant__ QuantDecodeParams qp,
                         const __grid_constant__ WL work) {
@@ -588,6 +596,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         mbar_init(q_bar, 1);
         fence_mbar_init();
     }
+    if constexpr (kCluster) cluster_arrive();  // (rank 0 is there once all have)
     // as a programmatic dependent: nothing in global memory before this
     grid_dependency_wait();
     // This CTA's units, from the parameter buffer or the workspace. Their range
@@ -605,8 +614,10 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
             listed = true;
         }
     }
+    int4 it0 = make_int4(0, 0, 0, 0);  // the first unit, beside the range
     if (!listed) {
         const int4 r = __ldg(p.cta_rec + 2 * blockIdx.x);
+        it0 = __ldg(p.cta_rec + 2 * blockIdx.x + 1);
         a = r.x;
         b = r.y;
     }
@@ -629,13 +640,13 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     int4 own_it = make_int4(0, 0, 0, 0);
     const bool have = threadIdx.x < kListed && static_cast<int>(threadIdx.x) < b - a;
     if (have) {
-        own_it = list[a + threadIdx.x];
+        own_it = threadIdx.x == 0 && !listed ? it0 : list[a + threadIdx.x];
         own = decode_unit(qp, own_it);
         shared_list[threadIdx.x] = own;
     }
     __syncthreads();
     const int u_begin = range[0], u_end = range[1];
-    if (u_begin >= u_end) return;
+    if (!kCluster && u_begin >= u_end) return;
     const UnitList units{shared_list, list, u_begin};
 
     uint8_t* ring = base + warp * C::kStages * C::kSlotBytes;
@@ -686,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     __syncthreads();
     copy_query(u_begin + 1);
 
+    if constexpr (kCluster) cluster_wait();
     State<C> st;
     st.set_lane(lane);
     const uint32_t q_addr = smem_addr(base) + C::kQOff + in.head * C::kQHeadBytes;
@@ -770,6 +782,14 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
                     *reinterpret_cast<uint2*>(p.out + row * kHeadDim + lane * 4) = v;
                     if (p.lse != nullptr) lse = p.lse + row;
                     to_lse = kLn2;
+                } else if constexpr (kCluster) {
+                    const int rank = static_cast<int>(cluster_ctarank());
+                    const uint32_t at_row = rank * C::kRows + n * 8 + r;
+                    st_cluster_v4(map_rank0(smem_addr(base) + C::kClusterOff +
+                                            (at_row * kHeadDim + lane * 4) * 4), o);
+                    if (lane == 0)
+                        st_cluster_f32(map_rank0(smem_addr(base) + C::kClusterSums + at_row * 4),
+                                       L != 0.f ? M - kPOffset + __log2f(L) : -INFINITY);
                 } else {
                     // partial states are [slot][heads * G][128]
                     const size_t row = static_cast<size_t>(u.slot) * G * qp.heads + row_in_unit;
@@ -787,9 +807,53 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
             in.refill(qp, units, ring_addr + held * C::kSlotBytes, dst, sdst, lane);
     }
     cp_async_wait<0>();
+    if constexpr (kCluster) {
+        // Every piece's state is in rank 0 now (a piece that is not a unit of
+        // this plan weighs nothing), which merges them, a warp a row.
+        const Unit u = u_begin < u_end ? units.get(qp, u_begin) : Unit{};
+        if (u.n_chunks == 0 && threadIdx.x < C::kRows)
+            st_cluster_f32(map_rank0(smem_addr(base) + C::kClusterSums +
+                                     (cluster_ctarank() * C::kRows + threadIdx.x) * 4),
+                           -INFINITY);
+        cluster_arrive();
+        cluster_wait();
+        if (cluster_ctarank() != 0 || u.n_chunks == 0) return;
+        const float* sums = reinterpret_cast<const float*>(base + C::kClusterSums);
+        const float* vals = reinterpret_cast<const float*>(base + C::kClusterOff);
+        for (int r = warp; r < G; r += kWarps) {
+            float sv[kMaxClusterCtas], M = -INFINITY, W = 0.f;
+#pragma unroll
+            for (int i = 0; i < kMaxClusterCtas; ++i) {
+                sv[i] = i < p.cluster_c ? sums[i * C::kRows + r] : -INFINITY;
+                M = fmaxf(M, sv[i]);
+            }
+            const float mu = M == -INFINITY ? 0.f : M;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kMaxClusterCtas; ++i) {
+                if (sv[i] == -INFINITY) continue;
+                const float f = fast_exp2(sv[i] - mu);
+                const float4 v = *reinterpret_cast<const float4*>(
+                    vals + (i * C::kRows + r) * kHeadDim + lane * 4);
+                W += f;
+                o.x = fmaf(v.x, f, o.x);
+                o.y = fmaf(v.y, f, o.y);
+                o.z = fmaf(v.z, f, o.z);
+                o.w = fmaf(v.w, f, o.w);
+            }
+            const float inv = W != 0.f ? __fdividef(1.f, W) : 0.f;
+            const size_t row = static_cast<size_t>(u.b) * p.num_qo_heads + u.h * G + r;
+            uint2 v;
+            v.x = pack_bf16x2(o.x * inv, o.y * inv);
+            v.y = pack_bf16x2(o.z * inv, o.w * inv);
+            *reinterpret_cast<uint2*>(p.out + row * kHeadDim + lane * 4) = v;
+            if (lane == 0 && p.lse != nullptr)
+                p.lse[row] = W != 0.f ? (M + __log2f(W)) * kLn2 : -INFINITY;
+        }
+    }
 }
 
-template <class C, class WL>
+template <class C, class WL, bool kCluster>
 cudaError_t ensure_smem() {
     static std::atomic<uint64_t> done{0};
     int dev = 0;
@@ -797,35 +861,57 @@ cudaError_t ensure_smem() {
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
     if (bit != 0 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-    e = cudaFuncSetAttribute(quant_decode_kernel<C, WL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::kSmemBytes);
+    e = cudaFuncSetAttribute(quant_decode_kernel<C, WL, kCluster>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kCluster ? C::kSmemBytesCluster : C::kSmemBytes);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
 }
 
-template <class C, class WL>
+template <class C, class WL, bool kCluster>
 cudaError_t launch_ex(const QuantDecodeParams& p, const WL& w, int grid, cudaStream_t stream,
                       bool pdl) {
-    const cudaError_t e = ensure_smem<C, WL>();
+    const cudaError_t e = ensure_smem<C, WL, kCluster>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.dynamicSmemBytes = kCluster ? C::kSmemBytesCluster : C::kSmemBytes;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if constexpr (kCluster) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(p.d.cluster_c);
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, quant_decode_kernel<C, WL>, p, w);
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, quant_decode_kernel<C, WL, kCluster>, p, w);
 }
 
 template <class C>
 cudaError_t launch(const QuantDecodeParams& p, const WorkList* w, int grid, cudaStream_t stream,
                    bool pdl) {
-    if (w != nullptr) return launch_ex<C>(p, *w, grid, stream, pdl);
-    return launch_ex<C>(p, NoList{0}, grid, stream, pdl);
+    if (p.d.cluster_c > 1) {
+        if constexpr (C::kNT != 1) {
+            return cudaErrorInvalidValue;  // clusters: groups of up to 8 heads
+        } else {
+            if (grid % p.d.cluster_c != 0 || p.d.cluster_c > kMaxClusterCtas || p.heads != 1)
+                return cudaErrorInvalidValue;
+            if (w != nullptr) return launch_ex<C, WorkList, true>(p, *w, grid, stream, pdl);
+            return launch_ex<C, NoList, true>(p, NoList{0}, grid, stream, pdl);
+        }
+    }
+    if (w != nullptr) return launch_ex<C, WorkList, false>(p, *w, grid, stream, pdl);
+    return launch_ex<C, NoList, false>(p, NoList{0}, grid, stream, pdl);
 }
 
 template <template <int> class C>
@@ -842,10 +928,10 @@ cudaError_t launch_ps(const QuantDecodeParams& p, const WorkList* w, int grid, c
 
 template <class C>
 cudaError_t occupancy(int* n) {
-    const cudaError_t e = ensure_smem<C, WorkList>();
+    const cudaError_t e = ensure_smem<C, WorkList, false>();
     if (e != cudaSuccess) return e;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, quant_decode_kernel<C, WorkList>,
-                                                         kThreads, C::kSmemBytes);
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+        n, quant_decode_kernel<C, WorkList, false>, kThreads, C::kSmemBytes);
 }
 
 template <class C>

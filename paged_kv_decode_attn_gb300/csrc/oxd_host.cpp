@@ -457,6 +457,18 @@ oxd_status plan_decode(const oxd_paged_decode_desc* desc, const int32_t* indptr,
             (quant ? static_cast<double>(longest) <= share + 7.0 * stage_tokens
                    : longest <= 2 * stage_tokens && static_cast<double>(longest) <= share + 160.0);
         const int64_t n_streams = static_cast<int64_t>(B) * H;
+        // 4-bit: a stage takes a lone CTA 1.3 us (a warp's chunk from load to
+        // product), a cluster's merge about one, so pieces of one stage.
+        if (quant && variant == kVariantQuant8 && heads == 1 && n_streams <= 64 &&
+            longest > stage_tokens) {
+            const int C = static_cast<int>(
+                std::min<int64_t>({kMaxClusterCtas, min_pages, resident / n_streams,
+                                   (longest + stage_tokens - 1) / stage_tokens}));
+            if (C >= 2 && (longest + C - 1) / C <= 4 * stage_tokens) {
+                cluster_c = C;
+                whole_streams = false;
+            }
+        }
         if (!whole_streams && prefix_pages == 0 && n_streams <= 64 &&
             (variant == kVariantFmaG1 || variant == kVariantFmaG2 || variant == kVariantMma8)) {
             const int C = static_cast<int>(

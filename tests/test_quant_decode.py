@@ -315,3 +315,22 @@ def test_any_workspace_contents_and_two_plans_on_one(G, Hkv, layout):
         out.zero_(), lse.zero_()
         graph.replay()
         assert torch.equal(out, first) and torch.equal(lse, l0)
+
+
+@pytest.mark.parametrize("G,Hkv", [(1, 8), (2, 4), (5, 3), (8, 1)])
+@pytest.mark.parametrize("lengths", [[512], [129], [4000], [300, 1000, 77, 130], [2048] * 3, [200] * 8])
+def test_small_batches_in_one_launch(G, Hkv, lengths):
+    """Streams cut into pieces that a cluster's first CTA merges, or run whole."""
+    for layout in ("NHD", "HND"):
+        c = Cache(lengths, G, Hkv, 16, layout, seed=25)
+        plan, out, lse = check(c)
+        assert plan.info.launches_per_run == 1 or max(lengths) > 2048
+        ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+        oxd.oxd_plan_bind_workspace(plan, ws)
+        for _ in range(5):
+            o2, l2, _ = c.run(plan, ws=ws)
+            assert torch.equal(out, o2) and torch.equal(lse, l2)
+        ws.zero_()  # the binding is gone: nothing is computed, and that is said
+        keep = torch.full_like(out, 3.0)
+        c.run(plan, ws=ws, out=keep)
+        assert oxd.oxd_read_device_status(ws) == 2 and (keep == 3).all()
