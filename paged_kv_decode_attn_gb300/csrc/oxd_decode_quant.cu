@@ -1,4 +1,5 @@
-// Decode attention over a 4-bit paged cache for sm_103a (oxd_quant_decode_run).
+// Decode attention over a 4-bit paged cache for sm_103a (oxd_quant_decode_run),
+// groups of up to 8 query heads (oxd_decode_quant_wide.cu: larger ones).
 //
 // For every query row q of a group and the tokens t of its request
 //   x_t = sm_scale * sum_c ks[t,c] (q_c . e2m1(kc[t,c])),  c the four groups of 32
@@ -34,40 +35,33 @@
 #include <atomic>
 #include <type_traits>
 
-#include "oxd_e2m1.cuh"
-#include "oxd_internal.h"
-#include "oxd_ptx.cuh"
+#include "oxd_decode_quant.cuh"
 
 namespace oxd {
 namespace {
 
-constexpr float kLazy = 4.f;     // log2: how far a score may pass the running maximum
-constexpr float kPOffset = 10.f; // log2 of the weight a score at the running maximum gets
-
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kChunk = 32;  // tokens a warp takes at a time
 
-constexpr int kListed = 32;  // of a CTA's units, the ones held decoded in shared memory
-
-// kNT: 8-head tiles a warp holds. kCtas: resident CTAs a SM, which caps the
-// registers at 65536 / (kThreads * kCtas). kPs: page size.
-template <int kNT_, int kStages_, int kCtas_, int kPs_>
+template <int kPs>  // page size
 struct QCfg {
-    static constexpr int kNT = kNT_;
-    static constexpr int kRows = 8 * kNT;
-    static constexpr int kStages = kStages_;
-    static constexpr int kCtas = kCtas_;
-    static constexpr int kPs = kPs_;
-    static constexpr int kPagesPerChunk = kPs < kQuantChunk ? kQuantChunk / kPs : 1;
+    static constexpr int kRows = 8;    // query heads: one N tile
+    static constexpr int kStages = 2;  // slots of a warp's ring
+    // Resident CTAs a SM, which caps the registers at 128. (Three with 168
+    // registers and longer rings: the same steady rate, slower short streams.)
+    static constexpr int kCtas = 4;
+    static constexpr int kPageSize = kPs;
+    static constexpr int kPagesPerChunk = kPs < kChunk ? kChunk / kPs : 1;
     static constexpr int kRun = 32 / kPagesPerChunk;  // chunks whose pages a window of 32 holds
     // slot: K codes | V codes | K scales | V scales of 32 tokens. 16-byte piece
     // i of a token's codes sits at piece i ^ (token / 2 % 4).
-    static constexpr int kVOff = kQuantChunk * kCodeBytes;
+    static constexpr int kVOff = kChunk * kCodeBytes;
     static constexpr int kKsOff = 2 * kVOff;
-    static constexpr int kVsOff = kKsOff + kQuantChunk * kScaleBytes;
-    static constexpr int kSlotBytes = kVsOff + kQuantChunk * kScaleBytes;
+    static constexpr int kVsOff = kKsOff + kChunk * kScaleBytes;
+    static constexpr int kSlotBytes = kVsOff + kChunk * kScaleBytes;
     static_assert(8 * kHeadDim * 4 <= kSlotBytes, "a dumped 8-row state fits a slot");
-    // query fragments of up to two heads: [head][group c][tile][lane] 16 bytes,
+    // query fragments of up to two heads: [head][group c][lane] 16 bytes,
     // and the next unit's query rows as they come from memory
     static constexpr int kQOff = kWarps * kStages * kSlotBytes;
     static constexpr int kQHeadBytes = kRows * kHeadDim * 2;
@@ -85,135 +79,13 @@ struct QCfg {
     static constexpr int kSmemBytesCluster = kClusterSums + kMaxClusterCtas * kRows * 4;
     static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "the CTAs fit a SM");
 };
-template <int kPs> using CfgQ8 = QCfg<1, 2, 4, kPs>;
-template <int kPs> using CfgQ16 = QCfg<2, 3, 3, kPs>;
-template <int kPs> using CfgQ32 = QCfg<4, 4, 2, kPs>;
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int kPending>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
-}
-
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr));
-    return v;
-}
-
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-    return v;
-}
-
-__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-    return v;
-}
-
-// D = A * B + D, m16n8k16, f16 inputs, f32 accumulate.
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// D = A * B.
-__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-
-__device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
-    uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-    __half2 v = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-    return *reinterpret_cast<uint32_t*>(&v);
-}
 
 // Token of MMA row r (0..7) of an 8-token block: 2 <-> 3 and 6 <-> 7 trade
 // places, so the four V rows that a quarter of a warp reads at once lie in
 // different banks.
 __device__ __forceinline__ int row_token(int r) { return r ^ ((r >> 1) & 1); }
 
-// A work unit, checked against the plan: no chunks if it is not one of it.
-struct Unit {
-    int first;     // offset of its first page in `indices`
-    int n_pages;
-    int valid;     // tokens
-    int n_chunks;
-    int b, h, slot, reserved;
-};
-static_assert(sizeof(Unit) == 32, "two 16-byte loads");
-
-__device__ __forceinline__ Unit decode_unit(const QuantDecodeParams& qp, const int4 it) {
-    const DecodeParams& p = qp.d;
-    Unit u;
-    u.first = it.x;
-    u.n_pages = it.y & ((1 << kUnitPagesBits) - 1);
-    const int last_len = (it.y >> kUnitPagesBits) & 0x7f;  // 0: not the request's last page
-    u.b = it.z & ((1 << kUnitBBits) - 1);
-    u.h = static_cast<int>(static_cast<uint32_t>(it.z) >> (kUnitBBits + 1)) * qp.heads;
-    u.slot = it.w;
-    u.reserved = 0;
-    const bool ok = u.n_pages >= 1 && it.x >= 0 &&
-                    static_cast<int64_t>(it.x) + u.n_pages <= p.nnz && u.b < p.batch &&
-                    u.h + qp.heads <= p.num_kv_heads && it.w >= -1 && it.w < p.n_slots &&
-                    last_len <= p.page_size;
-    u.valid = last_len ? (u.n_pages - 1) * p.page_size + last_len : u.n_pages * p.page_size;
-    u.n_chunks = ok ? (u.valid + kQuantChunk - 1) / kQuantChunk : 0;
-    return u;
-}
-
-// Whether the device's block tables say what the unit's plan was made from.
-__device__ __forceinline__ bool tables_match(const DecodeParams& p, const Unit& u, const int4 it) {
-    const int last_len = (it.y >> kUnitPagesBits) & 0x7f;
-    return u.n_chunks > 0 && (it.y >= 0 || p.indptr[u.b] == u.first) &&
-           (last_len == 0 || (p.indptr[u.b + 1] == u.first + u.n_pages &&
-                              p.last_page_len[u.b] == last_len));
-}
-
-// A CTA's units: the first kListed decoded in shared memory, others from the list.
-struct UnitList {
-    const Unit* shared;
-    const int4* list;
-    int first;
-    __device__ __forceinline__ Unit get(const QuantDecodeParams& qp, int i) const {
-        if (i - first < kListed) return shared[i - first];
-        return decode_unit(qp, __ldg(list + i));
-    }
-};
+using List = UnitList<true>;
 
 // One warp's stream of chunks: the refilling side, up to kStages chunks ahead
 // of the consuming one. The warp takes every fourth chunk of a unit (every
@@ -240,7 +112,7 @@ struct Stream {
     __device__ __forceinline__ int load_window(const int32_t* indices, int x_first, int x_chunks,
                                                int x_pages, int c0, int lane) const {
         const int cc = c0 + ((lane / C::kPagesPerChunk) << wl2);
-        const int pg = cc * kQuantChunk / C::kPs + lane % C::kPagesPerChunk;
+        const int pg = cc * kChunk / C::kPageSize + lane % C::kPagesPerChunk;
         return cc < x_chunks && pg < x_pages ? __ldg(indices + x_first + pg) : 0;
     }
     // An index outside the pool is recorded and replaced by page 0.
@@ -251,36 +123,36 @@ struct Stream {
         return bad ? 0 : i;
     }
     // Enters `unit`, whose first indices are in nx_win.
-    __device__ __forceinline__ void enter(const QuantDecodeParams& qp, const UnitList& units,
+    __device__ __forceinline__ void enter(const QuantDecodeParams& qp, const List& units,
                                           int lane) {
         const DecodeParams& p = qp.d;
         const Unit u = units.get(qp, unit);
         n_pages = u.n_pages;
-        n_chunks = u.n_chunks;
+        n_chunks = (u.valid + kChunk - 1) / kChunk;
         first = u.first;
         c = win_c = w;
-        const int h = u.n_chunks > 0 ? u.h + head : 0;
-        const size_t row = row_index(p.layout, 0, (lane >> 2) % C::kPs, h, p.num_kv_heads, C::kPs);
+        const int h = u.valid > 0 ? u.h + head : 0;
+        const size_t row = row_index(p.layout, 0, (lane >> 2) % C::kPageSize, h, p.num_kv_heads, C::kPageSize);
         k = qp.k_codes + row * kCodeBytes + (lane & 3) * 16;
         v = qp.v_codes + row * kCodeBytes + (lane & 3) * 16;
-        const int st = 2 * (lane & 15) % C::kPs;
+        const int st = 2 * (lane & 15) % C::kPageSize;
         sc = reinterpret_cast<const uint8_t*>((lane < 16 ? qp.k_scales : qp.v_scales) +
-                                              scale_index(0, st, h, p.num_kv_heads, C::kPs));
+                                              scale_index(0, st, h, p.num_kv_heads, C::kPageSize));
         win = check(p, nx_win, lane);
         ahead = load_window(p.indices, first, n_chunks, n_pages, w + (C::kRun << wl2), lane);
         load_next_window(qp, units, lane);
     }
     __device__ __forceinline__ void load_next_window(const QuantDecodeParams& qp,
-                                                     const UnitList& units, int lane) {
+                                                     const List& units, int lane) {
         if (unit + 1 < u_end) {
             const Unit x = units.get(qp, unit + 1);
-            nx_win = load_window(qp.d.indices, x.first, x.n_chunks, x.n_pages, w, lane);
+            nx_win = load_window(qp.d.indices, x.first, (x.valid + kChunk - 1) / kChunk, x.n_pages, w, lane);
         }
     }
     // Issues the next chunk's copies into `slot`, if there is one; always one
     // more copy group. `slot` is the shared address, dst / sdst this lane's
     // offsets in it. Pages past the unit's last are read as page 0.
-    __device__ __forceinline__ void refill(const QuantDecodeParams& qp, const UnitList& units,
+    __device__ __forceinline__ void refill(const QuantDecodeParams& qp, const List& units,
                                            uint32_t slot, uint32_t dst, uint32_t sdst,
                                            int lane) {
         const DecodeParams& p = qp.d;
@@ -297,18 +169,18 @@ struct Stream {
             const int w0 = ((c - win_c) >> wl2) * C::kPagesPerChunk;
             // bytes of one token and of a page
             const uint32_t tok = p.layout == 0 ? p.num_kv_heads * kCodeBytes : kCodeBytes;
-            const uint32_t page_bytes = p.num_kv_heads * (C::kPs * kCodeBytes);
-            const uint32_t half = C::kPs > kQuantChunk ? (c & 1) * kQuantChunk : 0;
+            const uint32_t page_bytes = p.num_kv_heads * (C::kPageSize * kCodeBytes);
+            const uint32_t half = C::kPageSize > kChunk ? (c & 1) * kChunk : 0;
 #pragma unroll
-            for (int i = 0; i < kQuantChunk / 8; ++i) {  // eight tokens of K and of V
-                const uint32_t page = __shfl_sync(0xffffffffu, win, w0 + i * 8 / C::kPs);
+            for (int i = 0; i < kChunk / 8; ++i) {  // eight tokens of K and of V
+                const uint32_t page = __shfl_sync(0xffffffffu, win, w0 + i * 8 / C::kPageSize);
                 const size_t off = static_cast<size_t>(page) * page_bytes +
-                                   (half + i * 8 % C::kPs) * tok;
+                                   (half + i * 8 % C::kPageSize) * tok;
                 cp_async16(slot + dst + i * 8 * kCodeBytes, k + off);
                 cp_async16(slot + dst + C::kVOff + i * 8 * kCodeBytes, v + off);
             }
             const uint32_t page =
-                __shfl_sync(0xffffffffu, win, w0 + 2 * (lane & 15) / C::kPs);
+                __shfl_sync(0xffffffffu, win, w0 + 2 * (lane & 15) / C::kPageSize);
             cp_async16(slot + sdst, sc + static_cast<size_t>(page) * (page_bytes / 8) +
                                         half * kScaleBytes);
             c += 1 << wl2;
@@ -319,10 +191,10 @@ struct Stream {
 
 template <class C>
 struct State {
-    uint32_t q;                // this lane's query fragments: [group c][tile] 512 bytes apart
-    float sc[C::kNT][2];       // logit scale (log2) of heads 2 tq, 2 tq + 1, positive
-    float m[C::kNT][2], l[C::kNT][2];
-    float acc[C::kNT][8][4];
+    uint32_t q;   // this lane's query fragments, 512 bytes from group to group
+    float sc[2];  // logit scale (log2) of heads 2 tq, 2 tq + 1, positive
+    float mu[2], l[2];  // mu: 10 - the running maximum (inf: none yet)
+    float acc[8][4];
     // This lane's offsets in a slot: its ldmatrix row and 16-byte chunk (chunk
     // c + 2 is 32 bytes away in the XOR), its K scales, and the codes and
     // scales of its two V tokens of an 8-token block. Eight tokens on, the
@@ -345,17 +217,14 @@ struct State {
     // q_addr, sc_row: the head's fragments and logit scales in shared memory.
     __device__ __forceinline__ void init(uint32_t q_addr, const float* sc_row, int lane) {
         q = q_addr + lane * 16;
+        const float2 f = *reinterpret_cast<const float2*>(sc_row + 2 * (lane & 3));
+        sc[0] = f.x;
+        sc[1] = f.y;
+        mu[0] = mu[1] = INFINITY;
+        l[0] = l[1] = 0.f;
 #pragma unroll
-        for (int n = 0; n < C::kNT; ++n) {
-            const float2 f = *reinterpret_cast<const float2*>(sc_row + n * 8 + 2 * (lane & 3));
-            sc[n][0] = f.x;
-            sc[n][1] = f.y;
-            m[n][0] = m[n][1] = -INFINITY;
-            l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
-        }
+        for (int i = 0; i < 8; ++i)
+            acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     }
 
     // One chunk of 32 tokens at `chunk`, of which the first `left` are there.
@@ -364,7 +233,7 @@ struct State {
         const int tq = lane & 3;
         const int pg = row_token(lane >> 2);
         // ---- S^T = K Q^T
-        float s[2][C::kNT][4];
+        float s[2][4];
         uint2 ks[2][2];  // [token block][row g, g + 8]: the four groups' f16 scales
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
@@ -392,83 +261,72 @@ struct State {
                         f[tb][j] = cc ? two.y : two.x;
                     }
                 }
+                const uint4 qf = lds128(q + grp * 512);
 #pragma unroll
-                for (int n = 0; n < C::kNT; ++n) {
-                    const uint4 qf = lds128(q + (grp * C::kNT + n) * 512);
+                for (int tb = 0; tb < 2; ++tb) {
+                    float t[4];
+                    mma_f16_zero(t, a[tb][0], b[tb][0], a[tb][1], b[tb][1], qf.x, qf.y);
+                    mma_f16(t, a[tb][2], b[tb][2], a[tb][3], b[tb][3], qf.z, qf.w);
+                    if (grp == 0) {
 #pragma unroll
-                    for (int tb = 0; tb < 2; ++tb) {
-                        float t[4];
-                        mma_f16_zero(t, a[tb][0], b[tb][0], a[tb][1], b[tb][1], qf.x, qf.y);
-                        mma_f16(t, a[tb][2], b[tb][2], a[tb][3], b[tb][3], qf.z, qf.w);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            s[tb][n][e] = grp == 0 ? t[e] * f[tb][e >> 1]
-                                                   : fmaf(t[e], f[tb][e >> 1], s[tb][n][e]);
+                        for (int e = 0; e < 4; ++e) s[tb][e] = t[e] * f[tb][e >> 1];
+                    } else {
+                        fma_pair(s[tb][0], s[tb][1], t[0], t[1], f[tb][0]);
+                        fma_pair(s[tb][2], s[tb][3], t[2], t[3], f[tb][1]);
                     }
                 }
             }
         }
         // ---- online softmax in the log2 domain: score s counts as s * sc
         bool raise = false;
-        float mx[C::kNT][2];
+        float mx[2];
 #pragma unroll
-        for (int n = 0; n < C::kNT; ++n) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if constexpr (kPartial) {
-#pragma unroll
-                    for (int tb = 0; tb < 2; ++tb) {
-                        if (tb * 16 + pg >= left) s[tb][n][j] = -INFINITY;
-                        if (tb * 16 + 8 + pg >= left) s[tb][n][2 + j] = -INFINITY;
-                    }
-                }
-                mx[n][j] = fmaxf(fmaxf(s[0][n][j], s[0][n][2 + j]),
-                                 fmaxf(s[1][n][j], s[1][n][2 + j])) * sc[n][j];
-                raise = raise || mx[n][j] > m[n][j] + kLazy;
-            }
-        }
-        if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-            for (int n = 0; n < C::kNT; ++n) {
-                float al[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float x = mx[n][j];
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    const float mn = fmaxf(m[n][j], x);
-                    al[j] = mn == -INFINITY ? 1.f : fast_exp2(m[n][j] - mn);
-                    m[n][j] = mn;
-                    l[n][j] *= al[j];
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    acc[n][i][0] *= al[0];
-                    acc[n][i][1] *= al[1];
-                    acc[n][i][2] *= al[0];
-                    acc[n][i][3] *= al[1];
-                }
-            }
-        }
-        uint32_t pb[2][C::kNT][2];  // P^T fragments of the two 16-token blocks
-#pragma unroll
-        for (int n = 0; n < C::kNT; ++n) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float mu = m[n][j] == -INFINITY ? 0.f : kPOffset - m[n][j];
+        for (int j = 0; j < 2; ++j) {
+            if constexpr (kPartial) {
 #pragma unroll
                 for (int tb = 0; tb < 2; ++tb) {
-                    s[tb][n][j] = fast_exp2(fmaf(s[tb][n][j], sc[n][j], mu));
-                    s[tb][n][2 + j] = fast_exp2(fmaf(s[tb][n][2 + j], sc[n][j], mu));
+                    if (tb * 16 + pg >= left) s[tb][j] = -INFINITY;
+                    if (tb * 16 + 8 + pg >= left) s[tb][2 + j] = -INFINITY;
                 }
-                l[n][j] += (s[0][n][j] + s[0][n][2 + j]) + (s[1][n][j] + s[1][n][2 + j]);
+            }
+            mx[j] = fmaxf(fmaxf(s[0][j], s[0][2 + j]), fmaxf(s[1][j], s[1][2 + j]));
+            raise = raise || fmaf(mx[j], sc[j], mu[j]) > kPOffset + kLazy;
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+            float al[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float x = mx[j] * sc[j];
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                const float was = kPOffset - mu[j], m = fmaxf(was, x);
+                al[j] = m == -INFINITY ? 1.f : fast_exp2(was - m);
+                mu[j] = kPOffset - m;
+                l[j] *= al[j];
             }
 #pragma unroll
-            for (int tb = 0; tb < 2; ++tb) {
-                pb[tb][n][0] = transpose_8x8(pack_f16x2(s[tb][n][0], s[tb][n][1]));
-                pb[tb][n][1] = transpose_8x8(pack_f16x2(s[tb][n][2], s[tb][n][3]));
+            for (int i = 0; i < 8; ++i) {
+                acc[i][0] *= al[0];
+                acc[i][1] *= al[1];
+                acc[i][2] *= al[0];
+                acc[i][3] *= al[1];
             }
+        }
+        uint32_t pb[2][2];  // P^T fragments of the two 16-token blocks
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+            fma_pairs(s[tb][0], s[tb][1], s[tb][0], s[tb][1], sc[0], sc[1], mu[0], mu[1]);
+            fma_pairs(s[tb][2], s[tb][3], s[tb][2], s[tb][3], sc[0], sc[1], mu[0], mu[1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[tb][e] = fast_exp2(s[tb][e]);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) l[j] += (s[0][j] + s[0][2 + j]) + (s[1][j] + s[1][2 + j]);
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+            pb[tb][0] = transpose_8x8(pack_f16x2(s[tb][0], s[tb][1]));
+            pb[tb][1] = transpose_8x8(pack_f16x2(s[tb][2], s[tb][3]));
         }
         // ---- O^T += V^T P^T: a thread's A rows are columns 16 g .. 16 g + 15
 #pragma unroll
@@ -500,82 +358,37 @@ struct State {
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t f0 = mul_f16x2(a0[i], sa), f1 = mul_f16x2(a1[i], sa);
                     const uint32_t f2 = mul_f16x2(a2[i], sb), f3 = mul_f16x2(a3[i], sb);
-#pragma unroll
-                    for (int n = 0; n < C::kNT; ++n)
-                        mma_f16(acc[n][half * 4 + i], f0, f1, f2, f3, pb[tb][n][0], pb[tb][n][1]);
+                    mma_f16(acc[half * 4 + i], f0, f1, f2, f3, pb[tb][0], pb[tb][1]);
                 }
             }
         }
     }
 
-    // Rows 8 n .. 8 n + 7 of the accumulator as f32 [8][128] into `dump`
-    // (float4 columns XOR-swizzled by the row), their maxima and sums.
-    __device__ __forceinline__ void dump(int n, float* dump, float* red_m, float* red_l,
-                                         int lane) {
+    // The accumulator as f32 [8][128] into `dump` (float4 columns XOR-swizzled
+    // by the row), the rows' maxima and sums.
+    __device__ __forceinline__ void dump(float* dump, float* red_m, float* red_l, int lane) {
         const int g = lane >> 2, tq = lane & 3;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            float t = l[n][j];
+            float t = l[j];
             t += __shfl_xor_sync(0xffffffffu, t, 4);
             t += __shfl_xor_sync(0xffffffffu, t, 8);
             t += __shfl_xor_sync(0xffffffffu, t, 16);
             const int row = 2 * tq + j;
             if (g == 0) {
-                red_m[row] = m[n][j];
+                red_m[row] = kPOffset - mu[j];
                 red_l[row] = t;
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int col4 = (g * 4 + i) ^ (row & 7);
                 *reinterpret_cast<float4*>(dump + row * kHeadDim + col4 * 4) =
-                    make_float4(acc[n][2 * i][j], acc[n][2 * i][2 + j], acc[n][2 * i + 1][j],
-                                acc[n][2 * i + 1][2 + j]);
+                    make_float4(acc[2 * i][j], acc[2 * i][2 + j], acc[2 * i + 1][j],
+                                acc[2 * i + 1][2 + j]);
             }
         }
     }
 };
-
-// Turns a unit's query rows into f16 fragments: eight rows a pass, 16 threads a
-// row, a thread 8 columns (one lane's fragment of a group). A row is scaled by a
-// power of two so that its largest size lies in [1, 2) (f16's range); a negative
-// logit scale's sign goes into q, and a scale of zero becomes the smallest normal
-// number (logits below 2^-100), so a masked score of -inf stays one.
-template <class C>
-__device__ __forceinline__ void convert_query(const QuantDecodeParams& qp, uint8_t* base) {
-    float* sc = reinterpret_cast<float*>(base + C::kScOff);
-    const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
-    const int G = qp.d.group;
-    for (int i = 0; i < qp.heads * C::kNT; ++i) {
-        const int hd = i >= C::kNT ? 1 : 0, n = i - hd * C::kNT;
-        const int r = n * 8 + row;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < G)
-            x = *reinterpret_cast<const uint4*>(base + C::kRawOff + (hd * G + r) * (kHeadDim * 2) +
-                                                col * 16);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[j] & 0x7fff7fffu);
-        top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // exponent field of the largest size, kept where 2^+-exponent is a
-        // normal float
-        const uint32_t e = min(max(top >> 7, 1u), 253u);
-        const float f = copysignf(__uint_as_float((254u - e) << 23), qp.d.scale_log2);
-        uint32_t h[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            h[j] = pack_f16x2(__uint_as_float(w[j] << 16) * f,
-                              __uint_as_float(w[j] & 0xffff0000u) * f);
-        *reinterpret_cast<uint4*>(base + C::kQOff + hd * C::kQHeadBytes +
-                                  ((col >> 2) * C::kNT + n) * 512 + (row * 4 + (col & 3)) * 16) =
-            make_uint4(h[0], h[1], h[2], h[3]);
-        if (col == 0)
-            sc[hd * C::kRows + r] =
-                fmaxf(fabsf(qp.d.scale_log2) * __uint_as_float(e << 23), 1.17549435e-38f);
-    }
-}
 
 // kCluster: launched as clusters of p.cluster_c CTAs, one unit each (an
 // instantiation of its own, so its code does not weigh on the others).
@@ -641,13 +454,13 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     const bool have = threadIdx.x < kListed && static_cast<int>(threadIdx.x) < b - a;
     if (have) {
         own_it = threadIdx.x == 0 && !listed ? it0 : list[a + threadIdx.x];
-        own = decode_unit(qp, own_it);
+        own = decode_unit<true>(qp, own_it);
         shared_list[threadIdx.x] = own;
     }
     __syncthreads();
     const int u_begin = range[0], u_end = range[1];
     if (!kCluster && u_begin >= u_end) return;
-    const UnitList units{shared_list, list, u_begin};
+    const List units{shared_list, list, u_begin};
 
     uint8_t* ring = base + warp * C::kStages * C::kSlotBytes;
     const uint32_t ring_addr = smem_addr(ring);
@@ -661,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     auto copy_query = [&](int i) {
         if (i >= u_end) return;
         const Unit u = units.get(qp, i);
-        if (u.n_chunks == 0) return;
+        if (u.valid == 0) return;
         if (threadIdx.x == 0) {
             const uint32_t bytes = qp.heads * G * kHeadDim * 2;
             mbar_arrive_expect_tx(q_bar, bytes);
@@ -673,13 +486,16 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     };
     // Waits for the last of them and makes the fragments. Every thread waits.
     auto take_query = [&](int i) {
-        if (i >= u_end || units.get(qp, i).n_chunks == 0) return;
+        if (i >= u_end || units.get(qp, i).valid == 0) return;
         const uint32_t parity = (q_issued - 1) & 1;
         if (!mbar_wait(q_bar, parity, nullptr, p.wait_ns)) {
             record_status(p.status, p.epoch, kDeviceWaitTimeout);
             mbar_wait(q_bar, parity, nullptr, kWaitTimeoutNs);  // the copy still lands first
         }
-        convert_query<C>(qp, base);
+        for (int hd = 0; hd < qp.heads; ++hd)
+            convert_query<1>(base + C::kRawOff + hd * G * (kHeadDim * 2), G, p.scale_log2,
+                             base + C::kQOff + hd * C::kQHeadBytes,
+                             reinterpret_cast<float*>(base + C::kScOff) + hd * C::kRows);
     };
     copy_query(u_begin);
     Stream<C> in;
@@ -707,101 +523,97 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         const Unit u = units.get(qp, ui);
         if (ui - u_begin >= kListed && threadIdx.x == 0 && !tables_match(p, u, __ldg(list + ui)))
             record_status(p.status, p.epoch, kDevicePlanMismatch);
+        const int n_chunks = (u.valid + kChunk - 1) / kChunk;
         int held = -1;  // the slot of the warp's last chunk, not refilled yet
         st.init(q_addr, sc_row, lane);
-        for (int c = in.w; c < u.n_chunks; c += 1 << in.wl2) {
+        for (int c = in.w; c < n_chunks; c += 1 << in.wl2) {
             cp_async_wait<C::kStages - 1>();
             __syncwarp();  // every lane's copies of the chunk have landed
             const uint32_t chunk = ring_addr + slot * C::kSlotBytes;
-            const int left = u.valid - c * kQuantChunk;
-            if (left >= kQuantChunk)
+            const int left = u.valid - c * kChunk;
+            if (left >= kChunk)
                 st.template consume<false>(chunk, left, lane);
             else
                 st.template consume<true>(chunk, left, lane);
             __syncwarp();
-            if (c + (1 << in.wl2) < u.n_chunks)
+            if (c + (1 << in.wl2) < n_chunks)
                 in.refill(qp, units, chunk, dst, sdst, lane);
             else
                 held = slot;
             slot = slot + 1 == C::kStages ? 0 : slot + 1;
         }
-        // ---- merge the warps' states, eight rows at a time, each through the
-        // slot its warp read last
+        // ---- merge the warps' states, each through the slot its warp read last
         const int dump_off = (warp * C::kStages + held) * C::kSlotBytes;
         if (lane == 0) dump_at[warp] = held >= 0 ? dump_off : -1;
+        if (held >= 0)
+            st.dump(reinterpret_cast<float*>(base + dump_off), red_m + warp * 8, red_l + warp * 8,
+                    lane);
+        __syncthreads();
+        const int rows = u.valid > 0 ? G : 0;
+        // a warp takes whole rows: a lane four columns
+        for (int i = warp; i < rows * qp.heads; i += kWarps) {
+            const int hd = i >= rows ? 1 : 0, r = i - hd * rows;
+            const int w0 = hd << in.wl2;  // the head's first warp
+            float mw[kWarps], M = -INFINITY;
+            int at[kWarps];
 #pragma unroll
-        for (int n = 0; n < C::kNT; ++n) {
-            if (n * 8 >= G) break;
-            if (held >= 0)
-                st.dump(n, reinterpret_cast<float*>(base + dump_off), red_m + warp * 8,
-                        red_l + warp * 8, lane);
-            __syncthreads();
-            const int rows = u.n_chunks > 0 ? min(8, G - n * 8) : 0;
-            // a warp takes whole rows: a lane four columns
-            for (int i = warp; i < rows * qp.heads; i += kWarps) {
-                const int hd = i >= rows ? 1 : 0, r = i - hd * rows;
-                const int w0 = hd << in.wl2;  // the head's first warp
-                float mw[kWarps], M = -INFINITY;
-                int at[kWarps];
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const bool there = w < 1 << in.wl2;
-                    at[w] = there ? dump_at[w0 + w] : -1;
-                    mw[w] = at[w] >= 0 ? red_m[(w0 + w) * 8 + r] : -INFINITY;
-                    M = fmaxf(M, mw[w]);
-                }
-                const float mu = M == -INFINITY ? 0.f : M;
-                float L = 0.f;
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    if (at[w] < 0) continue;
-                    const float f = fast_exp2(mw[w] - mu);
-                    const float4 v = *reinterpret_cast<const float4*>(
-                        base + at[w] + (r * kHeadDim + ((lane ^ (r & 7)) * 4)) * 4);
-                    L = fmaf(red_l[(w0 + w) * 8 + r], f, L);
-                    o.x = fmaf(v.x, f, o.x);
-                    o.y = fmaf(v.y, f, o.y);
-                    o.z = fmaf(v.z, f, o.z);
-                    o.w = fmaf(v.w, f, o.w);
-                }
-                const float inv = L != 0.f ? __fdividef(1.f, L) : 0.f;
-                o.x *= inv;
-                o.y *= inv;
-                o.z *= inv;
-                o.w *= inv;
-                const int row_in_unit = hd * G + n * 8 + r;
-                float* lse = nullptr;
-                float to_lse = 1.f;
-                if (u.slot < 0) {
-                    const size_t row =
-                        static_cast<size_t>(u.b) * p.num_qo_heads + u.h * G + row_in_unit;
-                    uint2 v;
-                    v.x = pack_bf16x2(o.x, o.y);
-                    v.y = pack_bf16x2(o.z, o.w);
-                    *reinterpret_cast<uint2*>(p.out + row * kHeadDim + lane * 4) = v;
-                    if (p.lse != nullptr) lse = p.lse + row;
-                    to_lse = kLn2;
-                } else if constexpr (kCluster) {
-                    const int rank = static_cast<int>(cluster_ctarank());
-                    const uint32_t at_row = rank * C::kRows + n * 8 + r;
-                    st_cluster_v4(map_rank0(smem_addr(base) + C::kClusterOff +
-                                            (at_row * kHeadDim + lane * 4) * 4), o);
-                    if (lane == 0)
-                        st_cluster_f32(map_rank0(smem_addr(base) + C::kClusterSums + at_row * 4),
-                                       L != 0.f ? M - kPOffset + __log2f(L) : -INFINITY);
-                } else {
-                    // partial states are [slot][heads * G][128]
-                    const size_t row = static_cast<size_t>(u.slot) * G * qp.heads + row_in_unit;
-                    *reinterpret_cast<float4*>(p.part_o + row * kHeadDim + lane * 4) = o;
-                    lse = p.part_lse + row;
-                }
-                if (lane == 0 && lse != nullptr)
-                    *lse = L != 0.f ? (M - kPOffset + __log2f(L)) * to_lse : -INFINITY;
+            for (int w = 0; w < kWarps; ++w) {
+                const bool there = w < 1 << in.wl2;
+                at[w] = there ? dump_at[w0 + w] : -1;
+                mw[w] = at[w] >= 0 ? red_m[(w0 + w) * 8 + r] : -INFINITY;
+                M = fmaxf(M, mw[w]);
             }
-            if (n == 0) take_query(ui + 1);  // no warp reads this unit's any more
-            __syncthreads();
+            const float mu = M == -INFINITY ? 0.f : M;
+            float L = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (at[w] < 0) continue;
+                const float f = fast_exp2(mw[w] - mu);
+                const float4 v = *reinterpret_cast<const float4*>(
+                    base + at[w] + (r * kHeadDim + ((lane ^ (r & 7)) * 4)) * 4);
+                L = fmaf(red_l[(w0 + w) * 8 + r], f, L);
+                o.x = fmaf(v.x, f, o.x);
+                o.y = fmaf(v.y, f, o.y);
+                o.z = fmaf(v.z, f, o.z);
+                o.w = fmaf(v.w, f, o.w);
+            }
+            const float inv = L != 0.f ? __fdividef(1.f, L) : 0.f;
+            o.x *= inv;
+            o.y *= inv;
+            o.z *= inv;
+            o.w *= inv;
+            const int row_in_unit = hd * G + r;
+            float* lse = nullptr;
+            float to_lse = 1.f;
+            if (u.slot < 0) {
+                const size_t row =
+                    static_cast<size_t>(u.b) * p.num_qo_heads + u.h * G + row_in_unit;
+                uint2 v;
+                v.x = pack_bf16x2(o.x, o.y);
+                v.y = pack_bf16x2(o.z, o.w);
+                *reinterpret_cast<uint2*>(p.out + row * kHeadDim + lane * 4) = v;
+                if (p.lse != nullptr) lse = p.lse + row;
+                to_lse = kLn2;
+            } else if constexpr (kCluster) {
+                const int rank = static_cast<int>(cluster_ctarank());
+                const uint32_t at_row = rank * C::kRows + r;
+                st_cluster_v4(map_rank0(smem_addr(base) + C::kClusterOff +
+                                        (at_row * kHeadDim + lane * 4) * 4), o);
+                if (lane == 0)
+                    st_cluster_f32(map_rank0(smem_addr(base) + C::kClusterSums + at_row * 4),
+                                   L != 0.f ? M - kPOffset + __log2f(L) : -INFINITY);
+            } else {
+                // partial states are [slot][heads * G][128]
+                const size_t row = static_cast<size_t>(u.slot) * G * qp.heads + row_in_unit;
+                *reinterpret_cast<float4*>(p.part_o + row * kHeadDim + lane * 4) = o;
+                lse = p.part_lse + row;
+            }
+            if (lane == 0 && lse != nullptr)
+                *lse = L != 0.f ? (M - kPOffset + __log2f(L)) * to_lse : -INFINITY;
         }
+        take_query(ui + 1);  // no warp reads this unit's any more
+        __syncthreads();
         copy_query(ui + 2);
         if (held >= 0)
             in.refill(qp, units, ring_addr + held * C::kSlotBytes, dst, sdst, lane);
@@ -811,13 +623,13 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         // Every piece's state is in rank 0 now (a piece that is not a unit of
         // this plan weighs nothing), which merges them, a warp a row.
         const Unit u = u_begin < u_end ? units.get(qp, u_begin) : Unit{};
-        if (u.n_chunks == 0 && threadIdx.x < C::kRows)
+        if (u.valid == 0 && threadIdx.x < C::kRows)
             st_cluster_f32(map_rank0(smem_addr(base) + C::kClusterSums +
                                      (cluster_ctarank() * C::kRows + threadIdx.x) * 4),
                            -INFINITY);
         cluster_arrive();
         cluster_wait();
-        if (cluster_ctarank() != 0 || u.n_chunks == 0) return;
+        if (cluster_ctarank() != 0 || u.valid == 0) return;
         const float* sums = reinterpret_cast<const float*>(base + C::kClusterSums);
         const float* vals = reinterpret_cast<const float*>(base + C::kClusterOff);
         for (int r = warp; r < G; r += kWarps) {
@@ -901,42 +713,13 @@ template <class C>
 cudaError_t launch(const QuantDecodeParams& p, const WorkList* w, int grid, cudaStream_t stream,
                    bool pdl) {
     if (p.d.cluster_c > 1) {
-        if constexpr (C::kNT != 1) {
-            return cudaErrorInvalidValue;  // clusters: groups of up to 8 heads
-        } else {
-            if (grid % p.d.cluster_c != 0 || p.d.cluster_c > kMaxClusterCtas || p.heads != 1)
-                return cudaErrorInvalidValue;
-            if (w != nullptr) return launch_ex<C, WorkList, true>(p, *w, grid, stream, pdl);
-            return launch_ex<C, NoList, true>(p, NoList{0}, grid, stream, pdl);
-        }
+        if (grid % p.d.cluster_c != 0 || p.d.cluster_c > kMaxClusterCtas || p.heads != 1)
+            return cudaErrorInvalidValue;
+        if (w != nullptr) return launch_ex<C, WorkList, true>(p, *w, grid, stream, pdl);
+        return launch_ex<C, NoList, true>(p, NoList{0}, grid, stream, pdl);
     }
     if (w != nullptr) return launch_ex<C, WorkList, false>(p, *w, grid, stream, pdl);
     return launch_ex<C, NoList, false>(p, NoList{0}, grid, stream, pdl);
-}
-
-template <template <int> class C>
-cudaError_t launch_ps(const QuantDecodeParams& p, const WorkList* w, int grid, cudaStream_t stream,
-                      bool pdl) {
-    switch (p.d.page_size) {
-        case 8: return launch<C<8>>(p, w, grid, stream, pdl);
-        case 16: return launch<C<16>>(p, w, grid, stream, pdl);
-        case 32: return launch<C<32>>(p, w, grid, stream, pdl);
-        case 64: return launch<C<64>>(p, w, grid, stream, pdl);
-    }
-    return cudaErrorInvalidValue;
-}
-
-template <class C>
-cudaError_t occupancy(int* n) {
-    const cudaError_t e = ensure_smem<C, WorkList, false>();
-    if (e != cudaSuccess) return e;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-        n, quant_decode_kernel<C, WorkList, false>, kThreads, C::kSmemBytes);
-}
-
-template <class C>
-VariantShape shape() {
-    return {kThreads, kWarps * kQuantChunk, C::kStages, C::kSmemBytes};
 }
 
 }  // namespace
@@ -944,28 +727,31 @@ VariantShape shape() {
 // The page size changes neither the registers (capped by the launch bound) nor
 // the shared memory.
 VariantShape quant_shape(int variant) {
-    switch (variant) {
-        case kVariantQuant8: return shape<CfgQ8<16>>();
-        case kVariantQuant16: return shape<CfgQ16<16>>();
-        default: return shape<CfgQ32<16>>();
-    }
+    if (variant != kVariantQuant8) return quant_wide_shape(variant);
+    using C = QCfg<16>;
+    return {kThreads, kWarps * kChunk, C::kStages, C::kSmemBytes};
 }
 
 cudaError_t quant_occupancy(int variant, int* n) {
-    switch (variant) {
-        case kVariantQuant8: return occupancy<CfgQ8<16>>(n);
-        case kVariantQuant16: return occupancy<CfgQ16<16>>(n);
-        default: return occupancy<CfgQ32<16>>(n);
-    }
+    if (variant != kVariantQuant8) return quant_wide_occupancy(variant, n);
+    using C = QCfg<16>;
+    const cudaError_t e = ensure_smem<C, WorkList, false>();
+    if (e != cudaSuccess) return e;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+        n, quant_decode_kernel<C, WorkList, false>, kThreads, C::kSmemBytes);
 }
 
 cudaError_t launch_decode_quant(int variant, const QuantDecodeParams& p, const WorkList* w,
                                 int grid, cudaStream_t stream, bool pdl) {
-    switch (variant) {
-        case kVariantQuant8: return launch_ps<CfgQ8>(p, w, grid, stream, pdl);
-        case kVariantQuant16: return launch_ps<CfgQ16>(p, w, grid, stream, pdl);
-        default: return launch_ps<CfgQ32>(p, w, grid, stream, pdl);
+    if (variant != kVariantQuant8)
+        return launch_decode_quant_wide(variant, p, w, grid, stream, pdl);
+    switch (p.d.page_size) {
+        case 8: return launch<QCfg<8>>(p, w, grid, stream, pdl);
+        case 16: return launch<QCfg<16>>(p, w, grid, stream, pdl);
+        case 32: return launch<QCfg<32>>(p, w, grid, stream, pdl);
+        case 64: return launch<QCfg<64>>(p, w, grid, stream, pdl);
     }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace oxd

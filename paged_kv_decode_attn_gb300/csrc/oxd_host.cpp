@@ -36,7 +36,7 @@ struct oxd_plan_s {
     int device;  // -1 for a host-only plan (desc.num_sms given)
     bool quant;  // for a 4-bit cache (oxd_quant_decode_run), else for bf16 pools
     int group;
-    int heads;   // KV heads a work unit covers (1; 2 for a 4-bit NHD cache)
+    int heads;   // KV heads a stream covers (1; 2 for a 4-bit NHD cache)
     int variant;
     int n_items;
     int n_slots;
@@ -351,7 +351,9 @@ oxd_status plan_decode(const oxd_paged_decode_desc* desc, const int32_t* indptr,
     // their pages after it.
     // Streams per request and query rows per stream: one KV head each, but in a
     // 4-bit NHD cache, where a head's codes of a token are half a 128-byte line,
-    // two (for an even number of heads), so that whole lines are read at once.
+    // two (for an even number of heads), so that whole lines are read at about
+    // the same time: by one CTA for groups of up to 8 query heads, by
+    // neighbouring CTAs for larger ones.
     // Below 512 tokens a resident CTA a call is short enough that the streams'
     // number counts for more than the bytes.
     const bool pairs = quant && d.layout == OXD_LAYOUT_NHD && d.num_kv_heads % 2 == 0 &&
@@ -401,11 +403,14 @@ oxd_status plan_decode(const oxd_paged_decode_desc* desc, const int32_t* indptr,
     // same pages). A piece is a run of consecutive pages of one stream; a
     // stream cut into several pieces is "split" and gets one partial-state
     // slot per piece.
-    const int pps = std::max(1, vs.stage_tokens / heads / ps);  // pages per pipeline stage
+    // pages per pipeline stage of a unit
+    const int pps = std::max(1, vs.stage_tokens / (variant == kVariantQuant8 ? heads : 1) / ps);
     // Groups of more than 16 query heads run every piece on a pair of CTAs,
     // one per 16-row half, side by side (the second read of each page is
-    // then served by L2); the partition below is over CTA pairs.
-    const int copies = variant == kVariantMma32 ? 2 : 1;
+    // then served by L2), the pairs of heads above on one per head; the
+    // partition below is over CTA pairs.
+    const int copies =
+        variant == kVariantMma32 || (heads == 2 && variant != kVariantQuant8) ? 2 : 1;
     const int64_t resident = static_cast<int64_t>(num_sms) * ctas_per_sm / copies;
     auto tokens_to = [&](int b, int k) {  // tokens in pages [0, k) of request b
         const int P = indptr[b + 1] - indptr[b];
@@ -685,7 +690,7 @@ oxd_status plan_decode(const oxd_paged_decode_desc* desc, const int32_t* indptr,
         }
     }
     const int n_split = static_cast<int>(split_tab.size());
-    // Units: each piece once per 16-row half, on CTAs copies*c + half.
+    // Units: each piece once per 16-row half (or head), on CTAs copies*c + half.
     const int n_units = n_pieces * copies;
     grid *= copies;
     std::vector<int4> units;

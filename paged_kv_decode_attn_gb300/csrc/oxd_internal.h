@@ -23,7 +23,7 @@ enum Variant : int {
     kVariantMma32 = 4,   // 17 <= G <= 32: each piece runs on a pair of 16-row CTAs
     kVariantWide = 5,    // 17 <= G <= 32: tcgen05 (TMEM accumulators), one CTA per piece
     kVariantQuant8 = 6,  // 4-bit cache (oxd_decode_quant.cu), G <= 8
-    kVariantQuant16 = 7, // 9 <= G <= 16
+    kVariantQuant16 = 7, // (oxd_decode_quant_wide.cu) 9 <= G <= 16
     kVariantQuant32 = 8, // 17 <= G <= 32
     kNumVariants = 9
 };
@@ -187,19 +187,23 @@ cudaError_t wide_occupancy(int* ctas_per_sm);
 cudaError_t launch_decode_wide(const CUtensorMap& tk, const CUtensorMap& tv,
                                const CUtensorMap& tq, const DecodeParams& p, const WorkList* w,
                                int grid, cudaStream_t stream, bool pdl);
-// Decode over a 4-bit cache (oxd_decode_quant.cu).
+// Decode over a 4-bit cache (oxd_decode_quant.cu, oxd_decode_quant_wide.cu).
 constexpr int kCodeBytes = 64;   // 4-bit codes of one (token, head) row
 constexpr int kScaleBytes = 8;   // its four f16 scales
-constexpr int kQuantChunk = 32;  // tokens a consumer warp takes at a time
 struct QuantDecodeParams {
     DecodeParams d;
     const uint8_t* k_codes;
     const uint8_t* v_codes;
     const uint16_t* k_scales;    // f16 [num_pages][Hkv][page_size][4]
     const uint16_t* v_scales;
-    int32_t heads;               // KV heads a unit covers: its h counts such groups
+    int32_t heads;               // KV heads of a stream (1 or 2): a unit's h counts such groups
 };
 VariantShape quant_shape(int variant);
+// Groups of 9..32 heads (oxd_decode_quant_wide.cu), called by the functions here.
+VariantShape quant_wide_shape(int variant);
+cudaError_t quant_wide_occupancy(int variant, int* ctas_per_sm);
+cudaError_t launch_decode_quant_wide(int variant, const QuantDecodeParams& p, const WorkList* w,
+                                     int grid, cudaStream_t stream, bool pdl);
 cudaError_t quant_occupancy(int variant, int* ctas_per_sm);
 cudaError_t launch_decode_quant(int variant, const QuantDecodeParams& p, const WorkList* w,
                                 int grid, cudaStream_t stream, bool pdl);
