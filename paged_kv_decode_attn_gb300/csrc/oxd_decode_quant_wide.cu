@@ -249,15 +249,15 @@ struct State {
     }
 
     // Weights of the scores (score s counts as s * sc) as P^T fragments at
-    // `p_at`; pr keeps them in F32.
-    __device__ __forceinline__ void weights(const float (&s)[C::kNT][4], float (&pr)[C::kNT][4],
+    // `p_at`, and their sums over this lane's two tokens.
+    __device__ __forceinline__ void weights(const float (&s)[C::kNT][4], float (&sum)[C::kNT][2],
                                             uint32_t p_at) {
 #pragma unroll
         for (int n = 0; n < C::kNT; n += 2) {
             uint32_t f[4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float* y = pr[n + i];
+                float y[4];
                 const float* x = s[n + i];
                 fma_pairs(y[0], y[1], x[0], x[1], sc[n + i][0], sc[n + i][1], mu[n + i][0],
                           mu[n + i][1]);
@@ -267,6 +267,8 @@ struct State {
                 for (int e = 0; e < 4; ++e) y[e] = fast_exp2(y[e]);
                 f[2 * i] = transpose_8x8(pack_f16x2(y[0], y[1]));
                 f[2 * i + 1] = transpose_8x8(pack_f16x2(y[2], y[3]));
+                sum[n + i][0] = y[0] + y[2];
+                sum[n + i][1] = y[1] + y[3];
             }
             sts128(p_at + n / 2 * 512, f);
         }
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
             const uint32_t p_buf = ring + C::kPOff + flip * C::kPBytes + lane * 16;
             const uint32_t t_buf = ring + C::kTOff + flip * C::kTBytes;
             const uint32_t p_mine = p_buf + warp * C::kNT * 256;
-            float x[C::kNT][4], pr[C::kNT][4];
+            float x[C::kNT][4], sum[C::kNT][2];
             st.scores(x, stage + k_off, stage + ks_off);
             if (left < kWarpTokens) {
 #pragma unroll
@@ -476,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
                     raise |= fmaf(mx[n][j], st.sc[n][j], st.mu[n][j]) > kPOffset + kLazy;
                 }
             }
-            if (s > 0) st.weights(x, pr, p_mine);
+            if (s > 0) st.weights(x, sum, p_mine);
             cp_async_wait<C::kStages - 3>();  // this warp's part of the next stage
             // The barrier: the stage's weights and the next stage are there, every
             // warp is done with the stage before, and whether some maximum rises.
@@ -518,13 +520,13 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
                         }
                     }
                 }
-                st.weights(x, pr, p_mine);
+                st.weights(x, sum, p_mine);
                 __syncthreads();
             }
 #pragma unroll
             for (int n = 0; n < C::kNT; ++n) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) st.l[n][j] += pr[n][j] + pr[n][2 + j];
+                for (int j = 0; j < 2; ++j) st.l[n][j] += sum[n][j];
             }
             st.values(stage + v_off, p_buf, t_buf + (warp * kStageTokens + 2 * tq) * 2);
             left -= kStageTokens;

@@ -90,8 +90,9 @@ double unit_overhead_tokens(int variant) {
         case kVariantMma32: return 320.0;
         case kVariantWide: return 96.0;
         // 4-bit: about 4 us of a CTA's streaming (its tokens are 3.6 times fewer
-        // bytes). 64 -> 320 took the log-normal GQA4 batch from 98 to 86 us and
-        // GQA8 B=256 from 428 to 416.
+        // bytes). 64 -> 320 took the log-normal GQA4 batch from 98 to 86 us (160:
+        // 90) and GQA8 B=256 from 428 to 416; groups of 16 and 32 heads do not
+        // tell 160 from 320 (within 2 %).
         case kVariantQuant8:
         case kVariantQuant16:
         case kVariantQuant32: return 320.0;
