@@ -41,9 +41,15 @@ __device__ __forceinline__ float scale_inverse(uint32_t scale) {
 // tie * s has 14 bits), and x * inv is within 2^-19 of it up to 6, so rounding
 // it to a multiple of 2^-17, by adding and taking away 1.5 * 2^6, restores ties
 // and moves nothing across one.
-__device__ __forceinline__ float code_argument(float x, float inv) {
+// Two at a time, as packed f32 (half the instructions).
+__device__ __forceinline__ void code_arguments(float& x, float& y, float inv) {
     constexpr float kGrid = 96.f;
-    return __fadd_rn(fmaf(x, inv, kGrid), -kGrid);
+    asm("{\n\t.reg .b64 u, v, g;\n\t"
+        "mov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %2};\n\tmov.b64 g, {%3, %3};\n\t"
+        "fma.rn.f32x2 u, u, v, g;\n\tmov.b64 g, {%4, %4};\n\t"
+        "add.rn.f32x2 u, u, g;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(inv), "f"(kGrid), "f"(-kGrid));
 }
 
 __device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
@@ -52,16 +58,21 @@ __device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(
 // Codes of eight columns (bf16 pairs): each the e2m1 number nearest to x / s,
 // ties to even, the first column in the lowest four bits.
 __device__ __forceinline__ uint32_t code_eight(const uint4& x, float inv) {
+    float f[8];
+    const uint32_t* w = &x.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_low(w[i]);
+        f[2 * i + 1] = bf16_high(w[i]);
+        code_arguments(f[2 * i], f[2 * i + 1], inv);
+    }
     uint32_t r;
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
         "mov.b32 %0, {a, b, c, d};\n\t}"
         : "=r"(r)
-        : "f"(code_argument(bf16_low(x.x), inv)), "f"(code_argument(bf16_high(x.x), inv)),
-          "f"(code_argument(bf16_low(x.y), inv)), "f"(code_argument(bf16_high(x.y), inv)),
-          "f"(code_argument(bf16_low(x.z), inv)), "f"(code_argument(bf16_high(x.z), inv)),
-          "f"(code_argument(bf16_low(x.w), inv)), "f"(code_argument(bf16_high(x.w), inv)));
+        : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
     return r;
 }
 

@@ -81,8 +81,6 @@ __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_const
     }
 }
 
-// What a lane holds of a row: as bf16 pairs, or as codes and the scales of its
-// two groups.
 // A page's rows of one tensor: where they and their scales begin.
 struct PageRows {
     uint8_t* data;
@@ -97,7 +95,9 @@ __device__ __forceinline__ PageRows page_rows_of(const PagePools& c, int tensor,
             k4 ? c.scales[tensor] + first * kRowScales : nullptr};
 }
 
-// row: in the pool's order; sc: in the order of scales (heads before tokens).
+// What a lane holds of a row: as bf16 pairs, or as codes and the scales of its
+// two groups. row: in the pool's order; sc: in the order of scales (heads before
+// tokens).
 template <bool k4>
 struct Piece;
 template <>
@@ -167,13 +167,17 @@ __device__ __forceinline__ void convert(const Piece<true>& a, Piece<false>& b) {
     b.hi = unhold(a.hi, a.s_hi);
 }
 
-// Other formats or layouts: kRows rows a thread's eight lanes take.
+// Other formats or layouts: kRows rows a thread's eight lanes take. A block's
+// life is a chain of loads (pair, refcount, rows), so the more blocks an SM holds
+// the better: eight at 32 registers, though a few spill, pack and unpack 4096
+// pages in 123 us, six at 40 registers in 130, as the compiler would have it
+// (48) in 133. One row a thread 146, four 137.
 constexpr int kRows = 2;
 constexpr int kSliceRows = kThreads / 8 * kRows;
 
 template <bool kSrc4, bool kDst4>
-__global__ void __launch_bounds__(kThreads) convert_pages_kernel(const __grid_constant__
-                                                                 CopyPagesParams p) {
+__global__ void __launch_bounds__(kThreads, 8)
+    convert_pages_kernel(const __grid_constant__ CopyPagesParams p) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.last_epoch = p.epoch;
     const int s = threadIdx.x & 7;
     const int page_rows = p.page_size * p.H;
