@@ -7,10 +7,10 @@
 // A call reads q, k and v once and writes q_out and the page rows once, so
 // bytes bound it (long calls) or the chain position -> page -> refcount (a
 // decode step). A block of eight warps takes four tokens (one in short calls,
-// which spreads them over the SMs; for long calls one, two and eight tokens a
-// block take 129, 101 and 88 us where four take 86). Its threads form the tokens' 64 cosines and sines each, one pair a thread,
-// which all of a token's heads share (formed per row in double, they were
-// the whole cost); then each warp takes rows of one token, four at a time,
+// which spreads them over the SMs; for a 16384-token prompt into 4-bit pages one,
+// two and eight tokens a block take 129, 101 and 88 us where four take 86). Its threads form the tokens'
+// 64 cosines and sines each, one pair a thread, which all of a token's heads
+// share (formed per row in double, they were the whole cost); then each warp takes rows of one token, four at a time,
 // eight lanes a row: lane s of a row holds columns 8s .. 8s + 7 and 64 + 8s ..
 // (two 16-byte loads), so a rotation pairs values of one lane, a 4-bit group
 // of 32 is four lanes, and a row's 8 cosines stay in registers.
