@@ -553,8 +553,9 @@ oxd_status oxd_prefill_plan_destroy(oxd_prefill_plan plan);
  * the largest size of the group's 32 bf16 values; code = the e2m1 number
  * nearest to x / s, ties to the even code (the one with mantissa bit 0), sizes
  * above 6 taken as 6; a value that rounds to zero may get either zero; a group
- * with s = 0 (amax up to about 1.8e-7) is all zeros. So values are held up to +-65472 (larger ones, infinities too, are
- * held as that) and a NaN is held as some finite value.
+ * with s = 0 (amax up to about 1.8e-7) is all zeros. So values are held up to
+ * +-65472 (larger ones, infinities too, are held as that). A NaN is held as some
+ * finite value, and so may the other columns of its group be.
  */
 typedef enum {
     OXD_FORMAT_BF16 = 0,
@@ -589,8 +590,10 @@ oxd_status oxd_quant_decode_plan(const oxd_paged_decode_desc* desc, const int32_
  * score product as f16 scaled by a power of two per head (exact for columns
  * within 2^-14 of the head's largest), codes exactly and K's scales in F32; a
  * V value (code times scale) and a softmax weight are each rounded once to
- * f16, weights below 2^-24 of the largest to multiples of 2^-34 of it. Arguments, errors, status codes and determinism as
- * oxd_paged_decode_run; the four pools of `cache` are read only.
+ * f16, weights below 2^-24 of the largest to multiples of 2^-34 of it.
+ * Arguments, errors, status codes and determinism as oxd_paged_decode_run (of
+ * the waits, only those for query rows have the plan's limit: the pages come by
+ * copies that end by themselves); the four pools of `cache` are read only.
  */
 oxd_status oxd_quant_decode_run(oxd_plan plan, const void* q, const oxd_kv_pools* cache,
                                 const int32_t* indptr, const int32_t* indices,
@@ -611,7 +614,8 @@ oxd_status oxd_quant_decode_run(oxd_plan plan, const void* q, const oxd_kv_pools
  * A rope position outside [0, 2^24) counts as OXD_DEVICE_BAD_POSITION: the
  * token's K/V rows are not written (its q_out rows are rotated at the low 24
  * bits). Everything else as oxd_rope_append, the errors too; num_axes outside
- * [1, 4] or a pair_axis entry not below num_axes is OXD_ERR_INVALID_ARGUMENT.
+ * [1, 4] or a pair_axis entry not below num_axes is OXD_ERR_INVALID_ARGUMENT,
+ * more than 2^20 heads OXD_ERR_UNSUPPORTED.
  */
 typedef struct {
     int32_t num_tokens;     /* T */
@@ -675,7 +679,7 @@ oxd_status oxd_quant_rope_append(const oxd_axes_append_desc* desc, const void* q
  * nothing and records OXD_DEVICE_BAD_PAGE; the other pairs are copied.
  * Host-side errors (nothing enqueued): OXD_ERR_INVALID_ARGUMENT (NULL, sizes,
  * formats, scales of a bf16 cache not NULL), OXD_ERR_UNSUPPORTED (head_dim,
- * page size), OXD_ERR_ALIGNMENT, OXD_ERR_ALIAS, OXD_ERR_WORKSPACE_TOO_SMALL,
+ * page size, more than 2^20 heads), OXD_ERR_ALIGNMENT, OXD_ERR_ALIAS, OXD_ERR_WORKSPACE_TOO_SMALL,
  * OXD_ERR_CUDA.
  */
 typedef struct {

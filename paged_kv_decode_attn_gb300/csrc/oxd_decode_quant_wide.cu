@@ -536,6 +536,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         // ---- the unit's end: denominators over the lanes and warps; the columns
         // are whole. Meanwhile the next unit's query rows (no warp reads this
         // unit's fragments any more).
+        if (n_stages == 0) __syncthreads();  // (the next unit's entry, and the sums' last readers)
 #pragma unroll
         for (int n = 0; n < C::kNT; ++n) {
 #pragma unroll
@@ -548,7 +549,6 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
             }
         }
         const Unit u = cur[ui & 1];
-        if (n_stages == 0) __syncthreads();  // (the next unit's entry)
         if (ui + 1 < u_end) take_query(cur[(ui + 1) & 1]);
         __syncthreads();
         if (u.valid == 0) continue;

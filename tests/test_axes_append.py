@@ -243,3 +243,61 @@ def test_many_tokens(four):
     j = Job([0, 3, 1000], [2100, 700, 1300], 8, 2, 16, "NHD", 3, four, seed=10, far=5000)
     assert j.run() == 0
     j.check()
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("Hq,Hkv", [(512, 64), (3, 50), (1000, 1)])
+def test_many_heads(four, Hq, Hkv):
+    j = Job([5, 0, 16], [2, 1, 1], Hq, Hkv, 8, "NHD", 2, four, seed=31)
+    assert j.run() == 0
+    j.check()
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_a_captured_step_replays_on_new_rows_and_positions(four):
+    """A decode step's append, captured once: the rows, slots and rope positions are what the tensors
+    hold at each replay, and a replayed call leaves what an eager one would."""
+    B, Hq, Hkv, ps, pages = 5, 8, 2, 8, 20
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.zeros(B, Hq, 128, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.zeros(B, Hkv, 128, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    i32 = lambda a: torch.as_tensor(np.asarray(a, np.int32), device="cuda")  # noqa: E731
+    req, pos, rope = i32(np.arange(B)), i32(np.zeros(B)), i32(np.zeros((3, B)))
+    indptr, indices = i32(np.arange(0, pages + 1, pages // B)), i32(np.arange(pages)[::-1].copy())
+    ref = torch.ones(pages, dtype=torch.int32, device="cuda")
+    desc = oxd.make_axes_append_desc(B, B, Hq, Hkv, ps, "NHD", pages, pages, sections=[16, 24, 24])
+
+    def pools():
+        if not four:
+            return [torch.zeros(pages, ps, Hkv, 128, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+        return ([torch.zeros(pages, ps, Hkv, 64, dtype=torch.uint8, device="cuda") for _ in "kv"] +
+                [torch.zeros(pages, Hkv, ps, 4, dtype=torch.float16, device="cuda") for _ in "kv"])
+
+    def call(to, q_out, ws):
+        args = (desc, q, k, v, req, pos, rope, indptr, indices, ref, q_out)
+        if four:
+            oxd.oxd_quant_rope_append(*args, oxd.KvPools(*to), ws)
+        else:
+            oxd.oxd_rope_axes_append(*args, *to, ws)
+
+    a, b = pools(), pools()
+    qa, qb = torch.empty_like(q), torch.empty_like(q)
+    wa, wb = (torch.zeros(256, dtype=torch.uint8, device="cuda") for _ in "ab")
+    call(a, qa, wa)
+    torch.cuda.synchronize()
+    for x in a:
+        x.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(a, qa, wa)
+    for step in range(6):
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape, device="cuda", generator=g))
+        pos.copy_(torch.arange(B, device="cuda") + 5 * step)
+        rope.copy_(torch.randint(0, 3000, rope.shape, device="cuda", generator=g))
+        graph.replay()
+        call(b, qb, wb)
+        assert torch.equal(qa, qb)
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+        assert oxd.oxd_read_device_status(wa) == oxd.oxd_read_device_status(wb) == 0

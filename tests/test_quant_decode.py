@@ -334,3 +334,49 @@ def test_small_batches_in_one_launch(G, Hkv, lengths):
         keep = torch.full_like(out, 3.0)
         c.run(plan, ws=ws, out=keep)
         assert oxd.oxd_read_device_status(ws) == 2 and (keep == 3).all()
+
+
+@pytest.mark.parametrize("G,Hkv,layout,n,L", [(16, 8, "HND", 2600, 3), (32, 4, "NHD", 2600, 9),
+                                              (32, 8, "NHD", 2600, 9), (4, 8, "NHD", 5000, 8),
+                                              (8, 8, "HND", 2600, 2)])
+def test_tens_of_units_a_cta(G, Hkv, layout, n, L):
+    """From the call's own list, bound and replayed. (A CTA holds 32 units decoded: all cases but that
+    of 10408 units pass it.)"""
+    c = Cache([L] * n + [300, 1], G, Hkv, 8, layout, seed=26)
+    plan, out, lse = check(c)
+    assert plan.info.num_work_items > (32 if n * Hkv > 10400 else 20) * plan.info.grid_ctas
+    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    oxd.oxd_plan_bind_workspace(plan, ws)
+    o2, l2, _ = c.run(plan, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(plan, ws=ws, out=o2, lse=l2)
+    o2.zero_(), l2.zero_()
+    graph.replay()
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+    assert oxd.oxd_read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("G,Hkv", [(1, 200), (8, 65), (32, 40)])
+@pytest.mark.parametrize("layout", ["NHD", "HND"])
+def test_many_heads(G, Hkv, layout):
+    check(Cache([70, 9], G, Hkv, 16, layout, seed=27))
+
+
+@pytest.mark.parametrize("G", [4, 16, 32])
+def test_two_runs_of_one_plan_at_once(G):
+    """One plan, two workspaces, two streams, neither waiting for the other."""
+    c = Cache([3000, 33, 700, 1], G, 2, 16, "NHD", seed=28)
+    plan, out, lse = check(c)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    runs = []
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                runs.append(c.run(plan))
+    torch.cuda.synchronize()
+    for o, l, ws in runs:
+        assert oxd.oxd_read_device_status(ws) == 0
+        assert torch.equal(o, out) and torch.equal(l, lse)
