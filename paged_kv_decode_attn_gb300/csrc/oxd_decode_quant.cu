@@ -19,8 +19,8 @@
 //     of shared memory, a group of up to 8 heads is one N tile, and neither
 //     operand goes back through shared memory;
 //   * codes become f16 pairs by cvt.f16x2.e2m1x2, exact. K's scales multiply
-//     the F32 sums of each 32-column group (4 FMAs for 2 MMAs), V's scales the
-//     f16 codes; P goes from the S^T accumulator to the P^T operand by
+//     the F32 sums of each 32-column group (2 packed FMAs for 2 MMAs), V's scales
+//     the f16 codes; P goes from the S^T accumulator to the P^T operand by
 //     movmatrix;
 //   * the running maximum is raised only when a score passes it by 2^4, so most
 //     chunks need one warp vote and no reduction or rescaling. P is held in f16
@@ -30,6 +30,12 @@
 // split streams leave F32 partial states for the merge kernel, as in the bf16
 // decode; a small batch is launched as clusters, one stream a cluster, whose
 // first CTA merges the pieces' states from its shared memory.
+//
+// HBM bounds long streams: 8 heads x 8, 256 requests U{128..16384}, NHD, 414 us
+// or 5.9 TB/s, 88 % of the copy rate (HND 403 us); between the ends of units the
+// stream runs at 97 %. A unit's end costs 2.9 us (4 heads) to 3.6 (8), which is
+// what log-normal batches pay: 84 us, 71 %. One request of 512 tokens, 8 KV heads:
+// 8.2 us, dependent latencies of one launch.
 #include <cuda_bf16.h>
 
 #include <atomic>
