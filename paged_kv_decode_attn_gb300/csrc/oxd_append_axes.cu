@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     axes_append_kernel(const __grid_constant__ AxesAppendParams p) {
     constexpr int kTokenWarps = kWarps / kTokens;
     __shared__ float2 cs_all[kTokens][kPairs], low_all[k4 ? kTokens : 1][kPairs];
+    __shared__ float4 turns[kTokens > 1 ? kPairs : 1];
     __shared__ int bad_rope[kTokens];
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.last_epoch = p.epoch;
@@ -269,12 +270,14 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
         b = p.token_request[t];
         pos = p.positions[t];
     }
+    // Lanes that read different parameters are served one by one: once a block.
+    if (kTokens > 1 && threadIdx.x < kPairs) turns[threadIdx.x] = p.turns[threadIdx.x];
     if (threadIdx.x < kTokens) bad_rope[threadIdx.x] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < kTokens * kPairs; i += kWarps * 32) {
         const long long ti = static_cast<long long>(blockIdx.x) * kTokens + i / kPairs;
         if (ti < p.T) {
-            const float4 g = p.turns[i % kPairs];
+            const float4 g = kTokens > 1 ? turns[i % kPairs] : p.turns[i % kPairs];
             const int rp = p.rope_positions[static_cast<size_t>(__float_as_int(g.w)) * p.T + ti];
             if (rp < 0 || rp >= (1 << 24)) bad_rope[i / kPairs] = 1;
             // pair 8 s + j at 8 j + s: the eight lanes of a row read a line
