@@ -555,7 +555,7 @@ oxd_status oxd_prefill_plan_destroy(oxd_prefill_plan plan);
  * above 6 taken as 6; a value that rounds to zero may get either zero; a group
  * with s = 0 (amax up to about 1.8e-7) is all zeros. So values are held up to
  * +-65472 (larger ones, infinities too, are held as that). A NaN is held as some
- * finite value, and so may the other columns of its group be.
+ * finite value and does not count for its group's amax.
  */
 typedef enum {
     OXD_FORMAT_BF16 = 0,

@@ -122,16 +122,25 @@ __device__ __forceinline__ float nudge_tie(float hi, float lo) {
     return __uint_as_float(b);
 }
 
-// a c - b s (c, s with low parts cl, sl), rounded to bf16 once.
+// a c - b s (c, s with low parts cl, sl), rounded to bf16 once. kLarge: for sizes
+// from 2^126 on, whose sum may pass the largest float, and infinities, whose low
+// parts would be NaN.
+template <bool kLarge>
 __device__ __forceinline__ float exact_turn(float a, float c, float cl, float b, float s,
                                             float sl) {
     float p, pe, q, qe, d, de;
+    if (kLarge) {
+        a *= 0.25f;
+        b *= 0.25f;
+    }
     two_prod(a, c, p, pe);
     two_prod(-b, s, q, qe);
     two_sum(p, q, d, de);
+    if (kLarge && !(fabsf(d) <= 3.40282347e38f)) return d;
     const float rest = fmaf(a, cl, fmaf(-b, sl, (pe + qe) + de));
     const float hi = __fadd_rn(d, rest);
-    return nudge_tie(hi, __fadd_rn(rest, -__fadd_rn(hi, -d)));
+    const float y = nudge_tie(hi, __fadd_rn(rest, -__fadd_rn(hi, -d)));
+    return kLarge ? 4.f * y : y;
 }
 
 // The lane's 16 columns of a row: eight below 64 and their partners.
@@ -166,11 +175,34 @@ __device__ __forceinline__ Slice rotate(const Slice& x, const float2* cs) {
     return y;
 }
 
-// The same with the bf16 numbers nearest to the exact rotation. The float
+// The larger sizes of two pairs, with any signs.
+__device__ __forceinline__ uint32_t max_sizes_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Rotates w[i] and w[4 + i], pairs of columns and their partners, exactly.
+template <bool kLarge>
+__device__ __forceinline__ void turn_slice(uint32_t (&w)[8], const float2* cs, const float2* low) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const float a0 = bf16_low(w[i]), a1 = bf16_high(w[i]);
+        const float b0 = bf16_low(w[4 + i]), b1 = bf16_high(w[4 + i]);
+        const float2 t0 = cs[8 * (2 * i)], t1 = cs[8 * (2 * i + 1)];
+        const float2 l0 = low[8 * (2 * i)], l1 = low[8 * (2 * i + 1)];
+        w[i] = pack_bf16x2(exact_turn<kLarge>(a0, t0.x, l0.x, b0, t0.y, l0.y),
+                           exact_turn<kLarge>(a1, t1.x, l1.x, b1, t1.y, l1.y));
+        w[4 + i] = pack_bf16x2(exact_turn<kLarge>(b0, t0.x, l0.x, -a0, t0.y, l0.y),
+                               exact_turn<kLarge>(b1, t1.x, l1.x, -a1, t1.y, l1.y));
+    }
+}
+
+// As rotate, with the bf16 numbers nearest to the exact rotation. The float
 // result y is within 2^-21 (|a| + |b|) of it (cosine and sine rounded once, two
 // products, a sum): where both ends of that range round alike, that is it. A
-// lane with a value where they do not (about one in 200) forms its slice anew
-// with the low parts, one pair of columns at a time.
+// lane with a value where they do not (about one in 200, infinities among them)
+// forms its slice anew with the low parts, one pair of columns at a time.
 __device__ __forceinline__ Slice rotate_exact(const Slice& x, const float2* cs,
                                               const float2* low) {
     const uint32_t* a = &x.lo.x;
@@ -194,23 +226,17 @@ __device__ __forceinline__ Slice rotate_exact(const Slice& x, const float2* cs,
         differ |= yb[i] ^ pack_bf16x2(fmaf(n0, -kErr, v0), fmaf(n1, -kErr, v1));
     }
     if (differ != 0) {
-        uint32_t w[8];
+        uint32_t w[8], top = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             w[i] = a[i];
             w[4 + i] = b[i];
+            top = max_sizes_bf16x2(top, max_sizes_bf16x2(a[i], b[i]));
         }
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-            const float a0 = bf16_low(w[i]), a1 = bf16_high(w[i]);
-            const float b0 = bf16_low(w[4 + i]), b1 = bf16_high(w[4 + i]);
-            const float2 t0 = cs[8 * (2 * i)], t1 = cs[8 * (2 * i + 1)];
-            const float2 l0 = low[8 * (2 * i)], l1 = low[8 * (2 * i + 1)];
-            w[i] = pack_bf16x2(exact_turn(a0, t0.x, l0.x, b0, t0.y, l0.y),
-                               exact_turn(a1, t1.x, l1.x, b1, t1.y, l1.y));
-            w[4 + i] = pack_bf16x2(exact_turn(b0, t0.x, l0.x, -a0, t0.y, l0.y),
-                                   exact_turn(b1, t1.x, l1.x, -a1, t1.y, l1.y));
-        }
+        if (__vcmpgeu2(top & 0x7fff7fffu, 0x7e807e80u) == 0)  // 2^126
+            turn_slice<false>(w, cs, low);
+        else
+            turn_slice<true>(w, cs, low);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             ya[i] = w[i];

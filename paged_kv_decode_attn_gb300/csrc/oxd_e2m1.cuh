@@ -76,15 +76,21 @@ __device__ __forceinline__ uint32_t code_eight(const uint4& x, float inv) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Eight columns of a row in 4 bits, and their group's f16 scale. The group's
 // other columns are in the lanes next to this one (a multiple of four and its
 // three followers): every lane of the warp calls it.
 __device__ __forceinline__ void hold_eight(const uint4& x, uint32_t& code, uint32_t& scale) {
-    // sizes as the integers their bits are
-    uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                          __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    // (the larger of a number and a NaN is the number, here and in fmaxf)
+    uint32_t m = max_bf16x2(max_bf16x2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                            max_bf16x2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+    m = max_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
     scale = group_scale(fmaxf(bf16_low(m), bf16_high(m)));
     code = code_eight(x, scale_inverse(scale));
 }

@@ -301,3 +301,23 @@ def test_a_captured_step_replays_on_new_rows_and_positions(four):
         for x, y in zip(a, b):
             assert torch.equal(x, y)
         assert oxd.oxd_read_device_status(wa) == oxd.oxd_read_device_status(wb) == 0
+
+
+@pytest.mark.parametrize("T", [40, 700])
+def test_infinite_and_overflowing_keys_are_held_as_the_formats_ends(T):
+    """A rotation that ends at an infinity, from an infinite column or past the largest float, is held
+    as +-65472 with its sign, in even and odd columns alike, and its group's other columns against
+    that scale; the bf16 append and a pack of its pages come to the same."""
+    j = Job([1], [T], 1, 2, 16, "NHD", 1, True, seed=31)
+    rng = np.random.default_rng(32)
+    kinds = np.array([np.inf, -np.inf, 3e38, -3e38, 1.8e38])
+    for t in range(T):
+        # one column of a pair infinite, or both large: no inf - inf, which is a NaN by the formula
+        col = rng.integers(0, 64)
+        x = R.round_bf16(rng.choice(kinds))
+        j.k[t, 0, col + 64 * rng.integers(0, 2)] = x
+        if np.isfinite(x):
+            j.k[t, 0, [col, col + 64]] = x * rng.choice([-1, 1], 2)
+    assert np.isnan(j.rotated(j.k)).sum() == 0
+    assert j.run() == 0
+    j.check()

@@ -247,3 +247,22 @@ def test_pools_past_32_bits():
     for x in (k, v):
         assert torch.equal(x[pages - 1], x[0]) and torch.equal(x[1], x[pages - 2])
         assert not x[2].any() and not x[pages // 2].any() and not x[pages - 3].any()
+
+
+@pytest.mark.parametrize("column", [0, 1, 7, 38, 69, 127])
+def test_a_nan_leaves_the_other_columns_of_its_group(column):
+    src, dst = Pools("bf16", "HND", 1, 8, 1, seed=12), Pools("e2m1", "HND", 1, 8, 1, seed=12)
+    x = src.rows(0)[0, 0].copy()
+    group = column // 32 * 32
+    x[:, group:group + 32] *= 1 + 9 * (np.arange(32) % 2 == column % 2)  # the NaN's like are largest
+    x = R.round_bf16(x)
+    src.dev[0][0, 0] = bf16(x)
+    src.dev[0][0, 0, :, column] = float("nan")
+    assert run(src, dst, [0], [0]) == 0
+    x[:, column] = 0
+    codes, scales = R.hold(x)
+    np.testing.assert_array_equal(dst.got(0)[1][0, 0], scales.view(np.int16))
+    v = R.values(dst.got(0)[0], dst.got(0)[1].view(np.float16))[0, 0]
+    keep = np.arange(128) != column
+    assert np.isfinite(v).all()
+    np.testing.assert_array_equal(v[:, keep], R.values(codes, scales)[:, keep])
