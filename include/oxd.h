@@ -679,8 +679,8 @@ oxd_status oxd_quant_rope_append(const oxd_axes_append_desc* desc, const void* q
  * nothing and records OXD_DEVICE_BAD_PAGE; the other pairs are copied.
  * Host-side errors (nothing enqueued): OXD_ERR_INVALID_ARGUMENT (NULL, sizes,
  * formats, scales of a bf16 cache not NULL), OXD_ERR_UNSUPPORTED (head_dim,
- * page size, more than 2^20 heads), OXD_ERR_ALIGNMENT, OXD_ERR_ALIAS, OXD_ERR_WORKSPACE_TOO_SMALL,
- * OXD_ERR_CUDA.
+ * page size, more than 2^20 heads or 2^31 - 65536 pairs), OXD_ERR_ALIGNMENT,
+ * OXD_ERR_ALIAS, OXD_ERR_WORKSPACE_TOO_SMALL, OXD_ERR_CUDA.
  */
 typedef struct {
     int32_t num_pairs;

@@ -237,6 +237,7 @@ struct AxesAppendParams {
 cudaError_t launch_axes_append(const AxesAppendParams& p, cudaStream_t stream);
 
 // Page copies and conversions (oxd_pages.cu).
+constexpr int kMaxPairRows = 65535;  // rows of blocks of one launch, each on pairs in turn
 struct PagePools {
     uint8_t* data[2];        // K, V: bf16 rows or codes
     uint16_t* scales[2];     // nullptr for bf16

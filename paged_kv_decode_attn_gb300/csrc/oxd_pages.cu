@@ -214,11 +214,12 @@ __global__ void __launch_bounds__(kThreads, 8)
     }
 }
 
-// A row of blocks for every pair (the pairs in turn past 65535): K and V in
+// A row of blocks for every pair (the pairs in turn past kMaxPairRows): K and V in
 // turn, slice by slice.
 template <class F>
 cudaError_t launch(F kernel, const CopyPagesParams& p, long long slices, cudaStream_t stream) {
-    const dim3 grid(2 * static_cast<unsigned>(slices), p.n < 1 ? 1 : p.n > 65535 ? 65535 : p.n);
+    const int pairs = p.n < 1 ? 1 : p.n > kMaxPairRows ? kMaxPairRows : p.n;
+    const dim3 grid(2 * static_cast<unsigned>(slices), pairs);
     kernel<<<grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }

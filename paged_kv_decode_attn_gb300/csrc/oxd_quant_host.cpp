@@ -191,9 +191,10 @@ extern "C" oxd_status oxd_copy_pages(const oxd_copy_pages_desc* desc, const oxd_
             return OXD_ERR_INVALID_ARGUMENT;
     }
     if (d.head_dim != kHeadDim || !page_size_ok(d.page_size)) return OXD_ERR_UNSUPPORTED;
-    // (a page's 16-byte pieces are counted in 32 bits)
+    // (a page's 16-byte pieces are counted in 32 bits, and so are the pairs, in
+    // steps of up to kMaxPairRows)
     if (d.src_num_pages >= (int64_t{1} << 31) || d.dst_num_pages >= (int64_t{1} << 31) ||
-        d.num_kv_heads > (1 << 20))
+        d.num_kv_heads > (1 << 20) || d.num_pairs > INT32_MAX - kMaxPairRows)
         return OXD_ERR_UNSUPPORTED;
     if (!pools_aligned(*src) || !pools_aligned(*dst) || !aligned(src_pages, 4) ||
         !aligned(dst_pages, 4) || !aligned(dst_refcount, 4) || !aligned(workspace, 256))

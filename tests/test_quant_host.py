@@ -212,3 +212,11 @@ def test_reserved_fields_must_be_zero():
     desc.reserved[1] = 1
     assert status(lambda: oxd.oxd_copy_pages(desc, oxd.KvPools(at(0), at(1)), oxd.KvPools(at(2), at(3)),
                                              at(6), at(7), None, at(9), 256, stream=0)) == 1
+
+
+@pytest.mark.parametrize("n", [2 ** 31 - 65534, 2 ** 31 - 1])
+def test_copy_refuses_lists_its_counter_cannot_walk(n):
+    # (far pools, so that nothing overlaps a list of 8 GB)
+    desc = oxd.make_copy_pages_desc(n, 2, 16, "bf16", "NHD", 30, "bf16", "NHD", 20)
+    assert status(lambda: oxd.oxd_copy_pages(desc, oxd.KvPools(at(0), at(1)), oxd.KvPools(at(2), at(3)),
+                                             at(6), at(7), None, at(9), 256, stream=0)) == 2
