@@ -614,8 +614,9 @@ oxd_status oxd_quant_decode_run(oxd_plan plan, const void* q, const oxd_kv_pools
  * A rope position outside [0, 2^24) counts as OXD_DEVICE_BAD_POSITION: the
  * token's K/V rows are not written (its q_out rows are rotated at the low 24
  * bits). Everything else as oxd_rope_append, the errors too; num_axes outside
- * [1, 4] or a pair_axis entry not below num_axes is OXD_ERR_INVALID_ARGUMENT,
- * more than 2^20 heads OXD_ERR_UNSUPPORTED.
+ * [1, 4], a pair_axis entry not below num_axes or an array in another device's
+ * memory than the calling thread's current one is OXD_ERR_INVALID_ARGUMENT, more
+ * than 2^20 heads OXD_ERR_UNSUPPORTED.
  */
 typedef struct {
     int32_t num_tokens;     /* T */
@@ -678,7 +679,8 @@ oxd_status oxd_quant_rope_append(const oxd_axes_append_desc* desc, const void* q
  * num_pairs = 0 is allowed. A pair with an index outside its pool copies
  * nothing and records OXD_DEVICE_BAD_PAGE; the other pairs are copied.
  * Host-side errors (nothing enqueued): OXD_ERR_INVALID_ARGUMENT (NULL, sizes,
- * formats, scales of a bf16 cache not NULL), OXD_ERR_UNSUPPORTED (head_dim,
+ * formats, scales of a bf16 cache not NULL, an array in another device's memory
+ * than the calling thread's current one), OXD_ERR_UNSUPPORTED (head_dim,
  * page size, more than 2^20 heads or 2^31 - 65536 pairs), OXD_ERR_ALIGNMENT,
  * OXD_ERR_ALIAS, OXD_ERR_WORKSPACE_TOO_SMALL, OXD_ERR_CUDA.
  */

@@ -1,10 +1,12 @@
 // C entries of the multi-axis append, the 4-bit append and the page copies:
 // operand checks and one launch each.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstddef>
 #include <cstring>
+#include <initializer_list>
 
 #include "../../include/oxd.h"
 #include "oxd_host_util.h"
@@ -17,16 +19,46 @@ namespace {
 bool page_size_ok(int ps) { return ps == 8 || ps == 16 || ps == 32 || ps == 64; }
 bool layout_ok(int l) { return l == OXD_LAYOUT_NHD || l == OXD_LAYOUT_HND; }
 
-// A tensor that lives on a device other than the calling thread's current one
-// is refused before a kernel on the wrong device touches it.
-bool on_current_device(const void* p) {
-    cudaPointerAttributes a;
+typedef CUresult (*PointerAttributeFn)(void*, CUpointer_attribute, CUdeviceptr);
+
+PointerAttributeFn pointer_attribute() {
+    static const PointerAttributeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuPointerGetAttribute", &p, 12000,
+                                                         cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return reinterpret_cast<PointerAttributeFn>(ok ? p : nullptr);
+    }();
+    return fn;
+}
+
+// A call with device memory of another device than the calling thread's current
+// one among its arrays (NULL ones aside) is refused before a kernel on the wrong
+// device touches it; managed memory, and memory the driver does not know, is
+// taken. One attribute of the driver's is 32 ns an array, the runtime's 55.
+bool on_current_device(std::initializer_list<const void*> arrays) {
     int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess || cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+    if (cudaGetDevice(&cur) != cudaSuccess) {
         cudaGetLastError();
         return true;  // no device to be wrong about: the launch reports it
     }
-    return a.type != cudaMemoryTypeDevice || a.device == cur;
+    const PointerAttributeFn attribute = pointer_attribute();
+    for (const void* p : arrays) {
+        int dev = -1;
+        if (p == nullptr ||
+            (attribute != nullptr &&
+             attribute(&dev, CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL,
+                       reinterpret_cast<CUdeviceptr>(p)) == CUDA_SUCCESS &&
+             dev == cur))
+            continue;
+        cudaPointerAttributes a;
+        if (cudaPointerGetAttributes(&a, p) != cudaSuccess)
+            cudaGetLastError();
+        else if (a.type == cudaMemoryTypeDevice && a.device != cur)
+            return false;
+    }
+    return true;
 }
 
 // The arrays of one cache: K, V and, in 4 bits, their scales.
@@ -103,7 +135,10 @@ oxd_status axes_append(const oxd_axes_append_desc* desc, const void* q, const vo
         for (int j = 0; j < i; ++j)
             if (overlap(outs[i], outs[j])) return OXD_ERR_ALIAS;
     }
-    if (!on_current_device(q)) return OXD_ERR_INVALID_ARGUMENT;
+    if (!on_current_device({q, k, v, token_request, positions, rope_positions, indptr, indices,
+                            page_refcount, q_out, pools.k, pools.v, e2m1 ? pools.k_scales : nullptr,
+                            e2m1 ? pools.v_scales : nullptr, workspace}))
+        return OXD_ERR_INVALID_ARGUMENT;
 
     AxesAppendParams p{};
     p.q = static_cast<const uint16_t*>(q);
@@ -224,7 +259,10 @@ extern "C" oxd_status oxd_copy_pages(const oxd_copy_pages_desc* desc, const oxd_
         for (int j = 0; j < from.n && !same; ++j)
             if (overlap(to.s[i], from.s[j])) return OXD_ERR_ALIAS;
     }
-    if (!on_current_device(dst->k)) return OXD_ERR_INVALID_ARGUMENT;
+    if (!on_current_device({src->k, src->v, src->k_scales, src->v_scales, dst->k, dst->v,
+                            dst->k_scales, dst->v_scales, src_pages, dst_pages, dst_refcount,
+                            workspace}))
+        return OXD_ERR_INVALID_ARGUMENT;
 
     CopyPagesParams p{};
     auto pools = [](const oxd_kv_pools& c, int64_t pages, int layout) {
