@@ -80,6 +80,36 @@ bool pools_aligned(const oxd_kv_pools& p) {
            aligned(p.v_scales, 16);
 }
 
+// A number as the sum of two doubles, good to about 2^-104.
+struct Double2 {
+    double hi, lo;
+};
+Double2 operator*(Double2 a, Double2 b) {
+    const double p = a.hi * b.hi;
+    const double e = std::fma(a.hi, b.hi, -p) + std::fma(a.hi, b.lo, a.lo * b.hi);
+    const double hi = p + e;
+    return {hi, e - (hi - p)};
+}
+
+// The frequencies theta^(-2i/128) / (2 pi), in turns a position, each as the sum
+// of three floats: a far position (below 2^24) times a double's rounding, 2^-53,
+// would be 2^-29 of a turn's angle, past what the kernel's rotation is good to.
+// r = theta^(-1/64) comes from pow by one Newton step on r^64 theta = 1.
+void frequencies(double theta, float4* turns) {
+    const double r0 = std::pow(theta, -1.0 / 64);
+    Double2 w = {r0, 0.0};
+    for (int i = 0; i < 6; ++i) w = w * w;
+    w = w * Double2{theta, 0.0};
+    const Double2 r = {r0, r0 * (((1.0 - w.hi) - w.lo) / 64)};
+    Double2 g = {0.15915494309189535, -9.839338337591243e-18};  // 1 / (2 pi)
+    for (int i = 0; i < kHeadDim / 2; ++i, g = g * r) {
+        turns[i].x = static_cast<float>(g.hi);
+        const double rest = g.hi - turns[i].x;
+        turns[i].y = static_cast<float>(rest);
+        turns[i].z = static_cast<float>((rest - turns[i].y) + g.lo);
+    }
+}
+
 oxd_status axes_append(const oxd_axes_append_desc* desc, const void* q, const void* k,
                        const void* v, const int32_t* token_request, const int32_t* positions,
                        const int32_t* rope_positions, const int32_t* indptr,
@@ -167,15 +197,10 @@ oxd_status axes_append(const oxd_axes_append_desc* desc, const void* q, const vo
     p.layout = d.layout;
     p.num_indices = d.num_indices;
     p.num_pages = d.num_pages;
+    frequencies(d.rope_theta, p.turns);
     for (int i = 0; i < kHeadDim / 2; ++i) {
-        const double g = std::pow(d.rope_theta, -2.0 * i / kHeadDim) /
-                         6.283185307179586476925286766559;
         const int32_t axis = rope_positions != nullptr ? d.pair_axis[i] : 0;
-        float4& f = p.turns[i];
-        f.x = static_cast<float>(g);
-        f.y = static_cast<float>(g - f.x);
-        f.z = static_cast<float>(g - f.x - f.y);
-        std::memcpy(&f.w, &axis, sizeof(axis));
+        std::memcpy(&p.turns[i].w, &axis, sizeof(axis));
     }
     if (launch_axes_append(p, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return OXD_ERR_CUDA;

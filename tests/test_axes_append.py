@@ -1,4 +1,6 @@
 """Multi-axis rotary append into bf16 and 4-bit pages on the GPU against the f64 reference."""
+from decimal import Decimal, localcontext
+
 import numpy as np
 import pytest
 import torch
@@ -319,5 +321,31 @@ def test_infinite_and_overflowing_keys_are_held_as_the_formats_ends(T):
         if np.isfinite(x):
             j.k[t, 0, [col, col + 64]] = x * rng.choice([-1, 1], 2)
     assert np.isnan(j.rotated(j.k)).sum() == 0
+    assert j.run() == 0
+    j.check()
+
+
+def far_rotation(x, rope, pair_axis, theta):
+    """As R.rotate, the angles reduced in whole numbers: good to 2^-52 at any position."""
+    with localcontext() as c:
+        c.prec = 60
+        pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+        turn = 1 << 120
+        f = [int((-Decimal(theta).ln() * i / 64).exp() / (2 * pi) * turn) for i in range(64)]
+    part = np.array([[int(p) * f[i] % turn / turn for i, p in enumerate(row)]
+                     for row in np.asarray(rope)[np.asarray(pair_axis)].T])
+    cos, sin = np.cos(2 * np.pi * part)[:, None], np.sin(2 * np.pi * part)[:, None]
+    lo, hi = x[..., :64], x[..., 64:]
+    return np.concatenate([lo * cos - hi * sin, hi * cos + lo * sin], -1)
+
+
+@pytest.mark.parametrize("theta", [10000.0, 5e6])
+def test_codes_at_the_farthest_positions(theta):
+    """Every code and scale is the exactly rotated row's up to position 2^24 - 1."""
+    j = Job([0], [2500], 1, 5, 16, "HND", 2, True, seed=33)
+    j.theta = theta
+    j.rope = np.random.default_rng(34).integers(1 << 23, 1 << 24, (2, j.T))
+    j.rope[:, :4] = (1 << 24) - 1 - np.arange(8).reshape(2, 4)
+    j.rotated = lambda x: far_rotation(x, j.rope, j.pair_axis, theta)
     assert j.run() == 0
     j.check()

@@ -1,9 +1,11 @@
 """The host side of the appends and the page copies over a stand-in for the device
-(``tests/fakes/quant_host.cpp``): which device a call's tensors may be on."""
+(``tests/fakes/quant_host.cpp``): which device a call's tensors may be on, and the frequencies of the
+rotation."""
 import ctypes
 import importlib
 import os
 import subprocess
+from decimal import Decimal, localcontext
 
 import pytest
 
@@ -74,3 +76,23 @@ def test_managed_memory_and_memory_of_no_device_is_taken(fake, call, used):
     for i in used[True][1:]:
         fake.fake_allocate(at(i), GAP, 0, MANAGED)
     assert call(fake, True) == 0 and fake.fake_launches() == 1
+
+
+PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+@pytest.mark.parametrize("theta", [10000.0, 500000.0, 5e6, 1e9, 1.5, 1.0000001, 12345.678])
+def test_frequencies_hold_up_to_the_farthest_position(fake, theta):
+    """Three floats hold 72 bits: within 2^-70 of the frequency, a turn's angle at position 2^24 is
+    good to 2^-43. (A double's 2^-53 would leave 2^-29, where the rotation is good to 2^-32.)"""
+    d = oxd.make_axes_append_desc(10, 3, 8, 2, 16, "NHD", 50, 20, rope_theta=theta, sections=(16, 24, 24))
+    fake.fake_reset(0)
+    assert fake.oxd_rope_axes_append(ctypes.addressof(d), *[at(i) for i in range(12)], at(14), 256,
+                                     None) == 0
+    got = fake.fake_turns()
+    with localcontext() as c:
+        c.prec = 50
+        for i in range(64):
+            want = (-Decimal(theta).ln() * i / 64).exp() / (2 * PI)
+            have = sum((Decimal(got[4 * i + j]) for j in range(3)), Decimal(0))
+            assert abs(have - want) <= want * Decimal(2) ** -70, i
