@@ -747,6 +747,26 @@ cudaError_t quant_occupancy(int variant, int* n) {
         n, quant_decode_kernel<C, WorkList, false>, kThreads, C::kSmemBytes);
 }
 
+cudaError_t quant_resident_clusters(int size, int* n) {
+    using C = QCfg<16>;
+    const cudaError_t e = ensure_smem<C, WorkList, true>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytesCluster;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(n, quant_decode_kernel<C, WorkList, true>, &cfg);
+}
+
+int quant_cluster_ctas_per_sm() { return 228 * 1024 / (QCfg<16>::kSmemBytesCluster + 1024); }
+
 cudaError_t launch_decode_quant(int variant, const QuantDecodeParams& p, const WorkList* w,
                                 int grid, cudaStream_t stream, bool pdl) {
     if (variant != kVariantQuant8)

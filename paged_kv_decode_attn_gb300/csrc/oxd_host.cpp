@@ -423,6 +423,16 @@ oxd_status plan_decode(const oxd_paged_decode_desc* desc, const int32_t* indptr,
     std::vector<Piece> pieces;
     std::vector<int> cta_of;  // CTA index of each piece, non-decreasing after ordering
     int grid = 0;
+    auto resident_clusters = [&](int size) -> int64_t {  // of the 4-bit decode
+        if (plan_device < 0)
+            return static_cast<int64_t>(num_sms) * quant_cluster_ctas_per_sm() / size;
+        int prev = 0, n = 0;
+        if (cudaGetDevice(&prev) != cudaSuccess || cudaSetDevice(plan_device) != cudaSuccess)
+            return 0;
+        const cudaError_t e = quant_resident_clusters(size, &n);
+        cudaSetDevice(prev);
+        return e == cudaSuccess ? n : 0;
+    };
     // How to cut a batch whose split the planner chooses. Measured on one GPU
     // (step times of small batches): a stream's pieces cost about a stage of
     // streaming (~1 us) each when a CTA runs alone, the separate merge about
@@ -456,21 +466,29 @@ oxd_status plan_decode(const oxd_paged_decode_desc* desc, const int32_t* indptr,
         const int64_t line_grid = std::max<int64_t>(
             1, std::min<int64_t>(resident, std::max<int64_t>(streamed * H / stage_tokens, live)));
         const double share = static_cast<double>(streamed) * H / line_grid;
-        // 4-bit: a stage of a lone CTA takes about 0.45 us and the merge launch
-        // 3.5, so a longest stream up to seven stages above the share runs whole.
+        // 4-bit: a lone CTA streams a stage in about 0.45 us and the merge launch
+        // costs 3.5, so a longest stream up to seven stages above the share runs
+        // whole.
         whole_streams =
             live <= resident &&
             (quant ? static_cast<double>(longest) <= share + 7.0 * stage_tokens
                    : longest <= 2 * stage_tokens && static_cast<double>(longest) <= share + 160.0);
         const int64_t n_streams = static_cast<int64_t>(B) * H;
-        // 4-bit: a stage takes a lone CTA 1.3 us (a warp's chunk from load to
-        // product), a cluster's merge about one, so pieces of one stage.
+        // 4-bit: from load to product a stage takes a lone CTA 1.3 us (the stages of
+        // its ring overlap, which is the 0.45 us above), a cluster's merge about
+        // one, so pieces of one stage; in as many CTAs a stream as let every
+        // cluster be resident at once, as its instance holds the pieces' states too
+        // and fits a SM half as often, and a cluster fits a GPC or waits. 64 streams
+        // of 1024 tokens: 9.4 us in clusters of 4 and 13.7 of 8, which come in two
+        // waves (a line 10.0); of 4000 tokens 16.0 and 20.9 (a line 15.8, and 12 us
+        // for its upload unless the workspace is bound).
         if (quant && variant == kVariantQuant8 && heads == 1 && n_streams <= 64 &&
             longest > stage_tokens) {
-            const int C = static_cast<int>(
-                std::min<int64_t>({kMaxClusterCtas, min_pages, resident / n_streams,
-                                   (longest + stage_tokens - 1) / stage_tokens}));
-            if (C >= 2 && (longest + C - 1) / C <= 4 * stage_tokens) {
+            int C = static_cast<int>(std::min<int64_t>(
+                {kMaxClusterCtas, min_pages, (longest + stage_tokens - 1) / stage_tokens}));
+            const bool short_pieces = C >= 2 && (longest + C - 1) / C <= 4 * stage_tokens;
+            while (C >= 2 && resident_clusters(C) < n_streams) --C;
+            if (C >= 2 && short_pieces) {
                 cluster_c = C;
                 whole_streams = false;
             }

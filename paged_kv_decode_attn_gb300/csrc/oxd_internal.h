@@ -205,6 +205,10 @@ cudaError_t quant_wide_occupancy(int variant, int* ctas_per_sm);
 cudaError_t launch_decode_quant_wide(int variant, const QuantDecodeParams& p, const WorkList* w,
                                      int grid, cudaStream_t stream, bool pdl);
 cudaError_t quant_occupancy(int variant, int* ctas_per_sm);
+// Clusters of `size` CTAs of the instance whose first CTA merges (groups of up to 8
+// heads) that are resident at once; without a device, its CTAs a SM by shared memory.
+cudaError_t quant_resident_clusters(int size, int* n);
+int quant_cluster_ctas_per_sm();
 cudaError_t launch_decode_quant(int variant, const QuantDecodeParams& p, const WorkList* w,
                                 int grid, cudaStream_t stream, bool pdl);
 

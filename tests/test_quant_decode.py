@@ -380,3 +380,15 @@ def test_two_runs_of_one_plan_at_once(G):
     for o, l, ws in runs:
         assert oxd.oxd_read_device_status(ws) == 0
         assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("n,Hkv", [(5, 8), (6, 8), (7, 8), (8, 8), (37, 1)])
+def test_clusters_of_every_size_that_fits(n, Hkv):
+    """37 to 64 streams: as many CTAs a stream as are resident at once, odd numbers among them."""
+    c = Cache([1024, 129, 1000, 512, 700, 1023, 333, 64][:n] + [1024] * (n - 8), 4, Hkv, 16, "HND", seed=29)
+    plan, out, lse = check(c)
+    size = plan.info.cluster_size
+    assert 4 <= size < 8 and plan.info.grid_ctas == size * n * Hkv
+    for _ in range(5):
+        o2, l2, _ = c.run(plan)
+        assert torch.equal(out, o2) and torch.equal(lse, l2)

@@ -220,3 +220,14 @@ def test_copy_refuses_lists_its_counter_cannot_walk(n):
     desc = oxd.make_copy_pages_desc(n, 2, 16, "bf16", "NHD", 30, "bf16", "NHD", 20)
     assert status(lambda: oxd.oxd_copy_pages(desc, oxd.KvPools(at(0), at(1)), oxd.KvPools(at(2), at(3)),
                                              at(6), at(7), None, at(9), 256, stream=0)) == 2
+
+
+@pytest.mark.parametrize("B,Hkv", [(38, 1), (5, 8), (7, 8), (8, 8), (64, 1), (63, 1)])
+@pytest.mark.parametrize("L", [512, 1024, 2048, 4000])
+@pytest.mark.parametrize("num_sms", [152, 100])
+def test_the_clusters_of_a_plan_are_resident_at_once(B, Hkv, L, num_sms):
+    # the instance that merges in its first CTA asks for 80 KB of a SM's 228
+    info = quant_plan([L] * B, Hkv=Hkv, layout="HND", num_sms=num_sms).info
+    assert info.grid_ctas <= 2 * num_sms or info.cluster_size == 0
+    if L == 1024 and num_sms == 152:
+        assert info.cluster_size == 304 // (B * Hkv) and info.launches_per_run == 1
