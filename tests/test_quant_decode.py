@@ -392,3 +392,37 @@ def test_clusters_of_every_size_that_fits(n, Hkv):
     for _ in range(5):
         o2, l2, _ = c.run(plan)
         assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("G", [1, 4, 8, 16, 32])
+def test_a_wait_that_runs_out_does_so(G):
+    """Every CTA's first wait is for query rows that come from memory (L2 holds something else), with
+    a limit of a nanosecond: at least one of the runs says that a wait ran out. The rows are waited
+    for all the same, so each run's outputs are those of a plan without the limit."""
+    n, ps = 600, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    codes = [torch.randint(0, 256, (n, 1, ps, 64), dtype=torch.uint8, device="cuda", generator=g)
+             for _ in "kv"]
+    scales = [torch.rand(n, 1, ps, 4, device="cuda", generator=g).half() for _ in "kv"]
+    q = torch.randn(n, G, 128, device="cuda", generator=g).bfloat16()
+    indptr, last = np.arange(n + 1, dtype=np.int32), np.full(n, ps, np.int32)
+    d = [torch.as_tensor(a, device="cuda") for a in (indptr, indptr[:-1].copy(), last)]
+    out, lse = torch.empty_like(q), torch.empty(n, G, device="cuda")
+    other = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+
+    def run(**kw):
+        plan = oxd.oxd_quant_decode_plan(oxd.make_desc(n, G, 1, ps, "HND", n, **kw), indptr, last)
+        ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+        oxd.oxd_plan_bind_workspace(plan, ws)
+        out.zero_(), lse.zero_(), other.fill_(1)
+        oxd.oxd_quant_decode_run(plan, q, oxd.KvPools(*codes, *scales), *d, 0.1, out, lse, ws)
+        return oxd.oxd_read_device_status(ws)
+
+    assert run() == 0
+    o0, l0 = out.clone(), lse.clone()
+    seen = []
+    for _ in range(10):
+        seen.append(run(wait_timeout_ns=1))
+        assert torch.equal(out, o0) and torch.equal(lse, l0)
+    assert set(seen) <= {0, 3} and 3 in seen, seen
+    assert run() == 0
