@@ -37,12 +37,16 @@ PointerAttributeFn pointer_attribute() {
 // one among its arrays (NULL ones aside) is refused before a kernel on the wrong
 // device touches it; managed memory, and memory the driver does not know, is
 // taken. One attribute of the driver's is 32 ns an array, the runtime's 55.
+// With one device there is nothing to ask.
 bool on_current_device(std::initializer_list<const void*> arrays) {
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess) {
+    static const int devices = [] {
+        int n = 0;
+        if (cudaGetDeviceCount(&n) == cudaSuccess) return n;
         cudaGetLastError();
-        return true;  // no device to be wrong about: the launch reports it
-    }
+        return 0;  // no device to be wrong about: the launch reports it
+    }();
+    int cur = -1;
+    if (devices < 2 || cudaGetDevice(&cur) != cudaSuccess) return true;
     const PointerAttributeFn attribute = pointer_attribute();
     for (const void* p : arrays) {
         int dev = -1;
