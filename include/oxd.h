@@ -590,7 +590,8 @@ oxd_status oxd_quant_decode_plan(const oxd_paged_decode_desc* desc, const int32_
  * score product as f16 scaled by a power of two per head (exact for columns
  * within 2^-14 of the head's largest), codes exactly and K's scales in F32; a
  * V value (code times scale) and a softmax weight are each rounded once to
- * f16, weights below 2^-24 of the largest to multiples of 2^-34 of it.
+ * f16, weights below 2^-24 of the largest to multiples of 2^-34 of it; the
+ * softmax's denominator sums the weights before that rounding.
  * Arguments, errors, status codes and determinism as oxd_paged_decode_run (of
  * the waits, only those for query rows have the plan's limit: the pages come by
  * copies that end by themselves); the four pools of `cache` are read only.
@@ -725,7 +726,9 @@ oxd_status oxd_plan_destroy(oxd_plan plan);
  * Synchronise `stream`, then read into *code the first error the last run
  * that started on `workspace` recorded (OXD_DEVICE_OK if it recorded none). Returns OXD_OK when
  * the code is OXD_DEVICE_OK, OXD_ERR_DEVICE_STATUS otherwise, OXD_ERR_CUDA if
- * the copy failed. This is the one call that blocks the host.
+ * the copy failed. This is the one call that blocks the host. The replays of a
+ * captured call count as one run: a code that one of them recorded is read after
+ * later ones too.
  */
 oxd_status oxd_read_device_status(const void* workspace, void* stream, int32_t* code);
 

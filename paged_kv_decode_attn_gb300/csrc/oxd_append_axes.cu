@@ -7,11 +7,12 @@
 // A call reads q, k and v once and writes q_out and the page rows once, so
 // bytes bound it (long calls) or the chain position -> page -> refcount (a
 // decode step). A block of eight warps takes four tokens (one in short calls,
-// which spreads them over the SMs; for a 16384-token prompt into 4-bit pages one,
-// two and eight tokens a block take 129, 101 and 88 us where four take 86). Its threads form the tokens'
-// 64 cosines and sines each, one pair a thread, which all of a token's heads
-// share (formed per row in double, they were the whole cost); then each warp takes rows of one token, four at a time,
-// eight lanes a row: lane s of a row holds columns 8s .. 8s + 7 and 64 + 8s ..
+// which spreads them over the SMs; a 16384-token prompt of 32 and 8 heads into
+// 4-bit pages takes 111, 77, 65 and 68 us with one, two, four and eight tokens a
+// block). Its threads form the tokens' 64 cosines and sines each, one pair a
+// thread, which all of a token's heads share (formed per row in double, they were
+// the whole cost); then each warp takes rows of one token, four at a time, eight
+// lanes a row: lane s of a row holds columns 8s .. 8s + 7 and 64 + 8s ..
 // (two 16-byte loads), so a rotation pairs values of one lane, a 4-bit group
 // of 32 is four lanes, and a row's 8 cosines stay in registers.
 //
@@ -402,9 +403,13 @@ cudaError_t launch(const AxesAppendParams& p, cudaStream_t stream) {
 cudaError_t launch_axes_append(const AxesAppendParams& p, cudaStream_t stream) {
     if (p.T < 1) return cudaErrorInvalidConfiguration;
     // Four tokens a block form their angles with every thread; a call of few
-    // tokens spreads each over a block of its own.
+    // tokens spreads each over a block of its own while these are all resident at
+    // once, four on each of the GB300's 152 SMs (608 tokens of 32 and 8 heads into
+    // 4-bit pages 7.4 us, in fours 7.9; 700 tokens 10.7 and 8.7; bf16 pages 6.4 and
+    // 7.1, 8.3 and 7.5).
+    constexpr int kResidentBlocks = 152 * 4;
     const bool k4 = p.k_scales != nullptr;
-    if (p.T <= 152 * 4) return k4 ? launch<true, 1>(p, stream) : launch<false, 1>(p, stream);
+    if (p.T <= kResidentBlocks) return k4 ? launch<true, 1>(p, stream) : launch<false, 1>(p, stream);
     return k4 ? launch<true, 4>(p, stream) : launch<false, 4>(p, stream);
 }
 

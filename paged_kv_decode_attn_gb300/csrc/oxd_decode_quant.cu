@@ -32,10 +32,10 @@
 // first CTA merges the pieces' states from its shared memory.
 //
 // HBM bounds long streams: 8 heads x 8, 256 requests U{128..16384}, NHD, 414 us
-// or 5.9 TB/s, 88 % of the copy rate (HND 403 us); between the ends of units the
-// stream runs at 97 %. A unit's end costs 2.9 us (4 heads) to 3.6 (8), which is
-// what log-normal batches pay: 84 us, 71 %. One request of 512 tokens, 8 KV heads:
-// 8.2 us, dependent latencies of one launch.
+// or 5.9 TB/s, 87 % of the copy rate (HND 403 us); between the ends of units the
+// stream runs at 97 %. A unit's end costs 2.9 us (4 heads) to 3.6 (8), a part of
+// what log-normal batches pay: 80 to 90 us, 66 to 75 %. One request of 512 tokens,
+// 8 KV heads: 8.2 us, dependent latencies of one launch.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -54,8 +54,9 @@ template <int kPs>  // page size
 struct QCfg {
     static constexpr int kRows = 8;    // query heads: one N tile
     static constexpr int kStages = 2;  // slots of a warp's ring
-    // Resident CTAs a SM, which caps the registers at 128. (Three with 168
-    // registers and longer rings: the same steady rate, slower short streams.)
+    // Resident CTAs a SM, which caps the registers at 128: most instances spill 24
+    // to 48 bytes. (Three with 168 registers and longer rings: the same steady rate,
+    // slower short streams.)
     static constexpr int kCtas = 4;
     static constexpr int kPageSize = kPs;
     static constexpr int kPagesPerChunk = kPs < kChunk ? kChunk / kPs : 1;

@@ -11,8 +11,9 @@
 //     halves the weights P go through shared memory: one barrier a stage.
 // One kernel for every group was measured: for up to 8 heads the other runs the
 // steady stream 1.25 times faster (no barriers, fewer instructions a token), for
-// 16 and 32 this one ends a unit in half the time and holds its registers. What
-// bounds it is issue and latency: 3 to 4 warps a scheduler at half their rate,
+// 16 and 32 this one ends a unit in half the time and keeps its accumulators in
+// registers (spilled: up to 24 bytes for 16 heads, 28 to 76 for 32). What bounds
+// it is issue and latency: 3 to 4 warps a scheduler at half their rate,
 // mma.sync at 38 % of its own (32 heads, 16 x 32768 tokens: 45 to 47 us, 25 % of
 // the copy rate; four CTAs a SM with a shorter ring 57; 16 heads 3.0 TB/s). On
 // tcgen05, a token a thread and K as the A operand in tensor memory, the same

@@ -108,8 +108,8 @@ __device__ __forceinline__ float2 f16x2_floats(uint32_t h) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Byte offset of the codes of (page, token t, head h), and index of the row's
-// first scale.
+// Index of the row of (page, token t, head h) in a pool of rows (codes or bf16),
+// and of the row's first scale.
 __device__ __forceinline__ size_t row_index(int layout, int64_t page, int t, int h, int H, int ps) {
     return layout == 0 ? (static_cast<size_t>(page) * ps + t) * H + h
                        : (static_cast<size_t>(page) * H + h) * ps + t;
