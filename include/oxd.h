@@ -79,7 +79,9 @@ typedef enum {
 #define OXD_DEVICE_PLAN_MISMATCH 2  /* device indptr/last_page_len differ from the plan's */
 #define OXD_DEVICE_WAIT_TIMEOUT 3   /* an internal pipeline wait gave up (about 1 s) */
 #define OXD_DEVICE_SHARED_PAGE 4    /* an append or copy targeted a page whose reference count is not 1 */
-#define OXD_DEVICE_BAD_POSITION 5   /* an append's request or position lies outside its table */
+#define OXD_DEVICE_BAD_POSITION 5   /* an append's request or position lies outside its table, or a
+                                       length, count or table entry outside its bounds */
+#define OXD_DEVICE_NO_PAGES 6       /* oxd_build_tables ran out of free pages */
 
 typedef struct oxd_plan_s* oxd_plan; /* opaque, host-owned, immutable after planning */
 
@@ -703,6 +705,160 @@ oxd_status oxd_copy_pages(const oxd_copy_pages_desc* desc, const oxd_kv_pools* s
                           const oxd_kv_pools* dst, const int32_t* src_pages,
                           const int32_t* dst_pages, const int32_t* dst_refcount,
                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ sliding window
+ *
+ * Attention in which a query sees the last tokens of its request and a few first
+ * ones: a query at position p sees the cached tokens j <= p with j > p - window
+ * (the window, the query's own token included) or j < sinks (the first tokens,
+ * which stay visible). Decode and prefill over the same pages and block tables,
+ * and the tables themselves built on the GPU, so that a serving step needs no
+ * host copy of the lengths. (The source pages name attention sinks and sliding
+ * windows as open, "Domain coverage", and print nothing more.)
+ *
+ * Pages that no query of a call sees are never read, nor is their entry of
+ * `indices`: a pager may hand them to another request and list anything there,
+ * -1 say. Rows of a visible page that no query sees (before the window, behind
+ * the last token) may hold anything, NaN too.
+ */
+
+/*
+ * Enqueue one decode step with a window on `stream`: for the last token of every
+ * request (position L_b - 1, its K and V already in the pages),
+ *   out[b, hq, :] = sum_j softmax_j(sm_scale * q[b, hq, :] . k_j) v_j
+ *   lse[b, hq]    = ln sum_j exp(sm_scale * q[b, hq, :] . k_j)
+ * over the tokens j that it sees. There is no plan: the work of a request is at
+ * most window + sinks tokens, the launch is sized by that, and the lengths are
+ * read on the device, so a captured call may be replayed as requests grow (the
+ * tables change in place), end and begin. A request without pages
+ * (indptr[b] == indptr[b+1]) gets out = 0 and lse = -inf.
+ *
+ *   desc          shapes, see below
+ *   q, out        device bf16 [B][Hq][128], 16-byte aligned
+ *   k_pages, v_pages  device bf16 pools in desc's layout, 16-byte aligned
+ *   indptr, indices, last_page_len  device int32 block tables as for decode;
+ *                 indices holds desc->num_indices entries
+ *   sm_scale      finite
+ *   lse           device f32 [B][Hq] or NULL
+ *   workspace     device, >= 256 bytes, 256-byte aligned, any contents: the
+ *                 status word, read with oxd_read_device_status
+ * Numerics as the bf16 decode (QK^T and PV on tensor cores for every group).
+ * The same call gives bitwise the same results.
+ * Host-side errors (nothing enqueued): OXD_ERR_INVALID_ARGUMENT (NULL, sizes,
+ * window < 1, sinks < 0, an array in another device's memory than the calling
+ * thread's current one), OXD_ERR_UNSUPPORTED (head_dim, page size, G > 32,
+ * window + sinks above 2^30, pools of 2^32 (token, head) rows or more, more than
+ * 2^25 (request, KV head) pairs), OXD_ERR_ALIGNMENT, OXD_ERR_ALIAS (out, lse and
+ * workspace must not overlap each other or any input),
+ * OXD_ERR_WORKSPACE_TOO_SMALL, OXD_ERR_CUDA. Device-side: a visible page's index
+ * outside the pool is recorded as OXD_DEVICE_BAD_PAGE and read as page 0; a
+ * request whose indptr entries are negative, decreasing or past num_indices,
+ * whose last_page_len is outside [1, page_size] or that has more than 2^30
+ * tokens is recorded as OXD_DEVICE_BAD_POSITION and sees nothing. The other
+ * requests are unaffected.
+ */
+typedef struct {
+    int32_t batch;          /* B >= 1 */
+    int32_t num_qo_heads;   /* Hq */
+    int32_t num_kv_heads;   /* Hkv; Hq % Hkv == 0, G = Hq / Hkv <= 32 */
+    int32_t head_dim;       /* 128 */
+    int32_t page_size;      /* 8, 16, 32 or 64 */
+    int32_t layout;         /* oxd_kv_layout */
+    int32_t num_indices;    /* entries of `indices` */
+    int32_t window;         /* >= 1: tokens a query sees up to its own */
+    int32_t sinks;          /* >= 0: first tokens that stay visible */
+    int32_t max_splits;     /* 0: the launch picks how many CTAs (at most 16, one cluster)
+                               share a request and KV head; n: at most n */
+    int64_t num_pages;      /* pages in each pool */
+    int32_t pdl;            /* 1: launched as a programmatic dependent of the kernel
+                               before it on the stream, as for oxd_paged_decode_desc */
+    int32_t reserved[2];    /* must be zero */
+} oxd_window_decode_desc;
+
+oxd_status oxd_window_decode(const oxd_window_decode_desc* desc, const void* q,
+                             const void* k_pages, const void* v_pages, const int32_t* indptr,
+                             const int32_t* indices, const int32_t* last_page_len,
+                             float sm_scale, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * The same over a 4-bit cache: out and lse as oxd_window_decode computes them for
+ * the values the cache stands for, with the numerics of oxd_quant_decode_run.
+ */
+oxd_status oxd_quant_window_decode(const oxd_window_decode_desc* desc, const void* q,
+                                   const oxd_kv_pools* cache, const int32_t* indptr,
+                                   const int32_t* indices, const int32_t* last_page_len,
+                                   float sm_scale, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * Block tables and token maps of one step, built on the GPU from the requests'
+ * lengths: what the appends, the decodes and the prefill run from.
+ *
+ * Request b holds lengths[b] tokens with this step's, of which the last
+ * new_tokens[b] are new. Its pages, in order, are listed in row b of page_rows:
+ * held[b] of them so far. With need = ceil(lengths[b] / page_size):
+ *   - pages held[b] .. need - 1, where there are any, are taken from free_pages,
+ *     in the order of requests and pages, from entry *taken on; they are written
+ *     into the row, and their page_refcount becomes 1;
+ *   - held_out[b] = max(held[b], need), *taken_out = *taken + the pages taken
+ *     (a request keeps the pages of tokens that it drops, for when it grows again);
+ *   - indptr, indices, last_page_len: the CSR tables of the need pages of every
+ *     request (last_page_len 0 for a request without tokens). With window > 0, a
+ *     page that no new token's query sees (nor, without new tokens, the last
+ *     token's) is listed as -1;
+ *   - qo_indptr, token_request, positions: the new tokens, request by request in
+ *     order of position, as the appends and the prefill take them;
+ *   - slots: where each goes, page * page_size + position % page_size.
+ * Entries of token_request, positions and slots behind the last new token are -1;
+ * entries of indices behind indptr[B] are left as they were.
+ *
+ *   lengths, new_tokens  device int32 [B] (new_tokens may be NULL: none are new)
+ *   page_rows     device int32 [B][row_pages], updated in place
+ *   held, held_out    device int32 [B]; held_out may be held itself
+ *   free_pages    device int32 [num_free]; NULL with num_free = 0
+ *   taken, taken_out  device int32 [1]; taken_out may be taken itself; NULL with
+ *                 num_free = 0
+ *   page_refcount device int32 [num_pages] or NULL
+ *   indptr [B+1], indices [num_indices], last_page_len [B]  device int32
+ *   qo_indptr [B+1], token_request, positions [num_tokens]  device int32, and
+ *   slots [num_tokens]  device int64, which may be NULL; none of them is written,
+ *                 and they may be NULL, with num_tokens = 0
+ *   workspace     device, >= 256 bytes, 256-byte aligned: the status word
+ * Host-side errors (nothing enqueued): OXD_ERR_INVALID_ARGUMENT (NULL, sizes, an
+ * array in another device's memory than the calling thread's current one),
+ * OXD_ERR_UNSUPPORTED (page size; batch * row_pages * page_size, num_free,
+ * num_indices, num_tokens, window or sinks above 2^30), OXD_ERR_ALIGNMENT,
+ * OXD_ERR_ALIAS (an output overlaps an input or another output, but for held_out
+ * and taken_out as above), OXD_ERR_WORKSPACE_TOO_SMALL, OXD_ERR_CUDA.
+ * Device-side: a request whose length, count of new tokens or held pages is
+ * outside its bounds (negative, more new tokens than tokens, more pages than
+ * row_pages) is listed as empty and recorded as OXD_DEVICE_BAD_POSITION, and so
+ * is a *taken outside [0, num_free] (nothing is taken then) and a table longer
+ * than num_indices or num_tokens (cut off there). Where the free list ends,
+ * pages are listed as -1 and not counted as held (OXD_DEVICE_NO_PAGES); a free
+ * page outside the pool is listed as it is (OXD_DEVICE_BAD_PAGE).
+ */
+typedef struct {
+    int32_t batch;          /* B >= 1 */
+    int32_t page_size;      /* 8, 16, 32 or 64 */
+    int32_t row_pages;      /* entries of a row of page_rows */
+    int32_t num_indices;    /* entries of indices */
+    int32_t num_tokens;     /* entries of the token maps; 0: none are written */
+    int32_t num_free;       /* entries of free_pages */
+    int32_t window;         /* 0: every page is listed; else as for oxd_window_decode */
+    int32_t sinks;
+    int64_t num_pages;      /* pages in the pool (and entries of page_refcount) */
+    int64_t reserved;       /* must be zero */
+} oxd_build_tables_desc;
+
+oxd_status oxd_build_tables(const oxd_build_tables_desc* desc, const int32_t* lengths,
+                            const int32_t* new_tokens, int32_t* page_rows, const int32_t* held,
+                            int32_t* held_out, const int32_t* free_pages, const int32_t* taken,
+                            int32_t* taken_out, int32_t* page_refcount, int32_t* indptr,
+                            int32_t* indices, int32_t* last_page_len, int32_t* qo_indptr,
+                            int32_t* token_request, int32_t* positions, int64_t* slots,
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 /* Planner decisions of a plan (host only). */
 oxd_status oxd_plan_get_info(oxd_plan plan, oxd_plan_info* info);

@@ -16,6 +16,8 @@ The functions keep the C names:
 * the 4-bit cache: :func:`oxd_quant_decode_plan` -> :class:`Plan`,
   :func:`oxd_quant_decode_run`, :func:`oxd_quant_rope_append`
 * :func:`oxd_copy_pages` (pages copied and converted between caches)
+* sliding windows: :func:`oxd_window_decode`, :func:`oxd_quant_window_decode` (no plan),
+  and the tables built on the GPU for them, :func:`oxd_build_tables`
 * :func:`oxd_plan_get_info`, :func:`oxd_plan_set_timing_events`,
   :func:`oxd_plan_destroy`, :func:`oxd_read_device_status`,
   :func:`oxd_status_string`, :func:`oxd_device_status_string`, :func:`oxd_version`
@@ -50,6 +52,8 @@ __all__ = [
     "OXD_FORMAT_BF16", "OXD_FORMAT_E2M1", "KvPools", "AxesAppendDesc", "make_axes_append_desc",
     "CopyPagesDesc", "make_copy_pages_desc", "oxd_quant_decode_plan", "oxd_quant_decode_run",
     "oxd_rope_axes_append", "oxd_quant_rope_append", "oxd_copy_pages",
+    "WindowDecodeDesc", "make_window_decode_desc", "oxd_window_decode",
+    "oxd_quant_window_decode", "BuildTablesDesc", "make_build_tables_desc", "oxd_build_tables",
 ]
 
 OXD_OK = 0
@@ -75,6 +79,7 @@ OXD_DEVICE_PLAN_MISMATCH = 2
 OXD_DEVICE_WAIT_TIMEOUT = 3
 OXD_DEVICE_SHARED_PAGE = 4
 OXD_DEVICE_BAD_POSITION = 5
+OXD_DEVICE_NO_PAGES = 6
 
 EXPORTED_SYMBOLS = (
     "oxd_paged_decode_plan", "oxd_paged_decode_run", "oxd_merge_states", "oxd_plan_get_info",
@@ -87,6 +92,7 @@ EXPORTED_SYMBOLS = (
     "oxd_prefill_plan_destroy",
     "oxd_quant_decode_plan", "oxd_quant_decode_run", "oxd_rope_axes_append",
     "oxd_quant_rope_append", "oxd_copy_pages",
+    "oxd_window_decode", "oxd_quant_window_decode", "oxd_build_tables",
 )
 
 
@@ -210,6 +216,32 @@ class CopyPagesDesc(ctypes.Structure):
     ]
 
 
+class WindowDecodeDesc(ctypes.Structure):
+    """``oxd_window_decode_desc``."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("num_qo_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("layout", ctypes.c_int32),
+        ("num_indices", ctypes.c_int32), ("window", ctypes.c_int32),
+        ("sinks", ctypes.c_int32), ("max_splits", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64), ("pdl", ctypes.c_int32),
+        ("reserved", ctypes.c_int32 * 2),
+    ]
+
+
+class BuildTablesDesc(ctypes.Structure):
+    """``oxd_build_tables_desc``."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("row_pages", ctypes.c_int32), ("num_indices", ctypes.c_int32),
+        ("num_tokens", ctypes.c_int32), ("num_free", ctypes.c_int32),
+        ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64), ("reserved", ctypes.c_int64),
+    ]
+
+
 class KvPools:
     """The pools of one cache (``oxd_kv_pools``): tensors or addresses. bf16 pools
     have no scales; a 4-bit cache's ``k`` and ``v`` are its codes. The tensors are
@@ -253,6 +285,24 @@ def make_copy_pages_desc(num_pairs, num_kv_heads, page_size, src_format, src_lay
                          formats.get(src_format, src_format), layouts.get(src_layout, src_layout),
                          formats.get(dst_format, dst_format), layouts.get(dst_layout, dst_layout),
                          src_num_pages, dst_num_pages, (ctypes.c_int32 * 2)(0, 0))
+
+
+def make_window_decode_desc(batch, num_qo_heads, num_kv_heads, page_size, layout, num_pages,
+                            num_indices, window, sinks=0, head_dim=128, max_splits=0,
+                            pdl=0) -> WindowDecodeDesc:
+    """Convenience constructor; ``layout`` may be "NHD"/"HND" or 0/1."""
+    if isinstance(layout, str):
+        layout = {"NHD": OXD_LAYOUT_NHD, "HND": OXD_LAYOUT_HND}[layout]
+    return WindowDecodeDesc(batch, num_qo_heads, num_kv_heads, head_dim, page_size, layout,
+                            num_indices, window, sinks, max_splits, num_pages, pdl,
+                            (ctypes.c_int32 * 2)(0, 0))
+
+
+def make_build_tables_desc(batch, page_size, row_pages, num_pages, num_indices, num_tokens=0,
+                           num_free=0, window=0, sinks=0) -> BuildTablesDesc:
+    """Convenience constructor; ``window`` 0 lists every page of a request."""
+    return BuildTablesDesc(batch, page_size, row_pages, num_indices, num_tokens, num_free, window,
+                           sinks, num_pages, 0)
 
 
 def make_prefill_desc(batch, num_qo_heads, num_kv_heads, page_size, layout, num_pages,
@@ -312,6 +362,11 @@ def lib():
             L.oxd_rope_axes_append.argtypes = [ctypes.POINTER(AxesAppendDesc)] + [vp] * 13 + [sz, vp]
             L.oxd_quant_rope_append.argtypes = [ctypes.POINTER(AxesAppendDesc)] + [vp] * 12 + [sz, vp]
             L.oxd_copy_pages.argtypes = [ctypes.POINTER(CopyPagesDesc)] + [vp] * 6 + [sz, vp]
+            L.oxd_window_decode.argtypes = ([ctypes.POINTER(WindowDecodeDesc)] + [vp] * 6
+                                            + [ctypes.c_float, vp, vp, vp, sz, vp])
+            L.oxd_quant_window_decode.argtypes = ([ctypes.POINTER(WindowDecodeDesc)] + [vp] * 5
+                                                  + [ctypes.c_float, vp, vp, vp, sz, vp])
+            L.oxd_build_tables.argtypes = [ctypes.POINTER(BuildTablesDesc)] + [vp] * 17 + [sz, vp]
             L.oxd_read_device_status.argtypes = [vp, vp, ctypes.POINTER(i32)]
             L.oxd_read_static_workspace_status.argtypes = [vp, ctypes.POINTER(i32)]
             for f in ("oxd_paged_decode_plan", "oxd_paged_decode_run",
@@ -323,7 +378,8 @@ def lib():
                       "oxd_prefill_plan_bind_workspace", "oxd_prefill_plan_get_info",
                       "oxd_prefill_plan_set_timing_events", "oxd_prefill_plan_destroy",
                       "oxd_quant_decode_plan", "oxd_quant_decode_run", "oxd_rope_axes_append",
-                      "oxd_quant_rope_append", "oxd_copy_pages"):
+                      "oxd_quant_rope_append", "oxd_copy_pages", "oxd_window_decode",
+                      "oxd_quant_window_decode", "oxd_build_tables"):
                 getattr(L, f).restype = ctypes.c_int
             L.oxd_status_string.argtypes = [ctypes.c_int]
             L.oxd_status_string.restype = ctypes.c_char_p
@@ -712,3 +768,49 @@ def oxd_copy_pages(desc: CopyPagesDesc, src: KvPools, dst: KvPools, src_pages, d
         _addr(dst_pages), _addr(dst_refcount), _addr(workspace), int(workspace_bytes),
         _stream(stream, workspace))
     _check("oxd_copy_pages", st)
+
+
+# ------------------------------------------------------------------ sliding window
+
+def oxd_window_decode(desc: WindowDecodeDesc, q, k_pages, v_pages, indptr, indices, last_page_len,
+                      sm_scale, out, lse, workspace, workspace_bytes=None, stream=None) -> None:
+    """Enqueue one decode step with a sliding window (see ``oxd_window_decode`` in
+    include/oxd.h); the lengths are read on the device, there is no plan."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.nbytes
+    st = lib().oxd_window_decode(
+        ctypes.byref(desc), _addr(q), _addr(k_pages), _addr(v_pages), _addr(indptr),
+        _addr(indices), _addr(last_page_len), float(sm_scale), _addr(out), _addr(lse),
+        _addr(workspace), int(workspace_bytes), _stream(stream, q))
+    _check("oxd_window_decode", st)
+
+
+def oxd_quant_window_decode(desc: WindowDecodeDesc, q, cache: KvPools, indptr, indices,
+                            last_page_len, sm_scale, out, lse, workspace, workspace_bytes=None,
+                            stream=None) -> None:
+    """Enqueue one decode step with a sliding window over a 4-bit cache (see
+    ``oxd_quant_window_decode`` in include/oxd.h)."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.nbytes
+    st = lib().oxd_quant_window_decode(
+        ctypes.byref(desc), _addr(q), ctypes.byref(cache.struct), _addr(indptr), _addr(indices),
+        _addr(last_page_len), float(sm_scale), _addr(out), _addr(lse), _addr(workspace),
+        int(workspace_bytes), _stream(stream, q))
+    _check("oxd_quant_window_decode", st)
+
+
+def oxd_build_tables(desc: BuildTablesDesc, lengths, new_tokens, page_rows, held, held_out,
+                     free_pages, taken, taken_out, page_refcount, indptr, indices, last_page_len,
+                     qo_indptr, token_request, positions, slots, workspace, workspace_bytes=None,
+                     stream=None) -> None:
+    """Enqueue the tables of one step, built from the requests' lengths (see
+    ``oxd_build_tables`` in include/oxd.h)."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.nbytes
+    st = lib().oxd_build_tables(
+        ctypes.byref(desc), _addr(lengths), _addr(new_tokens), _addr(page_rows), _addr(held),
+        _addr(held_out), _addr(free_pages), _addr(taken), _addr(taken_out), _addr(page_refcount),
+        _addr(indptr), _addr(indices), _addr(last_page_len), _addr(qo_indptr),
+        _addr(token_request), _addr(positions), _addr(slots), _addr(workspace),
+        int(workspace_bytes), _stream(stream, lengths))
+    _check("oxd_build_tables", st)

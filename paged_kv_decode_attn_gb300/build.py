@@ -18,12 +18,15 @@ LIB = os.path.join(LIBDIR, "liboxd.so")
 HEADERS = [os.path.join(ROOT, "include", "oxd.h")] + [
     os.path.join(CSRC, h) for h in ("oxd_internal.h", "oxd_merge_row.cuh", "oxd_ptx.cuh",
                                     "oxd_tcgen05.cuh", "oxd_prefill.h", "oxd_host_util.h",
-                                    "oxd_e2m1.cuh", "oxd_decode_quant.cuh")]
+                                    "oxd_e2m1.cuh", "oxd_decode_quant.cuh",
+                                    "oxd_decode_quant_state.cuh", "oxd_cache_host.h",
+                                    "oxd_window.cuh")]
 SOURCES = ["oxd_host.cpp", "oxd_decode.cu", "oxd_decode_wide.cu", "oxd_merge.cu",
            "oxd_noalloc.cu", "oxd_append.cu", "oxd_prefill.cu", "oxd_prefill_narrow.cu",
            "oxd_prefill_host.cpp", "oxd_decode_quant.cu", "oxd_decode_quant_wide.cu",
            "oxd_append_axes.cu", "oxd_pages.cu",
-           "oxd_quant_host.cpp"]
+           "oxd_quant_host.cpp", "oxd_window_decode.cu", "oxd_window_quant.cu", "oxd_tables.cu",
+           "oxd_window_host.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

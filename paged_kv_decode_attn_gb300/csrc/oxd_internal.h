@@ -261,6 +261,62 @@ struct CopyPagesParams {
 };
 cudaError_t launch_copy_pages(const CopyPagesParams& p, cudaStream_t stream);
 
+// Decode with a sliding window (oxd_window_decode.cu, oxd_window_quant.cu).
+constexpr int kMaxWindowTokens = 1 << 30;  // tokens of a request, and window + sinks
+constexpr int kMaxWindowSplits = 16;       // CTAs of a cluster that share a stream
+struct WindowParams {
+    const uint16_t* q;           // bf16 [B][Hq][128]
+    const uint8_t* k;            // rows (bf16 or codes) of the pools
+    const uint8_t* v;
+    const uint16_t* k_scales;    // 4-bit cache, else nullptr
+    const uint16_t* v_scales;
+    const int32_t* indptr;
+    const int32_t* indices;
+    const int32_t* last_page_len;
+    uint16_t* out;
+    float* lse;
+    unsigned long long* status;
+    uint32_t* last_epoch;
+    uint32_t epoch;
+    int32_t batch, num_qo_heads, num_kv_heads, group;
+    int32_t page_shift;          // log2 of the page size
+    int32_t layout;
+    int32_t num_indices;
+    int32_t window, sinks;
+    int32_t splits;              // CTAs a stream: the cluster's size
+    int32_t heads;               // 4-bit cache: KV heads a CTA takes (1 or 2)
+    int64_t num_pages;
+    float scale_log2;
+};
+cudaError_t launch_window_decode(WindowParams p, int max_splits, cudaStream_t stream, bool pdl);
+cudaError_t launch_window_quant(WindowParams p, int max_splits, cudaStream_t stream, bool pdl);
+
+// Block tables and token maps from request lengths (oxd_tables.cu).
+struct TablesParams {
+    const int32_t* lengths;
+    const int32_t* new_tokens;   // or nullptr: none
+    int32_t* rows;               // [batch][row_pages]
+    const int32_t* held;
+    int32_t* held_out;
+    const int32_t* free_pages;
+    const int32_t* taken;
+    int32_t* taken_out;
+    int32_t* refcount;           // or nullptr
+    int32_t* indptr;
+    int32_t* indices;
+    int32_t* last_page_len;
+    int32_t* qo_indptr;          // or nullptr, as the next three
+    int32_t* token_request;
+    int32_t* positions;
+    int64_t* slots;
+    unsigned long long* status;
+    uint32_t* last_epoch;
+    uint32_t epoch;
+    int32_t batch, page_shift, row_pages, num_indices, num_tokens, num_free, window, sinks;
+    int64_t num_pages;
+};
+cudaError_t launch_build_tables(const TablesParams& p, cudaStream_t stream);
+
 // Uniform-state merge (the public entry point).
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream);
 // Merge of the split (request, KV head) streams of a decode run, launched
