@@ -476,7 +476,8 @@ typedef struct {
     int64_t workspace_bytes;
     int64_t total_q_tokens;
     int64_t total_kv_tokens;
-    int64_t causal_pairs;       /* (query token, cached token) pairs per query head */
+    int64_t causal_pairs;       /* (query token, cached token) pairs per query head that the
+                                   mask leaves */
 } oxd_prefill_plan_info;
 
 /*
@@ -790,6 +791,26 @@ oxd_status oxd_quant_window_decode(const oxd_window_decode_desc* desc, const voi
                                    const int32_t* indices, const int32_t* last_page_len,
                                    float sm_scale, void* out, float* lse, void* workspace,
                                    size_t workspace_bytes, void* stream);
+
+/*
+ * Plan a causal prefill with a window: as oxd_paged_prefill_plan, but query token
+ * i of request b, at position p = L_b - q_len_b + i, sees the tokens j <= p with
+ * j > p - window or j < sinks. The plan is an oxd_prefill_plan like any other:
+ * oxd_paged_prefill_run enqueues it (out, lse, workspace, errors and status codes
+ * as there), oxd_prefill_plan_bind_workspace, _get_info (causal_pairs counts the
+ * pairs that the window leaves), _set_timing_events and _destroy take it.
+ * Of a tile's pages those that none of its queries sees are neither looked up nor
+ * copied. A row of K and V that no query of the call sees may hold anything; one
+ * that some query sees has to be finite for the others' sake (a masked row of V
+ * enters the product with weight 0, as in the prefill without a window).
+ * Errors: as oxd_paged_prefill_plan, and OXD_ERR_INVALID_ARGUMENT for window < 1
+ * or sinks < 0, OXD_ERR_UNSUPPORTED for window + sinks above 2^30.
+ */
+oxd_status oxd_window_prefill_plan(const oxd_paged_prefill_desc* desc, int32_t window,
+                                   int32_t sinks, const int32_t* qo_indptr,
+                                   const int32_t* indptr, const int32_t* last_page_len,
+                                   int device, oxd_prefill_plan* plan_out,
+                                   size_t* workspace_bytes);
 
 /*
  * Block tables and token maps of one step, built on the GPU from the requests'

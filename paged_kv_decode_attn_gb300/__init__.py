@@ -17,7 +17,8 @@ The functions keep the C names:
   :func:`oxd_quant_decode_run`, :func:`oxd_quant_rope_append`
 * :func:`oxd_copy_pages` (pages copied and converted between caches)
 * sliding windows: :func:`oxd_window_decode`, :func:`oxd_quant_window_decode` (no plan),
-  and the tables built on the GPU for them, :func:`oxd_build_tables`
+  :func:`oxd_window_prefill_plan` (run by :func:`oxd_paged_prefill_run`), and the tables
+  built on the GPU for them, :func:`oxd_build_tables`
 * :func:`oxd_plan_get_info`, :func:`oxd_plan_set_timing_events`,
   :func:`oxd_plan_destroy`, :func:`oxd_read_device_status`,
   :func:`oxd_status_string`, :func:`oxd_device_status_string`, :func:`oxd_version`
@@ -53,7 +54,7 @@ __all__ = [
     "CopyPagesDesc", "make_copy_pages_desc", "oxd_quant_decode_plan", "oxd_quant_decode_run",
     "oxd_rope_axes_append", "oxd_quant_rope_append", "oxd_copy_pages",
     "WindowDecodeDesc", "make_window_decode_desc", "oxd_window_decode",
-    "oxd_quant_window_decode", "BuildTablesDesc", "make_build_tables_desc", "oxd_build_tables",
+    "oxd_quant_window_decode", "oxd_window_prefill_plan", "BuildTablesDesc", "make_build_tables_desc", "oxd_build_tables",
 ]
 
 OXD_OK = 0
@@ -92,7 +93,8 @@ EXPORTED_SYMBOLS = (
     "oxd_prefill_plan_destroy",
     "oxd_quant_decode_plan", "oxd_quant_decode_run", "oxd_rope_axes_append",
     "oxd_quant_rope_append", "oxd_copy_pages",
-    "oxd_window_decode", "oxd_quant_window_decode", "oxd_build_tables",
+    "oxd_window_decode", "oxd_quant_window_decode", "oxd_window_prefill_plan",
+    "oxd_build_tables",
 )
 
 
@@ -352,6 +354,8 @@ def lib():
             L.oxd_plan_destroy.argtypes = [vp]
             L.oxd_paged_prefill_plan.argtypes = [ctypes.POINTER(PrefillDesc), vp, vp, vp,
                                                  ctypes.c_int, vp, vp]
+            L.oxd_window_prefill_plan.argtypes = [ctypes.POINTER(PrefillDesc), i32, i32, vp, vp, vp,
+                                                  ctypes.c_int, vp, vp]
             L.oxd_paged_prefill_run.argtypes = [vp] * 8 + [ctypes.c_float, vp, vp, vp, sz, vp]
             L.oxd_prefill_plan_bind_workspace.argtypes = [vp, vp, sz, vp]
             L.oxd_prefill_plan_get_info.argtypes = [vp, ctypes.POINTER(PrefillPlanInfo)]
@@ -379,7 +383,7 @@ def lib():
                       "oxd_prefill_plan_set_timing_events", "oxd_prefill_plan_destroy",
                       "oxd_quant_decode_plan", "oxd_quant_decode_run", "oxd_rope_axes_append",
                       "oxd_quant_rope_append", "oxd_copy_pages", "oxd_window_decode",
-                      "oxd_quant_window_decode", "oxd_build_tables"):
+                      "oxd_quant_window_decode", "oxd_window_prefill_plan", "oxd_build_tables"):
                 getattr(L, f).restype = ctypes.c_int
             L.oxd_status_string.argtypes = [ctypes.c_int]
             L.oxd_status_string.restype = ctypes.c_char_p
@@ -654,23 +658,36 @@ class PrefillPlan:
             pass
 
 
-def oxd_paged_prefill_plan(desc: PrefillDesc, qo_indptr_host, indptr_host, last_page_len_host,
-                           device: int = 0) -> PrefillPlan:
-    """Plan a causal prefill from host tables; returns a :class:`PrefillPlan`."""
+def _plan_prefill(name, desc: PrefillDesc, extra, qo_indptr_host, indptr_host, last_page_len_host,
+                  device) -> PrefillPlan:
     qo = np.ascontiguousarray(np.asarray(qo_indptr_host), dtype=np.int32)
     indptr = np.ascontiguousarray(np.asarray(indptr_host), dtype=np.int32)
     last = np.ascontiguousarray(np.asarray(last_page_len_host), dtype=np.int32)
     if (qo.shape != (desc.batch + 1,) or indptr.shape != (desc.batch + 1,)
             or last.shape != (desc.batch,)):
-        raise OxdError("oxd_paged_prefill_plan", OXD_ERR_INVALID_ARGUMENT,
+        raise OxdError(name, OXD_ERR_INVALID_ARGUMENT,
                        "qo_indptr and indptr must be [batch+1], last_page_len [batch]")
     h = ctypes.c_void_p()
     ws = ctypes.c_size_t()
-    st = lib().oxd_paged_prefill_plan(ctypes.byref(desc), qo.ctypes.data, indptr.ctypes.data,
-                                      last.ctypes.data, int(device), ctypes.byref(h),
-                                      ctypes.byref(ws))
-    _check("oxd_paged_prefill_plan", st)
+    st = getattr(lib(), name)(ctypes.byref(desc), *extra, qo.ctypes.data, indptr.ctypes.data,
+                              last.ctypes.data, int(device), ctypes.byref(h), ctypes.byref(ws))
+    _check(name, st)
     return PrefillPlan(h.value, ws.value, desc)
+
+
+def oxd_paged_prefill_plan(desc: PrefillDesc, qo_indptr_host, indptr_host, last_page_len_host,
+                           device: int = 0) -> PrefillPlan:
+    """Plan a causal prefill from host tables; returns a :class:`PrefillPlan`."""
+    return _plan_prefill("oxd_paged_prefill_plan", desc, (), qo_indptr_host, indptr_host,
+                         last_page_len_host, device)
+
+
+def oxd_window_prefill_plan(desc: PrefillDesc, window, sinks, qo_indptr_host, indptr_host,
+                            last_page_len_host, device: int = 0) -> PrefillPlan:
+    """Plan a causal prefill whose queries see a window of their last tokens and the first
+    ``sinks`` ones; run it with :func:`oxd_paged_prefill_run`."""
+    return _plan_prefill("oxd_window_prefill_plan", desc, (int(window), int(sinks)),
+                         qo_indptr_host, indptr_host, last_page_len_host, device)
 
 
 def oxd_paged_prefill_run(plan, q, k_pages, v_pages, qo_indptr, indptr, indices, last_page_len,

@@ -20,7 +20,7 @@ HEADERS = [os.path.join(ROOT, "include", "oxd.h")] + [
                                     "oxd_tcgen05.cuh", "oxd_prefill.h", "oxd_host_util.h",
                                     "oxd_e2m1.cuh", "oxd_decode_quant.cuh",
                                     "oxd_decode_quant_state.cuh", "oxd_cache_host.h",
-                                    "oxd_window.cuh")]
+                                    "oxd_window.cuh", "oxd_prefill_window.cuh")]
 SOURCES = ["oxd_host.cpp", "oxd_decode.cu", "oxd_decode_wide.cu", "oxd_merge.cu",
            "oxd_noalloc.cu", "oxd_append.cu", "oxd_prefill.cu", "oxd_prefill_narrow.cu",
            "oxd_prefill_host.cpp", "oxd_decode_quant.cu", "oxd_decode_quant_wide.cu",

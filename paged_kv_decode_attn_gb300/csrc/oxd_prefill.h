@@ -74,7 +74,25 @@ struct PrefillParams {
     int32_t wait_prior;             // 1: launched early behind another grid, which must
                                     // complete before this one does (griddepcontrol.wait)
     int64_t wait_ns;                // limit of a pipeline wait (> 0)
+    int32_t window;                 // 0: no window; else a query at position p sees tokens
+    int32_t sinks;                  // j > p - window or j < sinks
 };
+
+// The stages (of `stage` tokens) that a tile whose first query sits at p0 streams
+// under a window: those with sinks, then those from the first token that its window
+// holds on. Stage v of them is stage v of the request, or v + skip from `front` on.
+// A piece's kv_begin is its first stage's place in the request, its kv_valid and
+// n_pages count without the skipped ones.
+struct WindowStages {
+    int32_t front, skip;
+};
+__host__ __device__ inline WindowStages window_stages(int window, int sinks, int p0, int stage) {
+    const int lo = p0 >= window ? p0 - window + 1 : 0;
+    WindowStages w;
+    w.front = (sinks + stage - 1) / stage;
+    w.skip = lo / stage > w.front ? lo / stage - w.front : 0;
+    return w;
+}
 
 cudaError_t prefill_smem_bytes(int* bytes);
 cudaError_t prefill_occupancy(int* ctas_per_sm);

@@ -33,6 +33,7 @@ using namespace oxd;
 struct oxd_prefill_plan_s {
     oxd_paged_prefill_desc desc;
     int device;  // -1: host-only plan
+    int window, sinks;  // window 0: none
     int group;
     bool narrow;  // 128-row tiles on the narrow kernel, else 256-row tiles
     int tile_tokens;
@@ -97,13 +98,19 @@ void free_plan(oxd_prefill_plan P) {
     delete P;
 }
 
-}  // namespace
+// (query, token) pairs of queries at positions [p0, p1), each of which sees its
+// window and the sinks.
+int64_t window_pairs(int64_t p0, int64_t p1, int64_t window, int64_t sinks) {
+    // positions below window + sinks see everything up to themselves, the others the sum
+    const int64_t most = window + sinks;
+    const int64_t mid = std::max(p0, std::min(p1, most));
+    return (mid - p0) * (p0 + mid + 1) / 2 + (p1 - mid) * most;
+}
 
-extern "C" {
-
-oxd_status oxd_paged_prefill_plan(const oxd_paged_prefill_desc* desc, const int32_t* qo_indptr,
-                                  const int32_t* indptr, const int32_t* last, int device,
-                                  oxd_prefill_plan* plan_out, size_t* ws_out) {
+// The planner of oxd_paged_prefill_plan (window 0) and oxd_window_prefill_plan.
+oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sinks,
+                        const int32_t* qo_indptr, const int32_t* indptr, const int32_t* last,
+                        int device, oxd_prefill_plan* plan_out, size_t* ws_out) {
     if (desc == nullptr || qo_indptr == nullptr || indptr == nullptr || last == nullptr ||
         plan_out == nullptr || ws_out == nullptr)
         return OXD_ERR_INVALID_ARGUMENT;
@@ -113,7 +120,7 @@ oxd_status oxd_paged_prefill_plan(const oxd_paged_prefill_desc* desc, const int3
     const int B = d.batch, ps = d.page_size, H = d.num_kv_heads;
     const int G = d.num_qo_heads / H;
     if (qo_indptr[0] != 0 || indptr[0] < 0) return OXD_ERR_INVALID_ARGUMENT;
-    int64_t total_kv = 0, pairs = 0;
+    int64_t total_kv = 0, pairs = 0, longest = 0;
     for (int b = 0; b < B; ++b) {
         const int64_t P = static_cast<int64_t>(indptr[b + 1]) - indptr[b];
         const int64_t q = static_cast<int64_t>(qo_indptr[b + 1]) - qo_indptr[b];
@@ -122,8 +129,12 @@ oxd_status oxd_paged_prefill_plan(const oxd_paged_prefill_desc* desc, const int3
         if (q > L) return OXD_ERR_INVALID_ARGUMENT;
         if (L >= (int64_t{1} << 30)) return OXD_ERR_UNSUPPORTED;
         total_kv += L;
-        pairs += q * (L - q) + q * (q + 1) / 2;
+        pairs += window > 0 ? window_pairs(L - q, L, window, sinks)
+                            : q * (L - q) + q * (q + 1) / 2;
+        longest = std::max(longest, L);
     }
+    // a window that holds every request whole is none
+    if (window >= longest) window = 0;
     const int64_t nq = qo_indptr[B];
     if (nq * d.num_qo_heads >= (int64_t{1} << 31) || static_cast<int64_t>(indptr[B]) < 1)
         return OXD_ERR_UNSUPPORTED;
@@ -145,8 +156,10 @@ oxd_status oxd_paged_prefill_plan(const oxd_paged_prefill_desc* desc, const int3
             const int q_len = qo_indptr[b + 1] - qo_indptr[b];
             const int64_t L = static_cast<int64_t>(indptr[b + 1] - indptr[b] - 1) * ps + last[b];
             for (int qt = 0; qt * Tr < q_len; ++qt) {
-                const int64_t kv_end = L - q_len + qt * Tr + std::min(Tr, q_len - qt * Tr);
-                n += H * ((kv_end + stage - 1) / stage);
+                const int p0 = static_cast<int>(L - q_len + qt * Tr);
+                const int kv_end = p0 + std::min(Tr, q_len - qt * Tr);
+                const int skip = window > 0 ? window_stages(window, sinks, p0, stage).skip : 0;
+                n += static_cast<int64_t>(H) * ((kv_end + stage - 1) / stage - skip);
             }
         }
         return n;
@@ -181,8 +194,11 @@ oxd_status oxd_paged_prefill_plan(const oxd_paged_prefill_desc* desc, const int3
     // ---- tiles: up to T query tokens of one request with the G heads of one
     // KV head; a tile streams its request's cached tokens up to the position
     // of its last query token.
+    // With a window it skips the stages between the sinks and its first query's
+    // window.
     struct Tile {
         int b, hkv, q0, n_tok, p0, stages, kv_end;
+        WindowStages w;
     };
     std::vector<Tile> tiles;
     int64_t total_stages = 0;
@@ -193,9 +209,11 @@ oxd_status oxd_paged_prefill_plan(const oxd_paged_prefill_desc* desc, const int3
             const int n_tok = std::min(T, q_len - qt * T);
             const int p0 = static_cast<int>(L - q_len + qt * T);
             const int kv_end = p0 + n_tok;
-            const int stages = (kv_end + stage_tokens - 1) / stage_tokens;
+            const WindowStages w = window > 0 ? window_stages(window, sinks, p0, stage_tokens)
+                                              : WindowStages{0, 0};
+            const int stages = (kv_end + stage_tokens - 1) / stage_tokens - w.skip;
             for (int h = 0; h < H; ++h) {
-                tiles.push_back({b, h, qo_indptr[b] + qt * T, n_tok, p0, stages, kv_end});
+                tiles.push_back({b, h, qo_indptr[b] + qt * T, n_tok, p0, stages, kv_end, w});
                 total_stages += stages;
             }
         }
@@ -237,8 +255,10 @@ oxd_status oxd_paged_prefill_plan(const oxd_paged_prefill_desc* desc, const int3
             const int s0 = static_cast<int>(static_cast<int64_t>(t.stages) * i / S);
             const int s1 = static_cast<int>(static_cast<int64_t>(t.stages) * (i + 1) / S);
             PrefillUnit u{};
-            u.kv_begin = s0 * stage_tokens;
-            u.kv_valid = std::min(t.kv_end, s1 * stage_tokens) - u.kv_begin;
+            u.kv_begin = (s0 + (s0 >= t.w.front ? t.w.skip : 0)) * stage_tokens;
+            u.kv_valid = (s1 - s0) * stage_tokens;
+            if (s1 == t.stages)  // its last stage ends at the last query token
+                u.kv_valid -= (s1 + t.w.skip) * stage_tokens - t.kv_end;
             u.idx_begin = indptr[t.b] + u.kv_begin / ps;
             u.n_pages = (u.kv_valid + ps - 1) / ps;
             u.q_begin = t.q0;
@@ -264,6 +284,8 @@ oxd_status oxd_paged_prefill_plan(const oxd_paged_prefill_desc* desc, const int3
     oxd_prefill_plan P = new (std::nothrow) oxd_prefill_plan_s();
     if (P == nullptr) return OXD_ERR_NO_MEMORY;
     P->desc = d;
+    P->window = window;
+    P->sinks = sinks;
     P->device = plan_device;
     P->group = G;
     P->narrow = narrow;
@@ -320,6 +342,25 @@ oxd_status oxd_paged_prefill_plan(const oxd_paged_prefill_desc* desc, const int3
     *plan_out = P;
     *ws_out = P->ws_bytes;
     return OXD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+oxd_status oxd_paged_prefill_plan(const oxd_paged_prefill_desc* desc, const int32_t* qo_indptr,
+                                  const int32_t* indptr, const int32_t* last, int device,
+                                  oxd_prefill_plan* plan_out, size_t* ws_out) {
+    return plan_prefill(desc, 0, 0, qo_indptr, indptr, last, device, plan_out, ws_out);
+}
+
+oxd_status oxd_window_prefill_plan(const oxd_paged_prefill_desc* desc, int32_t window,
+                                   int32_t sinks, const int32_t* qo_indptr, const int32_t* indptr,
+                                   const int32_t* last, int device, oxd_prefill_plan* plan_out,
+                                   size_t* ws_out) {
+    if (window < 1 || sinks < 0) return OXD_ERR_INVALID_ARGUMENT;
+    if (static_cast<int64_t>(window) + sinks > kMaxWindowTokens) return OXD_ERR_UNSUPPORTED;
+    return plan_prefill(desc, window, sinks, qo_indptr, indptr, last, device, plan_out, ws_out);
 }
 
 oxd_status oxd_prefill_plan_get_info(oxd_prefill_plan plan, oxd_prefill_plan_info* info) {
@@ -488,6 +529,8 @@ oxd_status oxd_paged_prefill_run(oxd_prefill_plan plan, const void* q, const voi
     p.num_pages = d.num_pages;
     p.scale_log2 = sm_scale * 1.4426950408889634f;  // log2(e)
     p.wait_ns = d.wait_timeout_ns > 0 ? d.wait_timeout_ns : kWaitTimeoutNs;
+    p.window = plan->window;
+    p.sinks = plan->sinks;
 
     if (plan->ev_before != nullptr && cudaEventRecord(plan->ev_before, s) != cudaSuccess)
         return OXD_ERR_CUDA;

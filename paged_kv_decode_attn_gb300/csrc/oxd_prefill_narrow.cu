@@ -43,6 +43,7 @@
 
 #include "oxd_internal.h"
 #include "oxd_prefill.h"
+#include "oxd_prefill_window.cuh"
 #include "oxd_ptx.cuh"
 #include "oxd_tcgen05.cuh"
 
@@ -82,6 +83,11 @@ struct PCtl {
 // so no alignment slack: two CTAs fit one SM.
 constexpr int kPSmemBytes = kPCtlOff + static_cast<int>(sizeof(PCtl));
 
+using Window = TileWindow<kNarrowStageTokens>;
+
+// kWindow: queries see a window of their last tokens and the sinks (an instantiation
+// of its own, so its code does not weigh on the other).
+template <bool kWindow>
 __global__ void __launch_bounds__(kPThreads)
     paged_prefill_narrow_kernel(const __grid_constant__ CUtensorMap tmap_k,
                          const __grid_constant__ CUtensorMap tmap_v,
@@ -144,6 +150,14 @@ __global__ void __launch_bounds__(kPThreads)
                       static_cast<int64_t>(u.n_tok - 1) * u.n_pieces + u.piece + 1) *
                              G <=
                          p.n_states;
+            if constexpr (kWindow) {
+                if (ok) {
+                    Window w;
+                    w.init(p, u);
+                    ok = w.inside(u, (u.kv_valid + kNarrowStageTokens - 1) / kNarrowStageTokens,
+                                  kNarrowStageTokens / ps, p.nnz);
+                }
+            }
         } else {
             ok = 0;
         }
@@ -176,6 +190,8 @@ __global__ void __launch_bounds__(kPThreads)
     PrefillUnit u{};
     if (usable) u = p.units[blockIdx.x];
     const int n_st = usable ? (u.kv_valid + kNarrowStageTokens - 1) / kNarrowStageTokens : 0;
+    Window win_t;
+    if constexpr (kWindow) win_t.init(p, u);
 
     if (warp >= 5) {
         // ================================================ producer warps
@@ -185,7 +201,9 @@ __global__ void __launch_bounds__(kPThreads)
         const int pps = kNarrowStageTokens / ps;  // pages per stage (divides 32)
         const int32_t* idx = p.indices + u.idx_begin;
         int win = 0, nxt = 0, win_base = 0;
-        if (n_st > 0) {
+        if constexpr (kWindow) {
+            nxt = window_page(win_t, p, u, 0, n_st, lane);
+        } else if (n_st > 0) {
             if (lane < u.n_pages) win = __ldg(idx + lane);
             if (32 + lane < u.n_pages) nxt = __ldg(idx + 32 + lane);
         }
@@ -195,7 +213,7 @@ __global__ void __launch_bounds__(kPThreads)
                 record_status(p.status, p.epoch, kDeviceBadPage);
             win = bad ? 0 : win;  // an index outside the pool reads page 0
         };
-        if (n_st > 0) check_window();
+        if (!kWindow && n_st > 0) check_window();
         const int n_slots = is_k ? kPKStages : kPVStages;
         uint64_t* full = is_k ? ctl.kfull : ctl.vfull;
         uint64_t* empty = is_k ? ctl.kempty : ctl.vempty;
@@ -208,7 +226,13 @@ __global__ void __launch_bounds__(kPThreads)
             const int slot = s % n_slots;
             const int pg0 = s * pps;
             const int npg = min(pps, u.n_pages - pg0);
-            if (pg0 >= win_base + 32) {
+            if constexpr (kWindow) {
+                win = nxt;  // the stage's pages, a lane's own; the next stage's are read now
+                nxt = window_page(win_t, p, u, s + 1, n_st, lane);
+                if (__any_sync(0xffffffffu, win < 0) && lane == 0)
+                    record_status(p.status, p.epoch, kDeviceBadPage);
+                win = max(win, 0);
+            } else if (pg0 >= win_base + 32) {
                 win = nxt;
                 win_base += 32;
                 nxt = win_base + 32 + lane < u.n_pages ? __ldg(idx + win_base + 32 + lane) : 0;
@@ -230,7 +254,8 @@ __global__ void __launch_bounds__(kPThreads)
                 }
             }
             const int j = lane >> 1;
-            const int page = __shfl_sync(0xffffffffu, win, (pg0 - win_base + j) & 31);
+            const int page =
+                kWindow ? win : __shfl_sync(0xffffffffu, win, (pg0 - win_base + j) & 31);
             if (lane < 2 * npg) {
                 const uint32_t dst = (is_k ? ring_k(slot) : ring_v(slot)) + j * ps * 128 +
                                      ((lane & 1) ? kPHalf : 0);
@@ -332,7 +357,8 @@ __global__ void __launch_bounds__(kPThreads)
         const int r = threadIdx.x;  // 0 .. 127
         const int t = r / G, gi = r - (r / G) * G;
         const bool row_ok = r < G * p.tile_tokens && t < u.n_tok;
-        const int pos = row_ok ? u.p0 + t : (1 << 30);  // padding rows see everything
+        // (padding rows see everything, or with a window what the last query sees)
+        const int pos = row_ok ? u.p0 + t : kWindow ? u.p0 + u.n_tok - 1 : (1 << 30);
         const float sc = p.scale_log2;
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
@@ -344,7 +370,7 @@ __global__ void __launch_bounds__(kPThreads)
             tc_fence_after();
             uint32_t sr[64];
             tmem_ld64(t_s(g & 1) + lane_off, sr);
-            const int base = u.kv_begin + g * kNarrowStageTokens;
+            const int base = kWindow ? win_t.base(g) : u.kv_begin + g * kNarrowStageTokens;
             const int nvalid = min(kNarrowStageTokens, u.kv_valid - g * kNarrowStageTokens);
             // A stage that ends at or before the tile's first position is seen
             // whole by every row (the same for the whole CTA): no mask, the
@@ -352,7 +378,8 @@ __global__ void __launch_bounds__(kPThreads)
             // into the exponent's FMA. Otherwise scores are scaled and masked
             // first.
             const bool whole = nvalid == kNarrowStageTokens &&
-                               base + kNarrowStageTokens - 1 <= u.p0 && sc > 0.f;
+                               base + kNarrowStageTokens - 1 <= u.p0 && sc > 0.f &&
+                               (!kWindow || win_t.whole(base, u.p0 + u.n_tok - 1));
             float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             if (whole) {
 #pragma unroll
@@ -360,10 +387,15 @@ __global__ void __launch_bounds__(kPThreads)
                     mq[(j >> 1) & 3] = max3(mq[(j >> 1) & 3], __uint_as_float(sr[j]),
                                             __uint_as_float(sr[j + 1]));
             } else {
-                const int lim = min(nvalid, pos - base + 1);  // visible columns of this row
+                // visible columns of this row: below lim and, with a window, from w_lo on
+                // or below w_sink
+                const int lim = min(nvalid, pos - base + 1);
+                const int w_lo = kWindow ? pos - win_t.window + 1 - base : 0;
+                const int w_sink = kWindow ? win_t.sinks - base : 0;
 #pragma unroll
                 for (int j = 0; j < 64; ++j) {
-                    const float x = j < lim ? __uint_as_float(sr[j]) * sc : -INFINITY;
+                    const bool v = j < lim && (!kWindow || j >= w_lo || j < w_sink);
+                    const float x = v ? __uint_as_float(sr[j]) * sc : -INFINITY;
                     sr[j] = __float_as_uint(x);
                     mq[j & 3] = fmaxf(mq[j & 3], x);
                 }
@@ -435,8 +467,9 @@ __global__ void __launch_bounds__(kPThreads)
                 tmem_wait_st();
             }
             const bool last = g == n_st - 1;
-            if (last && nvalid < kNarrowStageTokens) {
-                // zero V rows past the piece once its V landed (whole 128-byte
+            if ((last && nvalid < kNarrowStageTokens) || (kWindow && win_t.hides(g))) {
+                // zero V rows that no row sees (past the piece, before the tile's
+                // window) once the stage's V landed (whole 128-byte
                 // rows, so the swizzle does not matter); PV(g - 2) was issued
                 // (QK(g) was), so this phase of vfull is the one for stage g
                 if (!wait_all(&ctl.vfull[g % kPVStages], (g / kPVStages) & 1)) {
@@ -444,12 +477,16 @@ __global__ void __launch_bounds__(kPThreads)
                     break;
                 }
                 uint8_t* v0 = sm + kPVOff + (g % kPVStages) * kPSlotBytes;
-                const int n16 = (kNarrowStageTokens - nvalid) * 16;
-                for (int i = r; i < n16; i += kPSoftmaxThreads) {
-                    const int row = nvalid + (i >> 4), c = i & 15;
-                    *reinterpret_cast<uint4*>(v0 + (c >> 3) * kPHalf + row * 128 + (c & 7) * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
-                }
+                auto zero_rows = [&](int r0, int r1) {
+                    const int n16 = (r1 - r0) * 16;
+                    for (int i = r; i < n16; i += kPSoftmaxThreads) {
+                        const int row = r0 + (i >> 4), c = i & 15;
+                        *reinterpret_cast<uint4*>(v0 + (c >> 3) * kPHalf + row * 128 +
+                                                  (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                };
+                zero_rows(nvalid, kNarrowStageTokens);
+                if constexpr (kWindow) zero_rows(win_t.hidden0(base), win_t.hidden1(base));
                 fence_proxy_async_smem();
             }
             tc_fence_before();
@@ -555,8 +592,11 @@ cudaError_t ensure_narrow_attribute() {
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
     if (bit != 0 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-    e = cudaFuncSetAttribute(paged_prefill_narrow_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kPSmemBytes);
+    e = cudaFuncSetAttribute(paged_prefill_narrow_kernel<false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmemBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(paged_prefill_narrow_kernel<true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmemBytes);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
 }
@@ -604,7 +644,10 @@ cudaError_t launch_prefill_narrow(const CUtensorMap& tk, const CUtensorMap& tv,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = early ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, paged_prefill_narrow_kernel, tk, tv, tq, p);
+    return cudaLaunchKernelEx(&cfg,
+                              p.window > 0 ? paged_prefill_narrow_kernel<true>
+                                           : paged_prefill_narrow_kernel<false>,
+                              tk, tv, tq, p);
 }
 
 }  // namespace oxd
