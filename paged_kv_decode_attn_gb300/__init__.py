@@ -291,8 +291,10 @@ def make_copy_pages_desc(num_pairs, num_kv_heads, page_size, src_format, src_lay
 
 def make_window_decode_desc(batch, num_qo_heads, num_kv_heads, page_size, layout, num_pages,
                             num_indices, window, sinks=0, head_dim=128, max_splits=0,
-                            pdl=0) -> WindowDecodeDesc:
-    """Convenience constructor; ``layout`` may be "NHD"/"HND" or 0/1."""
+                            pdl=1) -> WindowDecodeDesc:
+    """Convenience constructor; ``layout`` may be "NHD"/"HND" or 0/1. By default the call is
+    launched as a programmatic dependent of the kernel before it on the stream, which it waits
+    for before it touches memory: the results are those of a plain launch (``pdl`` = 0)."""
     if isinstance(layout, str):
         layout = {"NHD": OXD_LAYOUT_NHD, "HND": OXD_LAYOUT_HND}[layout]
     return WindowDecodeDesc(batch, num_qo_heads, num_kv_heads, head_dim, page_size, layout,

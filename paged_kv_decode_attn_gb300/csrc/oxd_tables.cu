@@ -40,7 +40,7 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {
     return x;
 }
 
-__global__ void __launch_bounds__(kTabThreads)
+__global__ void __launch_bounds__(kTabThreads, 1)
     build_tables_kernel(const __grid_constant__ TablesParams p) {
     __shared__ Request req[kTabThreads];
     __shared__ int sums[3][kTabWarps];

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <mutex>
 
 #include "oxd_internal.h"
 #include "oxd_ptx.cuh"
@@ -152,43 +153,72 @@ __device__ __forceinline__ void merge_states(const WindowParams& p, const uint8_
 
 // ------------------------------------------------------------------ launching
 
-// Sets a kernel's attributes once a device (`which`: the kernel's number among a file's)
-// and gives the current device's SM count.
-inline cudaError_t window_kernel_ready(const void* kernel, int most_smem, int which, int* sms) {
-    static std::atomic<uint64_t> done[8];
-    static std::atomic<int> count[64];
+// How many clusters of c CTAs of a kernel are resident at once, by c; filled once a
+// device, with the kernel's attributes set.
+struct WindowOccupancy {
+    int clusters[kMaxWindowSplits + 1];
+};
+constexpr int kMaxDevices = 64;
+
+// `which`: the kernel's number among a file's; smem(c): its shared memory in clusters
+// of c CTAs, at most `most_smem`.
+template <class Smem>
+cudaError_t window_kernel_ready(void (*kernel)(WindowParams), int which, int most_smem, Smem smem,
+                                const WindowOccupancy** out) {
+    static std::atomic<bool> done[3][kMaxDevices];
+    static WindowOccupancy table[3][kMaxDevices];
+    static std::mutex mu;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
-    if (bit != 0 && (done[which].load(std::memory_order_acquire) & bit)) {
-        *sms = count[dev].load(std::memory_order_relaxed);
-        return cudaSuccess;
-    }
+    if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    *out = &table[which][dev];
+    if (done[which][dev].load(std::memory_order_acquire)) return cudaSuccess;
+    std::lock_guard<std::mutex> lk(mu);
+    if (done[which][dev].load(std::memory_order_relaxed)) return cudaSuccess;
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   most_smem)) != cudaSuccess ||
         (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) !=
-            cudaSuccess ||
-        (e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+            cudaSuccess)
         return e;
-    if (bit != 0) {
-        count[dev].store(*sms, std::memory_order_relaxed);
-        done[which].fetch_or(bit, std::memory_order_release);
+    for (int c = 1; c <= kMaxWindowSplits; ++c) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(c);
+        cfg.blockDim = dim3(kWinThreads);
+        cfg.dynamicSmemBytes = smem(c);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(c);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+        table[which][dev].clusters[c] = n;
     }
+    done[which][dev].store(true, std::memory_order_release);
     return cudaSuccess;
 }
 
-// CTAs a stream: as many as leave every resident CTA one, each with at least a chunk a
-// warp (`least` tokens).
-inline int window_splits(const WindowParams& p, int64_t streams, int least, int max_splits,
-                         int resident) {
+// CTAs a stream. As many as still leave all of them resident at once (a cluster sits in
+// one GPC, so that fewer large ones fit), each with at least a chunk a warp (`least`
+// tokens); more than eight only for four chunks a warp: eight requests x 8 heads of 1024
+// tokens over 4 bits take 9.2 us with 8 and 12.0 with 12, 16 x 1 head of 8192 over bf16
+// 25 and 19. Long streams that fill the GPU are cut in two all the same, so that the
+// last to start end sooner (64 x 8 heads of 4096: 164 -> 158 us).
+inline int window_splits(const WindowParams& p, const WindowOccupancy& occ, int64_t streams,
+                         int least, int max_splits) {
     const int64_t most = std::min<int64_t>(
         static_cast<int64_t>(p.window) + p.sinks,
         static_cast<int64_t>(p.num_indices) << p.page_shift);
-    const int64_t c = std::min<int64_t>(
-        {resident / streams, most / least,
-         max_splits > 0 ? std::min(max_splits, kMaxWindowSplits) : kMaxWindowSplits});
-    return static_cast<int>(std::max<int64_t>(1, c));
+    const int cap =
+        max_splits > 0 ? std::min(max_splits, kMaxWindowSplits) : kMaxWindowSplits;
+    int c = 1;
+    for (int i = 2; i <= cap; ++i)
+        if (occ.clusters[i] >= streams && most >= int64_t{i} * least * (i > 8 ? 4 : 1)) c = i;
+    const bool full = streams * 4 >= int64_t{occ.clusters[1]} * 3;
+    return full && cap > 1 && most >= 4096 ? 2 : c;
 }
 
 inline cudaError_t window_launch(void (*kernel)(WindowParams), const WindowParams& p,

@@ -10,16 +10,19 @@
 //   * a stream (request, KV head) is one CTA's, or a cluster's: each CTA takes an equal
 //     share of the visible tokens and the states are merged through shared memory;
 //   * each of a CTA's four warps streams its own 16-token chunks through a private ring
-//     that it refills by 16-byte cp.async (16 lanes a row). The copies go by token, not
+//     of slots, K and V in turn, that it refills by 16-byte cp.async (16 lanes a row; a
+//     slot as soon as it is read). The copies go by token, not
 //     by page: a chunk starts at any visible token, so the window's edges, the sinks and
 //     pages cost no masked tokens, and rows outside the window are never read;
 //   * the tokens are the M dimension of mma.sync m16n8k16 (S^T = K Q^T, O^T = V^T P^T),
-//     so up to 8 heads are one N tile and one read of K and V serves the whole group;
+//     so 8 heads are one N tile and one read of K and V serves up to 16; a larger group
+//     is two parts, CTAs of their own that start together and find the rows in L2;
 //   * the running maximum is raised only when a score passes it by 2^8, so most chunks
 //     need one warp vote and no reduction or rescaling. Weights are rounded to bf16 for
 //     the product (the sum of weights is not).
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cfloat>
 
 #include "oxd_internal.h"
@@ -29,16 +32,19 @@
 namespace oxd {
 namespace {
 
-constexpr int kChunk = 16;                          // tokens a warp takes at a time
+constexpr int kChunk = 16;  // tokens a warp takes at a time
 constexpr int kRowBytes = kHeadDim * 2;
-constexpr int kSlotBytes = 2 * kChunk * kRowBytes;  // K, then V
+constexpr int kSlotBytes = kChunk * kRowBytes;  // K or V of a chunk
 constexpr float kLazy = 8.f;  // log2: how far a score may pass the running maximum
 
 template <int kTiles_>  // N tiles of 8 query heads
 struct WCfg {
     static constexpr int kTiles = kTiles_;
-    static constexpr int kSlots = 2;  // of a warp's ring
-    static constexpr int kCtas = kTiles < 4 ? 3 : 2;  // resident a SM
+    // Slots of a warp's ring, K and V of its chunks in turn, and the resident CTAs a SM
+    // that they leave. (Four slots: one CTA fewer, 16 x 1 head of 32 rows 19.1 -> 22.2 us;
+    // whole chunks as slots, two of them: 64 x 8 heads of 512 tokens 23.3 -> 27.0.)
+    static constexpr int kSlots = 3;
+    static constexpr int kCtas = kTiles == 1 ? 4 : 3;
     static constexpr int kRingBytes = kSlots * kSlotBytes;
     static constexpr int kRows = 8 * kTiles;
     static_assert(kRows * kHeadDim * 4 <= kRingBytes, "a warp's state fits its ring");
@@ -97,6 +103,7 @@ struct Stream {
     int head;
     int next, end;  // next chunk to copy (every fourth is this warp's), end of the CTA's share
     int page;       // page index of this lane's token of it
+    uint32_t row;   // its row in the pools, once its K is under way
 
     __device__ __forceinline__ int token(int c, int lane) const {
         const int v = min(c * kChunk + (lane & 15), vis.count - 1);  // the last once more past it
@@ -106,31 +113,34 @@ struct Stream {
         if (next < end)
             page = __ldg(p.indices + vis.first + (token(next, lane) >> p.page_shift));
     }
-    // Copies the next chunk into `slot`, if there is one; always one more copy group.
+    // Copies the next K or V into `slot`, if there is one; always one more copy group.
+    template <bool kV>
     __device__ __forceinline__ void refill(const WindowParams& p, uint32_t slot, int lane) {
         if (next < end) {
-            // An index outside the pool is recorded and replaced by page 0.
-            const bool bad = page < 0 || static_cast<int64_t>(page) >= p.num_pages;
-            if (__any_sync(0xffffffffu, bad) && lane == 0)
-                record_status(p.status, p.epoch, kDeviceBadPage);
-            const uint32_t pg = bad ? 0u : static_cast<uint32_t>(page);
-            const uint32_t at = token(next, lane) & ((1 << p.page_shift) - 1);
-            const uint32_t H = p.num_kv_heads;
-            // (a pool has fewer than 2^32 rows)
-            const uint32_t row = p.layout == 0 ? ((pg << p.page_shift) + at) * H + head
-                                               : ((pg * H + head) << p.page_shift) + at;
+            if constexpr (!kV) {
+                // An index outside the pool is recorded and replaced by page 0.
+                const bool bad = page < 0 || static_cast<int64_t>(page) >= p.num_pages;
+                if (__any_sync(0xffffffffu, bad) && lane == 0)
+                    record_status(p.status, p.epoch, kDeviceBadPage);
+                const uint32_t pg = bad ? 0u : static_cast<uint32_t>(page);
+                const uint32_t at = token(next, lane) & ((1 << p.page_shift) - 1);
+                const uint32_t H = p.num_kv_heads;
+                // (a pool has fewer than 2^32 rows)
+                row = p.layout == 0 ? ((pg << p.page_shift) + at) * H + head
+                                    : ((pg * H + head) << p.page_shift) + at;
+            }
             const int col = lane & 15;
+            const uint8_t* src = (kV ? p.v : p.k) + col * 16;
 #pragma unroll
             for (int i = 0; i < kChunk / 2; ++i) {
                 const int t = 2 * i + (lane >> 4);
-                const size_t off =
-                    static_cast<size_t>(__shfl_sync(0xffffffffu, row, t)) * kRowBytes + col * 16;
-                const uint32_t dst = slot + t * kRowBytes + ((col ^ (t & 7)) << 4);
-                cp_async16(dst, p.k + off);
-                cp_async16(dst + kChunk * kRowBytes, p.v + off);
+                cp_async16(slot + t * kRowBytes + ((col ^ (t & 7)) << 4),
+                           src + static_cast<size_t>(__shfl_sync(0xffffffffu, row, t)) * kRowBytes);
             }
-            next += kWinWarps;
-            look_up(p, lane);
+            if constexpr (kV) {
+                next += kWinWarps;
+                look_up(p, lane);
+            }
         }
         cp_async_commit();
     }
@@ -143,15 +153,17 @@ struct State {
     float m[C::kTiles][2], l[C::kTiles][2];  // heads 2 tq, 2 tq + 1 of each tile
     float acc[8][C::kTiles][4];              // [16 columns][tile]
 
-    // One chunk at `chunk`, of which the first `left` tokens count.
-    __device__ __forceinline__ void consume(uint32_t chunk, int left, float scale_log2, int lane) {
+    uint32_t pb[C::kTiles][2];               // P^T of the chunk
+
+    // The weights of one chunk from its K at `slot`; its first `left` tokens count.
+    __device__ __forceinline__ void scores(uint32_t slot, int left, float scale_log2, int lane) {
         const int g = lane >> 2;
         const int r = lane & 7, mi = lane >> 3;
         // ---- S^T = K Q^T, even and odd steps apart (two chains of dependent MMAs)
         float s[C::kTiles][4], s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int n = 0; n < C::kTiles; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-        const uint32_t krow = chunk + ((mi & 1) * 8 + r) * kRowBytes;
+        const uint32_t krow = slot + ((mi & 1) * 8 + r) * kRowBytes;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
             uint32_t a[4];
@@ -167,7 +179,6 @@ struct State {
             }
         }
         // ---- online softmax in the log2 domain
-        uint32_t pb[C::kTiles][2];
 #pragma unroll
         for (int n = 0; n < C::kTiles; ++n) {
 #pragma unroll
@@ -216,8 +227,13 @@ struct State {
             pb[n][0] = transpose_8x8(pack_bf16x2(s[n][0], s[n][1]));
             pb[n][1] = transpose_8x8(pack_bf16x2(s[n][2], s[n][3]));
         }
-        // ---- O^T += V^T P^T (tokens past the last are the last once more, weight 0)
-        const uint32_t vrow = chunk + kChunk * kRowBytes + ((mi >> 1) * 8 + r) * kRowBytes;
+    }
+
+    // O^T += V^T P^T from the chunk's V at `slot` (tokens past the last are the last
+    // once more, weight 0).
+    __device__ __forceinline__ void values(uint32_t slot, int lane) {
+        const int r = lane & 7, mi = lane >> 3;
+        const uint32_t vrow = slot + ((mi >> 1) * 8 + r) * kRowBytes;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             uint32_t a[4];
@@ -240,10 +256,14 @@ __global__ void __launch_bounds__(kWinThreads, C::kCtas)
         if (blockIdx.x == 0) *p.last_epoch = p.epoch;
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
-    const int stream = blockIdx.x / p.splits;
+    // stream: request, KV head, part of the group, the last fastest
+    int stream = blockIdx.x / p.splits;
     const int rank = blockIdx.x - stream * p.splits;
+    const int parts = (p.group + C::kRows - 1) / C::kRows;
+    const int part = stream % parts;
+    stream /= parts;
     const int b = stream / p.num_kv_heads;
-    const int G = p.group;
+    const int G = min(C::kRows, p.group - part * C::kRows);  // rows of the part
     Stream in;
     in.head = stream - b * p.num_kv_heads;
     in.vis = visible_tokens(p, b);
@@ -258,7 +278,8 @@ __global__ void __launch_bounds__(kWinThreads, C::kCtas)
 
     // the query rows as B fragments: columns 16 ks + 2 tq, + 1, + 8, + 9 of head 8 n + g
     State<C> st;
-    const size_t row0 = static_cast<size_t>(b) * p.num_qo_heads + in.head * G;
+    const size_t row0 =
+        static_cast<size_t>(b) * p.num_qo_heads + in.head * p.group + part * C::kRows;
     auto query = [&](int ks, int n, int ln) {
         const int g = n * 8 + (ln >> 2);
         if (g >= G) return make_uint2(0u, 0u);
@@ -289,18 +310,31 @@ __global__ void __launch_bounds__(kWinThreads, C::kCtas)
             st.acc[i][n][0] = st.acc[i][n][1] = st.acc[i][n][2] = st.acc[i][n][3] = 0.f;
     }
     const uint32_t ring = smem_addr(base) + warp * C::kRingBytes;
-    for (int i = 0; i < C::kSlots; ++i) in.refill(p, ring + i * kSlotBytes, lane);
+    uint32_t slot = ring;  // of the next K or V
+    auto advance = [&]() {
+        slot += kSlotBytes;
+        if (slot == ring + C::kRingBytes) slot = ring;
+    };
+    in.refill<false>(p, ring, lane);
+    in.refill<true>(p, ring + kSlotBytes, lane);
+    in.refill<false>(p, ring + 2 * kSlotBytes, lane);
+    static_assert(C::kSlots == 3, "what is copied ahead, and into which slot");
     if constexpr (C::kTiles > 1) __syncthreads();
 
-    int slot = 0;
+    // (a slot is refilled with what comes three further on: V behind K, K behind V)
     for (int c = c0; c < in.end; c += kWinWarps) {
         cp_async_wait<C::kSlots - 1>();
-        __syncwarp();  // every lane's copies of the chunk have landed
-        const uint32_t chunk = ring + slot * kSlotBytes;
-        st.consume(chunk, in.vis.count - c * kChunk, p.scale_log2, lane);
+        __syncwarp();  // every lane's copies of K have landed
+        st.scores(slot, in.vis.count - c * kChunk, p.scale_log2, lane);
         __syncwarp();
-        in.refill(p, chunk, lane);
-        slot = slot + 1 == C::kSlots ? 0 : slot + 1;
+        in.refill<true>(p, slot, lane);
+        advance();
+        cp_async_wait<C::kSlots - 1>();
+        __syncwarp();
+        st.values(slot, lane);
+        __syncwarp();
+        in.refill<false>(p, slot, lane);
+        advance();
     }
     cp_async_wait<0>();
     __syncwarp();
@@ -344,23 +378,25 @@ template <class C>
 cudaError_t launch(WindowParams& p, int max_splits, cudaStream_t stream, bool pdl) {
     // (rows rounded up to a multiple of the CTAs are fewer than this, bytes to 16)
     constexpr int kMostSmem = C::kXchgOff + (C::kRows + kMaxWindowSplits) * (kHeadDim + 1) * 4;
-    const int64_t streams = static_cast<int64_t>(p.batch) * p.num_kv_heads;
-    int sms = 0;
-    const cudaError_t e = window_kernel_ready(reinterpret_cast<const void*>(window_decode_kernel<C>),
-                                              kMostSmem, C::kTiles, &sms);
+    const int64_t streams = static_cast<int64_t>(p.batch) * p.num_kv_heads *
+                            ((p.group + C::kRows - 1) / C::kRows);
+    const WindowOccupancy* occ = nullptr;
+    const cudaError_t e = window_kernel_ready(
+        window_decode_kernel<C>, C::kTiles - 1, kMostSmem,
+        [](int c) { return C::kXchgOff + exchange_bytes(C::kRows, c); }, &occ);
     if (e != cudaSuccess) return e;
     p.heads = 1;
-    p.splits = window_splits(p, streams, kWinWarps * kChunk, max_splits, sms * C::kCtas);
+    p.splits = window_splits(p, *occ, streams, kWinWarps * kChunk, max_splits);
     return window_launch(window_decode_kernel<C>, p, streams,
-                         C::kXchgOff + exchange_bytes(p.group, p.splits), stream, pdl);
+                         C::kXchgOff + exchange_bytes(std::min(C::kRows, p.group), p.splits),
+                         stream, pdl);
 }
 
 }  // namespace
 
 cudaError_t launch_window_decode(WindowParams p, int max_splits, cudaStream_t stream, bool pdl) {
     if (p.group <= 8) return launch<WCfg<1>>(p, max_splits, stream, pdl);
-    if (p.group <= 16) return launch<WCfg<2>>(p, max_splits, stream, pdl);
-    return launch<WCfg<4>>(p, max_splits, stream, pdl);
+    return launch<WCfg<2>>(p, max_splits, stream, pdl);
 }
 
 }  // namespace oxd

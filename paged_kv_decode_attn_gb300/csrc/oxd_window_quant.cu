@@ -9,7 +9,6 @@
 // in L2. In NHD pools a CTA takes two KV heads where it can (64 bytes of codes a head:
 // half a 128-byte line).
 #include <algorithm>
-#include <atomic>
 
 #include "oxd_decode_quant_state.cuh"
 #include "oxd_internal.h"
@@ -188,12 +187,12 @@ cudaError_t launch_window_quant(WindowParams p, int max_splits, cudaStream_t str
     p.heads = p.layout == 0 && p.num_kv_heads % 2 == 0 ? 2 : 1;
     const int64_t streams = static_cast<int64_t>(p.batch) * (p.num_kv_heads / p.heads) *
                             ((p.group + kRows - 1) / kRows);
-    int resident = 0;
-    cudaError_t e = window_kernel_ready(reinterpret_cast<const void*>(window_quant_kernel),
-                                        kMostSmem, 0, &resident);
+    const WindowOccupancy* occ = nullptr;
+    const cudaError_t e = window_kernel_ready(
+        window_quant_kernel, 0, kMostSmem,
+        [](int c) { return QW::kXchgOff + 2 * exchange_bytes(kRows, c); }, &occ);
     if (e != cudaSuccess) return e;
-    p.splits = window_splits(p, streams, kWinWarps / p.heads * kChunk, max_splits,
-                             resident * QW::kCtas);
+    p.splits = window_splits(p, *occ, streams, kWinWarps / p.heads * kChunk, max_splits);
     return window_launch(window_quant_kernel, p, streams,
                          QW::kXchgOff + p.heads * exchange_bytes(std::min(kRows, p.group), p.splits),
                          stream, pdl);
