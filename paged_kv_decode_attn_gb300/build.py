@@ -23,7 +23,7 @@ HEADERS = [os.path.join(ROOT, "include", "oxd.h")] + [
                                     "oxd_window.cuh", "oxd_prefill_window.cuh")]
 SOURCES = ["oxd_host.cpp", "oxd_decode.cu", "oxd_decode_wide.cu", "oxd_merge.cu",
            "oxd_noalloc.cu", "oxd_append.cu", "oxd_prefill.cu", "oxd_prefill_narrow.cu",
-           "oxd_prefill_host.cpp", "oxd_decode_quant.cu", "oxd_decode_quant_wide.cu",
+           "oxd_prefill_window.cu", "oxd_prefill_host.cpp", "oxd_decode_quant.cu", "oxd_decode_quant_wide.cu",
            "oxd_append_axes.cu", "oxd_pages.cu",
            "oxd_quant_host.cpp", "oxd_window_decode.cu", "oxd_window_quant.cu", "oxd_tables.cu",
            "oxd_window_host.cpp"]

@@ -43,7 +43,6 @@
 
 #include "oxd_internal.h"
 #include "oxd_prefill.h"
-#include "oxd_prefill_window.cuh"
 #include "oxd_ptx.cuh"
 #include "oxd_tcgen05.cuh"
 
@@ -82,8 +81,7 @@ struct PCtl {
                           // a single-half tile's P(g): phase g / 2 of p_ready[g % 2]
     uint64_t o_done[2];   // the half's last PV done
     uint64_t pv_done;     // single-half tile: PV(g) done, phase g
-    uint64_t vz[2];       // V rows that no row sees zeroed in the k-th stage that has some:
-                          // phase k / 2 of vz[k % 2] (one arrival a warp)
+    uint64_t vz;          // V rows past the piece zeroed (one arrival a warp)
     uint64_t mma_done;
     int kissued[kPKStages];
     int vissued[kPVStages];
@@ -93,44 +91,17 @@ struct PCtl {
 // The dynamic shared memory starts 1024-byte aligned (checked in the kernel).
 constexpr int kPSmemBytes = kPCtlOff + static_cast<int>(sizeof(PCtl));
 
-// 32 lanes x 16 consecutive 32-bit columns, without the wait (see tmem_ld_wait16).
-__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
-}
-
 // Stages a half streams of a piece: its rows see cached tokens up to the
 // position of its last query token.
-using Window = TileWindow<kPrefillStageTokens>;
-
-template <bool kWindow>
-__device__ __forceinline__ int half_stages(const PrefillUnit& u, const Window& w, int G, int h) {
+__device__ __forceinline__ int half_stages(const PrefillUnit& u, int G, int h) {
     const int rows = u.n_tok * G;
     if (rows <= 128 * h) return 0;  // the half holds no row of the tile
     const int t_last = (min(rows, 128 * (h + 1)) - 1) / G;
-    if constexpr (kWindow) {
-        // (the tile's last stages: no skipped ones among or behind them)
-        int n = (u.kv_valid + kPrefillStageTokens - 1) / kPrefillStageTokens;
-        while (n > 0 && w.base(n - 1) > u.p0 + t_last) --n;
-        return n;
-    }
     const int end = min(u.kv_begin + u.kv_valid, u.p0 + t_last + 1);
     return end > u.kv_begin ? (end - u.kv_begin + kPrefillStageTokens - 1) / kPrefillStageTokens
                             : 0;
 }
 
-// kWindow: queries see a window of their last tokens and the sinks (an instantiation
-// of its own, so its code does not weigh on the other).
-template <bool kWindow>
 __global__ void __launch_bounds__(kPThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                          const __grid_constant__ CUtensorMap tmap_v,
@@ -165,8 +136,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             mbar_init(&ctl.o_done[h], 1);
         }
         mbar_init(&ctl.pv_done, 1);
-        mbar_init(&ctl.vz[0], 4);
-        mbar_init(&ctl.vz[1], 4);
+        mbar_init(&ctl.vz, 4);
         mbar_init(&ctl.mma_done, 1);
         flags[0] = 0;
         fence_mbar_init();
@@ -209,14 +179,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
                       static_cast<int64_t>(u.n_tok - 1) * u.n_pieces + u.piece + 1) *
                              G <=
                          p.n_states;
-            if constexpr (kWindow) {
-                if (ok) {
-                    Window w;
-                    w.init(p, u);
-                    ok = w.inside(u, (u.kv_valid + kPrefillStageTokens - 1) / kPrefillStageTokens,
-                                  kPrefillStageTokens / ps, p.nnz);
-                }
-            }
         } else {
             ok = 0;
         }
@@ -237,22 +199,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
     PrefillUnit u{};
     if (usable) u = p.units[blockIdx.x];
     const int n_st = usable ? (u.kv_valid + kPrefillStageTokens - 1) / kPrefillStageTokens : 0;
-    Window win_t;
-    if constexpr (kWindow) win_t.init(p, u);
-    const int nst_h[2] = {usable ? half_stages<kWindow>(u, win_t, G, 0) : 0,
-                          usable ? half_stages<kWindow>(u, win_t, G, 1) : 0};
+    const int nst_h[2] = {usable ? half_stages(u, G, 0) : 0, usable ? half_stages(u, G, 1) : 0};
     const int last_valid = n_st > 0 ? u.kv_valid - (n_st - 1) * kPrefillStageTokens : 0;
     // A tile whose rows all sit in the first half (half 1 streams nothing)
     // gives half 0 both score buffers: QK(g + 1) runs while the softmax of
     // stage g does.
     const bool single = nst_h[1] == 0;
-    // Stages of whose V rows some are zeroed: those past the piece, in its last one,
-    // and those before the tile's window.
-    const bool tail_vz = n_st > 0 && last_valid < kPrefillStageTokens;
-    auto need_vz = [&](int g) {
-        if constexpr (kWindow) return (tail_vz && g == n_st - 1) || win_t.hides(g);
-        return tail_vz && g == n_st - 1;
-    };
+    const bool need_vz = n_st > 0 && last_valid < kPrefillStageTokens;
 
     if (warp == kPKWarp || warp == kPVWarp) {
         // ================================================ producer warps
@@ -262,9 +215,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int pps = kPrefillStageTokens / ps;  // pages per stage (divides 32)
         const int32_t* idx = p.indices + u.idx_begin;
         int win = 0, nxt = 0, win_base = 0;
-        if constexpr (kWindow) {
-            nxt = window_page(win_t, p, u, 0, n_st, lane);
-        } else if (n_st > 0) {
+        if (n_st > 0) {
             if (lane < u.n_pages) win = __ldg(idx + lane);
             if (32 + lane < u.n_pages) nxt = __ldg(idx + 32 + lane);
         }
@@ -274,7 +225,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 record_status(p.status, p.epoch, kDeviceBadPage);
             win = bad ? 0 : win;  // an index outside the pool reads page 0
         };
-        if (!kWindow && n_st > 0) check_window();
+        if (n_st > 0) check_window();
         const int n_slots = is_k ? kPKStages : kPVStages;
         uint64_t* full = is_k ? ctl.kfull : ctl.vfull;
         uint64_t* empty = is_k ? ctl.kempty : ctl.vempty;
@@ -287,13 +238,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const int slot = s % n_slots;
             const int pg0 = s * pps;
             const int npg = min(pps, u.n_pages - pg0);
-            if constexpr (kWindow) {
-                win = nxt;  // the stage's pages, a lane's own; the next stage's are read now
-                nxt = window_page(win_t, p, u, s + 1, n_st, lane);
-                if (__any_sync(0xffffffffu, win < 0) && lane == 0)
-                    record_status(p.status, p.epoch, kDeviceBadPage);
-                win = max(win, 0);
-            } else if (pg0 >= win_base + 32) {
+            if (pg0 >= win_base + 32) {
                 win = nxt;
                 win_base += 32;
                 nxt = win_base + 32 + lane < u.n_pages ? __ldg(idx + win_base + 32 + lane) : 0;
@@ -308,8 +253,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
             if (lane == 0) mbar_arrive_expect_tx(&full[slot], npg * ps * kHeadDim * 2);
             const int j = lane >> 1;
-            const int page =
-                kWindow ? win : __shfl_sync(0xffffffffu, win, (pg0 - win_base + j) & 31);
+            const int page = __shfl_sync(0xffffffffu, win, (pg0 - win_base + j) & 31);
             if (lane < 2 * npg) {
                 const uint32_t dst = (is_k ? ring_k(slot) : ring_v(slot)) + j * ps * 128 +
                                      ((lane & 1) ? kPHalf : 0);
@@ -375,12 +319,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     umma_ts_warp(t_o(h), ps0 + 8u * ks, vd0 + static_cast<uint64_t>(ks * 2048 >> 4),
                                  kIdPV, (ks > 0 || g > 0) ? 1u : 0u);
             };
-            int n_vz = 0;  // stages with zeroed V rows so far
-            auto wait_vz = [&](int g) {
-                if (!need_vz(g)) return true;
-                const int k = n_vz++;
-                return wait(&ctl.vz[k & 1], (k >> 1) & 1);
-            };
             if (single) {
                 // Half 0 alone, scores in S_0 and S_1 by stage parity: QK(0),
                 // QK(1), then per stage g PV(g) and QK(g + 2) into the buffer PV(g)
@@ -399,7 +337,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     // P(g + 1) before this wait for P(g) has seen its phase
                     if (!wait(&ctl.p_ready[g & 1], (g >> 1) & 1)) break;
                     if (!wait(&ctl.vfull[g % kPVStages], (g / kPVStages) & 1)) break;
-                    if (!wait_vz(g)) break;
+                    if (g == n_st - 1 && need_vz && !wait(&ctl.vz, 0)) break;
                     tc_fence_after();
                     issue_pv(0, g, t_s(g & 1));
                     umma_commit_warp(&ctl.pv_done);
@@ -424,7 +362,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         if (!wait(&ctl.p_ready[h], gp & 1)) break;
                         if (h == 0 || gp >= nst_h[0]) {  // the first half to read V(gp)
                             if (!wait(&ctl.vfull[gp % kPVStages], (gp / kPVStages) & 1)) break;
-                            if (!wait_vz(gp)) break;
+                            if (gp == n_st - 1 && need_vz && !wait(&ctl.vz, 0)) break;
                         }
                         tc_fence_after();
                         issue_pv(h, gp, t_s(h));
@@ -470,8 +408,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int R = 128 * h + r;  // row of the tile: token R / G, head R % G
         const int t = R / G, gi = R - (R / G) * G;
         const bool row_ok = usable && t < u.n_tok;
-        // (padding rows see everything, or with a window what the last query sees)
-        const int pos = row_ok ? u.p0 + t : kWindow ? u.p0 + u.n_tok - 1 : (1 << 30);
+        const int pos = row_ok ? u.p0 + t : (1 << 30);  // padding rows see everything
         const int nst = nst_h[h];
         // the half's query rows into shared memory (once; zeros past the
         // tile), laid out as the score MMA's A operand: two 64-column halves
@@ -495,13 +432,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
         // the half's first row position: a stage ending at or before it is
         // seen whole by every row of the half
         const int p_first = usable ? u.p0 + (128 * h) / G : 0;
-        // the half's last row position: a stage that starts inside its window is in
-        // every row's
-        const int p_end = usable ? u.p0 + (min(u.n_tok * G, 128 * (h + 1)) - 1) / G : 0;
         // the half with the tile's last rows streams every stage of the piece;
-        // its warps zero V rows that no row sees
-        const bool zeroes = h == (usable && u.n_tok * G > 128 ? 1 : 0);
-        int n_vz = 0;  // stages it did that for
+        // its warps zero V rows past the piece
+        const bool zeroes = need_vz && h == (usable && u.n_tok * G > 128 ? 1 : 0);
         const float sc = p.scale_log2;
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
@@ -517,23 +450,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
             // PV_h(g - 1) among them with two halves (O_h is up to date), and
             // PV(g - 2) for a single-half tile (its P was in this buffer)
             tc_fence_after();
-            const int base = kWindow ? win_t.base(g) : u.kv_begin + g * kPrefillStageTokens;
+            const int base = u.kv_begin + g * kPrefillStageTokens;
             const int nvalid = min(kPrefillStageTokens, u.kv_valid - g * kPrefillStageTokens);
             // A stage that ends at or before the half's first position is seen
             // whole by every row (the same for the whole warpgroup): no mask,
             // the maximum is taken over the raw scores and the scale is folded
             // into the exponent's FMA. Otherwise scores are scaled and masked.
             const bool whole = nvalid == kPrefillStageTokens &&
-                               base + kPrefillStageTokens - 1 <= p_first && sc > 0.f &&
-                               (!kWindow || win_t.whole(base, p_end));
-            // visible columns of this row: below lim and, with a window, from w_lo on or
-            // below w_sink
-            const int lim = min(nvalid, pos - base + 1);
-            const int w_lo = kWindow ? pos - win_t.window + 1 - base : 0;
-            const int w_sink = kWindow ? win_t.sinks - base : 0;
-            auto visible = [&](int j) {
-                return j < lim && (!kWindow || j >= w_lo || j < w_sink);
-            };
+                               base + kPrefillStageTokens - 1 <= p_first && sc > 0.f;
+            const int lim = min(nvalid, pos - base + 1);  // visible columns of this row
             float lq[4] = {0.f, 0.f, 0.f, 0.f};
             bool rescale = false;
             float alpha = 1.f;
@@ -599,7 +524,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 } else {
 #pragma unroll
                     for (int j = 0; j < 64; ++j) {
-                        const float x = visible(j) ? __uint_as_float(s0[j]) * sc : -INFINITY;
+                        const float x = j < lim ? __uint_as_float(s0[j]) * sc : -INFINITY;
                         s0[j] = __float_as_uint(x);
                         mq[j & 3] = fmaxf(mq[j & 3], x);
                     }
@@ -616,7 +541,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            mq[j & 3] = fmaxf(mq[j & 3], visible(64 + 32 * c + j)
+                            mq[j & 3] = fmaxf(mq[j & 3], 64 + 32 * c + j < lim
                                                              ? __uint_as_float(s1[j]) * sc
                                                              : -INFINITY);
                     }
@@ -675,10 +600,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const int t0 = 64 + 32 * c + 2 * j;
-                            const float x0 =
-                                visible(t0) ? __uint_as_float(s1[2 * j]) * sc : -INFINITY;
+                            const float x0 = t0 < lim ? __uint_as_float(s1[2 * j]) * sc : -INFINITY;
                             const float x1 =
-                                visible(t0 + 1) ? __uint_as_float(s1[2 * j + 1]) * sc : -INFINITY;
+                                t0 + 1 < lim ? __uint_as_float(s1[2 * j + 1]) * sc : -INFINITY;
                             const float p0 = fast_exp2(x0 - m_use);
                             const float p1 = fast_exp2(x1 - m_use);
                             lq[j & 3] += p0 + p1;
@@ -708,8 +632,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 }
             }
             tmem_wait_st();
-            if (zeroes && need_vz(g)) {
-                // zero V rows that no row sees once the stage's V landed (whole 128-byte
+            const bool last = g == nst - 1;
+            if (last && zeroes) {
+                // zero V rows past the piece once its V landed (whole 128-byte
                 // rows, so the swizzle does not matter); V(g - 2), the slot's
                 // previous stage, has been read (PV(g - 2) is done), so this
                 // phase of vfull is the one for stage g
@@ -718,20 +643,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     break;
                 }
                 uint8_t* v0 = sm + kPVOff + (g % kPVStages) * kPSlotBytes;
-                auto zero_rows = [&](int r0, int r1) {
-                    const int n16 = (r1 - r0) * 16;
-                    for (int i = r; i < n16; i += 128) {
-                        const int row = r0 + (i >> 4), c = i & 15;
-                        *reinterpret_cast<uint4*>(v0 + (c >> 3) * kPHalf + row * 128 +
-                                                  (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                };
-                zero_rows(nvalid, kPrefillStageTokens);
-                if constexpr (kWindow) zero_rows(win_t.hidden0(base), win_t.hidden1(base));
+                const int n16 = (kPrefillStageTokens - nvalid) * 16;
+                for (int i = r; i < n16; i += 128) {
+                    const int row = nvalid + (i >> 4), c = i & 15;
+                    *reinterpret_cast<uint4*>(v0 + (c >> 3) * kPHalf + row * 128 + (c & 7) * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.vz[n_vz & 1]);
-                ++n_vz;
+                if (lane == 0) mbar_arrive(&ctl.vz);
             }
             tc_fence_before();
             __syncwarp();
@@ -833,11 +753,8 @@ cudaError_t ensure_prefill_attribute() {
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
     if (bit != 0 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-    e = cudaFuncSetAttribute(paged_prefill_kernel<false>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmemBytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(paged_prefill_kernel<true>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmemBytes);
+    e = cudaFuncSetAttribute(paged_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kPSmemBytes);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
 }
@@ -884,8 +801,7 @@ cudaError_t launch_prefill(const CUtensorMap& tk, const CUtensorMap& tv, const P
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = early ? 1 : 0;
-    return cudaLaunchKernelEx(
-        &cfg, p.window > 0 ? paged_prefill_kernel<true> : paged_prefill_kernel<false>, tk, tv, p);
+    return cudaLaunchKernelEx(&cfg, paged_prefill_kernel, tk, tv, p);
 }
 
 }  // namespace oxd

@@ -76,21 +76,25 @@ struct PrefillParams {
     int64_t wait_ns;                // limit of a pipeline wait (> 0)
     int32_t window;                 // 0: no window; else a query at position p sees tokens
     int32_t sinks;                  // j > p - window or j < sinks
+    const int32_t* cta_begin;       // the persistent kernel's: units of CTA c are
+                                    // [cta_begin[c], cta_begin[c + 1])
 };
 
-// The stages (of `stage` tokens) that a tile whose first query sits at p0 streams
-// under a window: those with sinks, then those from the first token that its window
-// holds on. Stage v of them is stage v of the request, or v + skip from `front` on.
-// A piece's kv_begin is its first stage's place in the request, its kv_valid and
-// n_pages count without the skipped ones.
-struct WindowStages {
+// The pages that a tile whose first query sits at p0 streams under a window: the first
+// `front` (with the sinks), then those from front + skip on (from the first token of its
+// first query's window). Its cached tokens are counted without the skipped pages: token
+// v of a tile is token v of the request, or v + skip pages from `front` pages on, and so
+// are kv_begin, kv_valid and n_pages of its pieces. In that count a query at position p
+// (count it by window_position) sees the tokens v <= p with v > p - window or v < sinks.
+struct WindowPages {
     int32_t front, skip;
 };
-__host__ __device__ inline WindowStages window_stages(int window, int sinks, int p0, int stage) {
-    const int lo = p0 >= window ? p0 - window + 1 : 0;
-    WindowStages w;
-    w.front = (sinks + stage - 1) / stage;
-    w.skip = lo / stage > w.front ? lo / stage - w.front : 0;
+__host__ __device__ inline WindowPages window_pages(int window, int sinks, int p0, int page_size) {
+    const int first = (p0 >= window ? p0 - window + 1 : 0) / page_size;
+    const int with_sinks = (sinks + page_size - 1) / page_size;
+    WindowPages w;
+    w.front = with_sinks < first ? with_sinks : first;
+    w.skip = first - w.front;
     return w;
 }
 
@@ -109,5 +113,12 @@ cudaError_t prefill_narrow_occupancy(int* ctas_per_sm);
 cudaError_t launch_prefill_narrow(const CUtensorMap& tk, const CUtensorMap& tv,
                                   const CUtensorMap& tq, const PrefillParams& p, int grid,
                                   cudaStream_t stream, bool early = false);
+
+// The persistent kernel of prefills with a window (oxd_prefill_window.cu): tiles and
+// stages of the two-half kernel, one CTA a SM, each with up to kWindowUnits units.
+constexpr int kWindowUnits = 256;
+cudaError_t prefill_window_smem_bytes(int* bytes);
+cudaError_t launch_prefill_window(const CUtensorMap& tk, const CUtensorMap& tv,
+                                  const PrefillParams& p, int grid, cudaStream_t stream);
 
 }  // namespace oxd

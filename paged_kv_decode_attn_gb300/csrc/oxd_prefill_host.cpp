@@ -20,7 +20,9 @@
 #include <limits>
 #include <mutex>
 #include <new>
+#include <queue>
 #include <unordered_set>
+#include <utility>
 #include <vector>
 
 #include "../../include/oxd.h"
@@ -49,7 +51,8 @@ struct oxd_prefill_plan_s {
     int64_t nnz;
     int64_t total_kv;
     int64_t pairs;
-    size_t off_units, off_entries, meta_bytes, off_part_o, off_part_lse, ws_bytes;
+    int n_ctas;
+    size_t off_units, off_entries, off_ctas, meta_bytes, off_part_o, off_part_lse, ws_bytes;
     void* meta;  // workspace image [0, meta_bytes) (stamp word 0), then the plan's stamp
     bool pinned;
     unsigned long long stamp;
@@ -107,6 +110,89 @@ int64_t window_pairs(int64_t p0, int64_t p1, int64_t window, int64_t sinks) {
     return (mid - p0) * (p0 + mid + 1) / 2 + (p1 - mid) * most;
 }
 
+// What a piece costs the persistent kernel besides its stages, and what the merge of
+// split tiles costs a run, in stages (about 1.8 us each).
+constexpr double kPieceStages = 1.0, kMergeStages = 4.0;
+
+// Shares tiles of `stages` out over persistent CTAs: whole tiles, the longest first, each
+// to the CTA with the least so far; or, where that ends sooner by more than the merge
+// costs, the tiles end to end, cut into equal shares (at most `cap` pieces a tile). A CTA
+// takes up to kWindowUnits pieces; more tiles than that make more CTAs.
+void share_out(const std::vector<int>& stages, int num_sms, int cap,
+               std::vector<std::vector<int>>* cuts,
+               std::vector<std::vector<std::pair<int, int>>>* lists) {
+    const int n = static_cast<int>(stages.size());
+    int64_t total = 0;
+    for (const int s : stages) total += s;
+    const int64_t waves = (n + int64_t{num_sms} * (kWindowUnits / 2) - 1) /
+                          (int64_t{num_sms} * (kWindowUnits / 2));
+    std::vector<int> order(n);
+    for (int i = 0; i < n; ++i) order[i] = i;
+    std::stable_sort(order.begin(), order.end(),
+                     [&](int a, int b) { return stages[a] > stages[b]; });
+    const int64_t ctas = std::min<int64_t>(num_sms * waves, n);
+    std::vector<std::vector<std::pair<int, int>>> whole(ctas);
+    double whole_end = 0;
+    {
+        std::priority_queue<std::pair<double, int>, std::vector<std::pair<double, int>>,
+                            std::greater<std::pair<double, int>>>
+            load;
+        for (int c = 0; c < ctas; ++c) load.push({0.0, c});
+        for (const int i : order) {
+            std::pair<double, int> l = load.top();
+            load.pop();
+            whole[l.second].push_back({i, 0});
+            l.first += stages[i] + kPieceStages;
+            whole_end = std::max(whole_end, l.first);
+            if (static_cast<int>(whole[l.second].size()) < kWindowUnits) load.push(l);
+        }
+    }
+    cuts->assign(n, {});
+    for (int i = 0; i < n; ++i) (*cuts)[i] = {0, stages[i]};
+    *lists = std::move(whole);
+    if (cap < 2 || waves > 1) return;
+
+    const double share = (total + kPieceStages * n) / num_sms + kPieceStages;
+    std::vector<std::vector<int>> c2(n);
+    std::vector<std::vector<std::pair<int, int>>> l2(1);
+    double load = 0, end = 0;
+    auto next_cta = [&] {
+        l2.push_back({});
+        load = 0;
+    };
+    for (int i = 0; i < n; ++i) {
+        c2[i] = {0};
+        int at = 0;
+        while (at < stages[i]) {
+            const bool more = static_cast<int>(l2.size()) < num_sms;
+            const double room = share - load - kPieceStages;
+            int take = stages[i] - at;
+            if (more && take > room + 0.5) {
+                const int fit = static_cast<int>(room);
+                if (fit >= 1 && static_cast<int>(c2[i].size()) < cap) {
+                    take = fit;
+                } else if (load > 0) {
+                    next_cta();
+                    continue;
+                }
+            }
+            l2.back().push_back({i, static_cast<int>(c2[i].size()) - 1});
+            at += take;
+            c2[i].push_back(at);
+            load += take + kPieceStages;
+            end = std::max(end, load);
+            if (more && static_cast<int>(l2.back().size()) >= kWindowUnits) next_cta();
+        }
+    }
+    for (const auto& l : l2)
+        if (static_cast<int>(l.size()) > kWindowUnits) return;
+    if (end + kMergeStages < whole_end) {
+        if (l2.back().empty()) l2.pop_back();
+        *cuts = std::move(c2);
+        *lists = std::move(l2);
+    }
+}
+
 // The planner of oxd_paged_prefill_plan (window 0) and oxd_window_prefill_plan.
 oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sinks,
                         const int32_t* qo_indptr, const int32_t* indptr, const int32_t* last,
@@ -158,8 +244,8 @@ oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sink
             for (int qt = 0; qt * Tr < q_len; ++qt) {
                 const int p0 = static_cast<int>(L - q_len + qt * Tr);
                 const int kv_end = p0 + std::min(Tr, q_len - qt * Tr);
-                const int skip = window > 0 ? window_stages(window, sinks, p0, stage).skip : 0;
-                n += static_cast<int64_t>(H) * ((kv_end + stage - 1) / stage - skip);
+                const int skip = window > 0 ? window_pages(window, sinks, p0, ps).skip * ps : 0;
+                n += static_cast<int64_t>(H) * ((kv_end - skip + stage - 1) / stage);
             }
         }
         return n;
@@ -194,11 +280,9 @@ oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sink
     // ---- tiles: up to T query tokens of one request with the G heads of one
     // KV head; a tile streams its request's cached tokens up to the position
     // of its last query token.
-    // With a window it skips the stages between the sinks and its first query's
-    // window.
+    // (With a window its tokens are counted without the pages that it skips.)
     struct Tile {
         int b, hkv, q0, n_tok, p0, stages, kv_end;
-        WindowStages w;
     };
     std::vector<Tile> tiles;
     int64_t total_stages = 0;
@@ -208,42 +292,30 @@ oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sink
         for (int qt = 0; qt * T < q_len; ++qt) {
             const int n_tok = std::min(T, q_len - qt * T);
             const int p0 = static_cast<int>(L - q_len + qt * T);
-            const int kv_end = p0 + n_tok;
-            const WindowStages w = window > 0 ? window_stages(window, sinks, p0, stage_tokens)
-                                              : WindowStages{0, 0};
-            const int stages = (kv_end + stage_tokens - 1) / stage_tokens - w.skip;
+            const int skip = window > 0 ? window_pages(window, sinks, p0, ps).skip * ps : 0;
+            const int kv_end = p0 + n_tok - skip;
+            const int stages = (kv_end + stage_tokens - 1) / stage_tokens;
             for (int h = 0; h < H; ++h) {
-                tiles.push_back({b, h, qo_indptr[b] + qt * T, n_tok, p0, stages, kv_end, w});
+                tiles.push_back({b, h, qo_indptr[b] + qt * T, n_tok, p0, stages, kv_end});
                 total_stages += stages;
             }
         }
     }
     if (tiles.empty()) return OXD_ERR_INVALID_ARGUMENT;  // no query token at all
-    // ---- pieces: when the tiles alone do not fill the resident CTAs, long
-    // tiles are cut into pieces of about equal stage counts
-    const int64_t resident = static_cast<int64_t>(num_sms) * ctas_per_sm;
-    int64_t chunk = std::numeric_limits<int64_t>::max();
-    if (d.max_splits != 1 && static_cast<int64_t>(tiles.size()) < resident)
-        chunk = std::max<int64_t>(kMinPieceTokens / stage_tokens,
-                                  (total_stages + resident - 1) / resident);
+    // ---- pieces: each tile's stages cut at `cuts` (0 and its stages among them)
     const int cap = d.max_splits > 1 ? std::min(d.max_splits, kMaxPieces) : kMaxPieces;
     std::vector<PrefillUnit> units;
     std::vector<int4> entries;
     int64_t n_groups = 0;
     int n_split = 0, max_pieces = 1;
-    for (const Tile& t : tiles) {
-        int S = 1;
-        if (chunk != std::numeric_limits<int64_t>::max())
-            S = static_cast<int>(std::min<int64_t>(
-                {(t.stages + chunk - 1) / chunk, static_cast<int64_t>(cap),
-                 static_cast<int64_t>(t.stages)}));
-        S = std::max(1, S);
+    auto add_tile = [&](const Tile& t, const std::vector<int>& cuts) {
+        const int S = static_cast<int>(cuts.size()) - 1;
         max_pieces = std::max(max_pieces, S);
         int state = 0;
         if (S > 1) {
             ++n_split;
             if (n_groups + static_cast<int64_t>(t.n_tok) * S >= (int64_t{1} << 31) / rows)
-                return OXD_ERR_UNSUPPORTED;
+                return false;
             state = static_cast<int>(n_groups);
             n_groups += static_cast<int64_t>(t.n_tok) * S;
             for (int i = 0; i < t.n_tok; ++i)
@@ -252,13 +324,9 @@ oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sink
         }
         const int64_t L = static_cast<int64_t>(indptr[t.b + 1] - indptr[t.b] - 1) * ps + last[t.b];
         for (int i = 0; i < S; ++i) {
-            const int s0 = static_cast<int>(static_cast<int64_t>(t.stages) * i / S);
-            const int s1 = static_cast<int>(static_cast<int64_t>(t.stages) * (i + 1) / S);
             PrefillUnit u{};
-            u.kv_begin = (s0 + (s0 >= t.w.front ? t.w.skip : 0)) * stage_tokens;
-            u.kv_valid = (s1 - s0) * stage_tokens;
-            if (s1 == t.stages)  // its last stage ends at the last query token
-                u.kv_valid -= (s1 + t.w.skip) * stage_tokens - t.kv_end;
+            u.kv_begin = cuts[i] * stage_tokens;
+            u.kv_valid = std::min(t.kv_end, cuts[i + 1] * stage_tokens) - u.kv_begin;
             u.idx_begin = indptr[t.b] + u.kv_begin / ps;
             u.n_pages = (u.kv_valid + ps - 1) / ps;
             u.q_begin = t.q0;
@@ -274,11 +342,53 @@ oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sink
             u.page_base = indptr[t.b];
             units.push_back(u);
         }
+        return true;
+    };
+    std::vector<int32_t> cta_begin;  // of the persistent kernel
+    if (window > 0 && !narrow) {
+        std::vector<std::vector<int>> cuts(tiles.size());
+        std::vector<std::vector<std::pair<int, int>>> lists;  // (tile, piece) of each CTA
+        std::vector<int> stages(tiles.size());
+        for (size_t i = 0; i < tiles.size(); ++i) stages[i] = tiles[i].stages;
+        share_out(stages, num_sms, d.max_splits == 1 ? 1 : cap, &cuts, &lists);
+        std::vector<size_t> first(tiles.size());
+        std::vector<PrefillUnit> all;
+        for (size_t i = 0; i < tiles.size(); ++i) {
+            first[i] = units.size();
+            if (!add_tile(tiles[i], cuts[i])) return OXD_ERR_UNSUPPORTED;
+        }
+        all.swap(units);
+        for (const auto& l : lists) {
+            cta_begin.push_back(static_cast<int32_t>(units.size()));
+            for (const auto& [tile, piece] : l) units.push_back(all[first[tile] + piece]);
+        }
+        cta_begin.push_back(static_cast<int32_t>(units.size()));
+    } else {
+        // when the tiles alone do not fill the resident CTAs, long tiles are cut into
+        // pieces of about equal stage counts
+        const int64_t resident = static_cast<int64_t>(num_sms) * ctas_per_sm;
+        int64_t chunk = std::numeric_limits<int64_t>::max();
+        if (d.max_splits != 1 && static_cast<int64_t>(tiles.size()) < resident)
+            chunk = std::max<int64_t>(kMinPieceTokens / stage_tokens,
+                                      (total_stages + resident - 1) / resident);
+        for (const Tile& t : tiles) {
+            int S = 1;
+            if (chunk != std::numeric_limits<int64_t>::max())
+                S = static_cast<int>(std::min<int64_t>(
+                    {(t.stages + chunk - 1) / chunk, static_cast<int64_t>(cap),
+                     static_cast<int64_t>(t.stages)}));
+            S = std::max(1, S);
+            std::vector<int> cuts(S + 1);
+            for (int i = 0; i <= S; ++i)
+                cuts[i] = static_cast<int>(static_cast<int64_t>(t.stages) * i / S);
+            if (!add_tile(t, cuts)) return OXD_ERR_UNSUPPORTED;
+        }
+        // longest pieces first: the block scheduler starts CTAs in grid order
+        std::stable_sort(units.begin(), units.end(),
+                         [](const PrefillUnit& a, const PrefillUnit& x) {
+                             return a.kv_valid > x.kv_valid;
+                         });
     }
-    // longest pieces first: the block scheduler starts CTAs in grid order
-    std::stable_sort(units.begin(), units.end(), [](const PrefillUnit& a, const PrefillUnit& x) {
-        return a.kv_valid > x.kv_valid;
-    });
     if (units.size() >= (size_t{1} << 31)) return OXD_ERR_UNSUPPORTED;
 
     oxd_prefill_plan P = new (std::nothrow) oxd_prefill_plan_s();
@@ -304,7 +414,9 @@ oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sink
     P->pairs = pairs;
     P->off_units = sizeof(WsHeader);
     P->off_entries = align_up(P->off_units + sizeof(PrefillUnit) * units.size(), 256);
-    P->meta_bytes = align_up(P->off_entries + 16 * std::max<size_t>(entries.size(), 1), 256);
+    P->off_ctas = align_up(P->off_entries + 16 * std::max<size_t>(entries.size(), 1), 256);
+    P->n_ctas = cta_begin.empty() ? P->n_units : static_cast<int>(cta_begin.size()) - 1;
+    P->meta_bytes = align_up(P->off_ctas + 4 * cta_begin.size(), 256);
     P->off_part_o = P->meta_bytes;
     P->off_part_lse =
         align_up(P->off_part_o + static_cast<size_t>(n_groups) * G * kHeadDim * 4, 256);
@@ -329,6 +441,8 @@ oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sink
         std::memset(m, 0, image_bytes);
         std::memcpy(m + P->off_units, units.data(), sizeof(PrefillUnit) * units.size());
         if (!entries.empty()) std::memcpy(m + P->off_entries, entries.data(), 16 * entries.size());
+        if (!cta_begin.empty())
+            std::memcpy(m + P->off_ctas, cta_begin.data(), 4 * cta_begin.size());
         P->stamp = next_plan_stamp();
         std::memcpy(m + P->meta_bytes, &P->stamp, sizeof(P->stamp));
     }
@@ -531,11 +645,13 @@ oxd_status oxd_paged_prefill_run(oxd_prefill_plan plan, const void* q, const voi
     p.wait_ns = d.wait_timeout_ns > 0 ? d.wait_timeout_ns : kWaitTimeoutNs;
     p.window = plan->window;
     p.sinks = plan->sinks;
+    p.cta_begin = reinterpret_cast<const int32_t*>(ws + plan->off_ctas);
 
     if (plan->ev_before != nullptr && cudaEventRecord(plan->ev_before, s) != cudaSuccess)
         return OXD_ERR_CUDA;
-    if ((plan->narrow ? launch_prefill_narrow(tk, tv, tq, p, plan->n_units, s)
-                      : launch_prefill(tk, tv, p, plan->n_units, s)) != cudaSuccess)
+    if ((plan->narrow        ? launch_prefill_narrow(tk, tv, tq, p, plan->n_units, s)
+         : plan->window > 0 ? launch_prefill_window(tk, tv, p, plan->n_ctas, s)
+                            : launch_prefill(tk, tv, p, plan->n_units, s)) != cudaSuccess)
         return OXD_ERR_CUDA;
     if (plan->ev_after != nullptr && cudaEventRecord(plan->ev_after, s) != cudaSuccess)
         return OXD_ERR_CUDA;

@@ -83,8 +83,6 @@ struct PCtl {
 // so no alignment slack: two CTAs fit one SM.
 constexpr int kPSmemBytes = kPCtlOff + static_cast<int>(sizeof(PCtl));
 
-using Window = TileWindow<kNarrowStageTokens>;
-
 // kWindow: queries see a window of their last tokens and the sinks (an instantiation
 // of its own, so its code does not weigh on the other).
 template <bool kWindow>
@@ -152,10 +150,9 @@ __global__ void __launch_bounds__(kPThreads)
                          p.n_states;
             if constexpr (kWindow) {
                 if (ok) {
-                    Window w;
+                    TileWindow w;
                     w.init(p, u);
-                    ok = w.inside(u, (u.kv_valid + kNarrowStageTokens - 1) / kNarrowStageTokens,
-                                  kNarrowStageTokens / ps, p.nnz);
+                    ok = w.inside(u, ps, p.nnz);
                 }
             }
         } else {
@@ -190,8 +187,8 @@ __global__ void __launch_bounds__(kPThreads)
     PrefillUnit u{};
     if (usable) u = p.units[blockIdx.x];
     const int n_st = usable ? (u.kv_valid + kNarrowStageTokens - 1) / kNarrowStageTokens : 0;
-    Window win_t;
-    if constexpr (kWindow) win_t.init(p, u);
+    TileWindow sight;
+    if constexpr (kWindow) sight.init(p, u);
 
     if (warp >= 5) {
         // ================================================ producer warps
@@ -201,11 +198,14 @@ __global__ void __launch_bounds__(kPThreads)
         const int pps = kNarrowStageTokens / ps;  // pages per stage (divides 32)
         const int32_t* idx = p.indices + u.idx_begin;
         int win = 0, nxt = 0, win_base = 0;
-        if constexpr (kWindow) {
-            nxt = window_page(win_t, p, u, 0, n_st, lane);
-        } else if (n_st > 0) {
-            if (lane < u.n_pages) win = __ldg(idx + lane);
-            if (32 + lane < u.n_pages) nxt = __ldg(idx + 32 + lane);
+        // page j of the piece
+        auto page_index = [&](int j) {
+            if constexpr (kWindow) return __ldg(p.indices + u.page_base + sight.entry(u, ps, j));
+            return __ldg(idx + j);
+        };
+        if (n_st > 0) {
+            if (lane < u.n_pages) win = page_index(lane);
+            if (32 + lane < u.n_pages) nxt = page_index(32 + lane);
         }
         auto check_window = [&]() {
             const bool bad = win < 0 || static_cast<int64_t>(win) >= p.num_pages;
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kPThreads)
                 record_status(p.status, p.epoch, kDeviceBadPage);
             win = bad ? 0 : win;  // an index outside the pool reads page 0
         };
-        if (!kWindow && n_st > 0) check_window();
+        if (n_st > 0) check_window();
         const int n_slots = is_k ? kPKStages : kPVStages;
         uint64_t* full = is_k ? ctl.kfull : ctl.vfull;
         uint64_t* empty = is_k ? ctl.kempty : ctl.vempty;
@@ -226,16 +226,10 @@ __global__ void __launch_bounds__(kPThreads)
             const int slot = s % n_slots;
             const int pg0 = s * pps;
             const int npg = min(pps, u.n_pages - pg0);
-            if constexpr (kWindow) {
-                win = nxt;  // the stage's pages, a lane's own; the next stage's are read now
-                nxt = window_page(win_t, p, u, s + 1, n_st, lane);
-                if (__any_sync(0xffffffffu, win < 0) && lane == 0)
-                    record_status(p.status, p.epoch, kDeviceBadPage);
-                win = max(win, 0);
-            } else if (pg0 >= win_base + 32) {
+            if (pg0 >= win_base + 32) {
                 win = nxt;
                 win_base += 32;
-                nxt = win_base + 32 + lane < u.n_pages ? __ldg(idx + win_base + 32 + lane) : 0;
+                nxt = win_base + 32 + lane < u.n_pages ? page_index(win_base + 32 + lane) : 0;
                 check_window();
             }
             int okw = 1;
@@ -254,8 +248,7 @@ __global__ void __launch_bounds__(kPThreads)
                 }
             }
             const int j = lane >> 1;
-            const int page =
-                kWindow ? win : __shfl_sync(0xffffffffu, win, (pg0 - win_base + j) & 31);
+            const int page = __shfl_sync(0xffffffffu, win, (pg0 - win_base + j) & 31);
             if (lane < 2 * npg) {
                 const uint32_t dst = (is_k ? ring_k(slot) : ring_v(slot)) + j * ps * 128 +
                                      ((lane & 1) ? kPHalf : 0);
@@ -357,8 +350,10 @@ __global__ void __launch_bounds__(kPThreads)
         const int r = threadIdx.x;  // 0 .. 127
         const int t = r / G, gi = r - (r / G) * G;
         const bool row_ok = r < G * p.tile_tokens && t < u.n_tok;
-        // (padding rows see everything, or with a window what the last query sees)
-        const int pos = row_ok ? u.p0 + t : kWindow ? u.p0 + u.n_tok - 1 : (1 << 30);
+        // (padding rows see everything, or with a window what the last query sees; with
+        // a window tokens are counted from the piece's first, see TileWindow)
+        const int p0 = kWindow ? sight.p0 : u.p0;
+        const int pos = row_ok ? p0 + t : kWindow ? p0 + u.n_tok - 1 : (1 << 30);
         const float sc = p.scale_log2;
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
@@ -370,7 +365,7 @@ __global__ void __launch_bounds__(kPThreads)
             tc_fence_after();
             uint32_t sr[64];
             tmem_ld64(t_s(g & 1) + lane_off, sr);
-            const int base = kWindow ? win_t.base(g) : u.kv_begin + g * kNarrowStageTokens;
+            const int base = (kWindow ? 0 : u.kv_begin) + g * kNarrowStageTokens;
             const int nvalid = min(kNarrowStageTokens, u.kv_valid - g * kNarrowStageTokens);
             // A stage that ends at or before the tile's first position is seen
             // whole by every row (the same for the whole CTA): no mask, the
@@ -378,8 +373,9 @@ __global__ void __launch_bounds__(kPThreads)
             // into the exponent's FMA. Otherwise scores are scaled and masked
             // first.
             const bool whole = nvalid == kNarrowStageTokens &&
-                               base + kNarrowStageTokens - 1 <= u.p0 && sc > 0.f &&
-                               (!kWindow || win_t.whole(base, u.p0 + u.n_tok - 1));
+                               base + kNarrowStageTokens - 1 <= p0 && sc > 0.f &&
+                               (!kWindow || base > p0 + u.n_tok - 1 - p.window ||
+                                base + kNarrowStageTokens <= sight.sinks);
             float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             if (whole) {
 #pragma unroll
@@ -390,8 +386,8 @@ __global__ void __launch_bounds__(kPThreads)
                 // visible columns of this row: below lim and, with a window, from w_lo on
                 // or below w_sink
                 const int lim = min(nvalid, pos - base + 1);
-                const int w_lo = kWindow ? pos - win_t.window + 1 - base : 0;
-                const int w_sink = kWindow ? win_t.sinks - base : 0;
+                const int w_lo = kWindow ? pos - p.window + 1 - base : 0;
+                const int w_sink = kWindow ? sight.sinks - base : 0;
 #pragma unroll
                 for (int j = 0; j < 64; ++j) {
                     const bool v = j < lim && (!kWindow || j >= w_lo || j < w_sink);
@@ -467,7 +463,7 @@ __global__ void __launch_bounds__(kPThreads)
                 tmem_wait_st();
             }
             const bool last = g == n_st - 1;
-            if ((last && nvalid < kNarrowStageTokens) || (kWindow && win_t.hides(g))) {
+            if ((last && nvalid < kNarrowStageTokens) || (kWindow && sight.hides(base, kNarrowStageTokens))) {
                 // zero V rows that no row sees (past the piece, before the tile's
                 // window) once the stage's V landed (whole 128-byte
                 // rows, so the swizzle does not matter); PV(g - 2) was issued
@@ -486,7 +482,8 @@ __global__ void __launch_bounds__(kPThreads)
                     }
                 };
                 zero_rows(nvalid, kNarrowStageTokens);
-                if constexpr (kWindow) zero_rows(win_t.hidden0(base), win_t.hidden1(base));
+                if constexpr (kWindow)
+                    zero_rows(sight.hidden0(base), sight.hidden1(base, kNarrowStageTokens));
                 fence_proxy_async_smem();
             }
             tc_fence_before();
