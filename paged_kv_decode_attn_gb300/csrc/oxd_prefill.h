@@ -115,10 +115,14 @@ cudaError_t launch_prefill_narrow(const CUtensorMap& tk, const CUtensorMap& tv,
                                   cudaStream_t stream, bool early = false);
 
 // The persistent kernel of prefills with a window (oxd_prefill_window.cu): tiles and
-// stages of the two-half kernel, one CTA a SM, each with up to kWindowUnits units.
-constexpr int kWindowUnits = 256;
+// stages of the two-half kernel, one CTA a SM, each with up to kWindowUnits units. Their
+// n_pages fills the last stage where the request has the pages.
+constexpr int kWindowUnits = 32;
 cudaError_t prefill_window_smem_bytes(int* bytes);
+// tq: q as (d, head, token) with a box of 64 x G x (128 / G) and the 128-byte swizzle,
+// used where G divides 128.
 cudaError_t launch_prefill_window(const CUtensorMap& tk, const CUtensorMap& tv,
-                                  const PrefillParams& p, int grid, cudaStream_t stream);
+                                  const CUtensorMap& tq, const PrefillParams& p, int grid,
+                                  cudaStream_t stream);
 
 }  // namespace oxd

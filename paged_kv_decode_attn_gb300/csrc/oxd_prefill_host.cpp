@@ -329,6 +329,12 @@ oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sink
             u.kv_valid = std::min(t.kv_end, cuts[i + 1] * stage_tokens) - u.kv_begin;
             u.idx_begin = indptr[t.b] + u.kv_begin / ps;
             u.n_pages = (u.kv_valid + ps - 1) / ps;
+            if (window > 0 && !narrow) {
+                const int64_t left = static_cast<int64_t>(indptr[t.b + 1]) - indptr[t.b] -
+                                     window_pages(window, sinks, t.p0, ps).skip - u.kv_begin / ps;
+                u.n_pages = static_cast<int>(std::min<int64_t>(
+                    left, static_cast<int64_t>(cuts[i + 1] - cuts[i]) * (stage_tokens / ps)));
+            }
             u.q_begin = t.q0;
             u.n_tok = t.n_tok;
             u.p0 = t.p0;
@@ -588,16 +594,16 @@ oxd_status oxd_paged_prefill_run(oxd_prefill_plan plan, const void* q, const voi
     if (!encode_kv_pool(&tk, k_pages, d.layout, d.page_size, d.num_kv_heads, d.num_pages) ||
         !encode_kv_pool(&tv, v_pages, d.layout, d.page_size, d.num_kv_heads, d.num_pages))
         return OXD_ERR_CUDA;
-    if (plan->narrow) {
+    if (plan->narrow || plan->window > 0) {
         // q as (d, head, token): a box is 64 columns x the G heads of one KV
-        // head x the tile's query tokens
+        // head x the query tokens of 128 rows
         const uint64_t dims[3] = {static_cast<uint64_t>(kHeadDim),
                                   static_cast<uint64_t>(d.num_qo_heads),
                                   static_cast<uint64_t>(plan->nq)};
         const uint64_t strides[2] = {static_cast<uint64_t>(kHeadDim) * 2,
                                      static_cast<uint64_t>(d.num_qo_heads) * kHeadDim * 2};
         const uint32_t box[3] = {64, static_cast<uint32_t>(plan->group),
-                                 static_cast<uint32_t>(plan->tile_tokens)};
+                                 static_cast<uint32_t>(kNarrowRows / plan->group)};
         if (!encode_bf16_map(&tq, q, 3, dims, strides, box)) return OXD_ERR_CUDA;
     }
 
@@ -650,7 +656,7 @@ oxd_status oxd_paged_prefill_run(oxd_prefill_plan plan, const void* q, const voi
     if (plan->ev_before != nullptr && cudaEventRecord(plan->ev_before, s) != cudaSuccess)
         return OXD_ERR_CUDA;
     if ((plan->narrow        ? launch_prefill_narrow(tk, tv, tq, p, plan->n_units, s)
-         : plan->window > 0 ? launch_prefill_window(tk, tv, p, plan->n_ctas, s)
+         : plan->window > 0 ? launch_prefill_window(tk, tv, tq, p, plan->n_ctas, s)
                             : launch_prefill(tk, tv, p, plan->n_units, s)) != cudaSuccess)
         return OXD_ERR_CUDA;
     if (plan->ev_after != nullptr && cudaEventRecord(plan->ev_after, s) != cudaSuccess)

@@ -12,11 +12,11 @@
 //   * with a window a tile is short (1024 tokens: nine stages), so that what a tile
 //     costs besides its stages counts: the kernel is persistent, one CTA a SM walking
 //     its list of pieces. K and V run ahead into the next piece, the next piece's query
-//     rows are copied (cp.async) while the last stage's softmax runs, its first score
+//     rows are copied while the last stage's softmax runs, its first score
 //     MMAs follow the last PV, and a half's epilogue overlaps the other half's products;
 //   * every stage takes one pass over its scores against the row's reference (the
-//     first: the maximum of 16 columns that the whole warp sees; a lagging reference is
-//     as good, see oxd_prefill.cu), 16 columns at a time: a warp's rows are few tokens,
+//     first: the maximum of 16 columns; a lagging reference is as good, see
+//     oxd_prefill.cu), 16 columns at a time: a warp's rows are few tokens,
 //     so that most blocks of 16 columns at the window's edges are seen by all of its rows
 //     or by none, and only the blocks in between are masked column by column. A pass
 //     whose sum shows a term above 2^64 is done again in two (maximum, then weights).
@@ -61,29 +61,41 @@ struct Piece {
     int pages;         // pages of the piece
     int first;         // index of its first page in `indices`
     int front, skip;   // pages from `front` on lie `skip` entries further
-    int p0, sinks, lo; // position of the first query, the sinks, the first token seen
+    int p0, sinks;     // position of the first query, the sinks
+    int hide0, hide1;  // tokens that no query of the call sees, [hide0, hide1) and those
+    int end;           // from `end` on, behind the request's last
     int q_begin, n_tok, hkv;
     int state, n_pieces, piece;
+    int pad[2];
 };
-static_assert(sizeof(Piece) == 64, "four 16-byte loads");
+static_assert(sizeof(Piece) == 80, "five 16-byte loads");
 
 struct Ctl {
     uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
-    uint64_t q_ready[2];  // a half's query rows are in shared memory (one arrival a warp)
+    uint64_t q_ready[2];  // a half's query rows are in shared memory (G divides 128: their
+                          // copies' bytes; else one arrival a warp)
     uint64_t s_ready[2];  // the n-th scores of the half: phase n
     uint64_t p_ready[2];  // their P written (one arrival a warp)
     uint64_t o_done[2];   // the half's last PV of a piece
     uint64_t mma_done;
-    int kissued[kStages], vissued[kStages];
+    int kissued[kStages], vissued[kStages], qissued[2];
     uint32_t tmem;
     int flags[3];  // [0] abort, [1] pieces of this CTA
 };
 constexpr int kListOff = kCtlOff + (static_cast<int>(sizeof(Ctl)) + 15) / 16 * 16;
-constexpr int kSmemBytes = kListOff + kWindowUnits * static_cast<int>(sizeof(Piece));
+// a softmax warp's outputs on their way out: 32 rows of 128 bytes
+constexpr int kOutOff = kListOff + kWindowUnits * static_cast<int>(sizeof(Piece));
+constexpr int kOutBytes = 32 * 128;
+constexpr int kSmemBytes = kOutOff + 8 * kOutBytes;
 static_assert(kSmemBytes <= 227 * 1024, "one CTA a SM");
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// The lowest n bits (all of 32, none for a negative n).
+__device__ __forceinline__ uint32_t below(int n) {
+    return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u;
 }
 
 // Unit `u` as a piece; n_st 0 (recorded) if it is not one that this plan can have.
@@ -123,7 +135,14 @@ __device__ __forceinline__ Piece make_piece(const PrefillParams& p, const Prefil
     c.skip = w.skip;
     c.p0 = w.p0;
     c.sinks = w.sinks;
-    c.lo = w.lo;
+    // The call's first query sees from token lo on; what lies before it and is no sink no
+    // query sees. (With skipped pages in between: the rest of the sinks' pages, and of the
+    // first page behind them if that is the first query's.)
+    const int begin = u.kv_begin;
+    const int lo = u.kv_len - (p.qo_indptr[b + 1] - p.qo_indptr[b]) - p.window + 1;
+    c.hide0 = w.sinks;
+    c.hide1 = max(min((w.front + begin / ps) * ps, lo), lo - w.skip * ps) - begin;
+    c.end = u.kv_len - w.skip * ps - begin;
     c.q_begin = u.q_begin;
     c.n_tok = u.n_tok;
     c.hkv = u.hkv;
@@ -143,6 +162,7 @@ __device__ __forceinline__ Piece make_piece(const PrefillParams& p, const Prefil
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_window_kernel(const __grid_constant__ CUtensorMap tmap_k,
                           const __grid_constant__ CUtensorMap tmap_v,
+                          const __grid_constant__ CUtensorMap tmap_q,
                           const __grid_constant__ PrefillParams p) {
     extern __shared__ __align__(1024) uint8_t sm[];
     Ctl& ctl = *reinterpret_cast<Ctl*>(sm + kCtlOff);
@@ -163,10 +183,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ctl.kissued[s] = ctl.vissued[s] = 0;
         }
         for (int h = 0; h < 2; ++h) {
-            mbar_init(&ctl.q_ready[h], 4);
+            mbar_init(&ctl.q_ready[h], 128 % G == 0 ? 1 : 4);
             mbar_init(&ctl.s_ready[h], 1);
             mbar_init(&ctl.p_ready[h], 4);
             mbar_init(&ctl.o_done[h], 1);
+            ctl.qissued[h] = 0;
         }
         mbar_init(&ctl.mma_done, 1);
         flags[0] = 0;
@@ -190,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kKWarp && lane == 0) {
         prefetch_tmap(&tmap_k);
         prefetch_tmap(&tmap_v);
+        prefetch_tmap(&tmap_q);
     }
     {
         // the CTA's pieces, a thread a unit, checked before anything uses them (and the
@@ -371,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_off = static_cast<uint32_t>(32 * wq) << 16;
         const int r = threadIdx.x & 127;
         const int R = 128 * h + r;  // row of the tile: token R / G, head R % G
-        const int t = R / G, gi = R - t * G;
+        const int t = R / G;
         const uint32_t g_magic = (65536u + G - 1) / G;  // R / G = R * magic >> 16 below 256
         const uint32_t ts = t_s(h);
         // (a scale of zero as the smallest normal number: a masked score stays -inf)
@@ -380,11 +402,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         // Copies the half's query rows of piece `c` into shared memory, laid out as the
         // score MMA's A operand: two 64-column halves of [128 rows][128 B] with the
-        // 128-byte swizzle (16-byte chunk j of row r at chunk j ^ (r % 8)). A warp copies
-        // its 32 rows, 16 lanes a row; zeros past the tile.
+        // 128-byte swizzle (16-byte chunk j of row r at chunk j ^ (r % 8)). Where G divides
+        // 128 the half's rows are a box of G heads x 128 / G tokens (rows past the tile are
+        // other queries, or zeros behind the last); otherwise a warp copies its 32 rows, 16
+        // lanes a row, zeros past the tile.
+        const bool boxed = 128 % G == 0;
         auto copy_query = [&](const Piece& c) {
+            if (boxed) {
+                if (r == 0) {
+                    ctl.qissued[h] += 1;
+                    mbar_arrive_expect_tx(&ctl.q_ready[h], 2 * kQHalf);
+                    tma_load_3d(s_q(h), &tmap_q, &ctl.q_ready[h], 0, c.hkv * G,
+                                c.q_begin + h * (128 / G));
+                    tma_load_3d(s_q(h) + kQHalf, &tmap_q, &ctl.q_ready[h], 64, c.hkv * G,
+                                c.q_begin + h * (128 / G));
+                }
+                return;
+            }
             const int col = lane & 15;
-#pragma unroll 4
+#pragma unroll 1
             for (int i = 0; i < 16; ++i) {
                 const uint32_t row = 32 * wq + 2 * i + (lane >> 4);
                 const uint32_t RR = 128 * h + row, tt = RR * g_magic >> 16;
@@ -399,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         auto query_ready = [&]() {
+            if (boxed) return;
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();
             __syncwarp();
@@ -420,21 +457,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int pi = 0; pi < n_pieces && ok; n0 += list[pi].n_st, ++pi) {
             const Piece c = list[pi];
             const int nst = c.nst[h];
-            const bool row_ok = c.n_st > 0 && t < c.n_tok;
             // (padding rows see what the tile's last query sees)
             const int pos = c.p0 + min(t, c.n_tok - 1);
             const int w_lo = pos - p.window + 1;  // the row sees [w_lo, pos] and [0, sinks)
             const int pos_a = __shfl_sync(0xffffffffu, pos, 0);   // the warp's first
             const int pos_z = __shfl_sync(0xffffffffu, pos, 31);  // and last position
-            const int lo_a = pos_a - p.window + 1, lo_z = pos_z - p.window + 1;
-            // whether every row, or none, of the warp sees the columns [c0, c1)
+            const int lo_z = pos_z - p.window + 1;
+            // whether every row of the warp sees the columns [c0, c1)
             auto all_see = [&](int c0, int c1) {
                 return c1 <= pos_a + 1 && (c0 >= lo_z || c1 <= c.sinks);
             };
-            auto none_sees = [&](int c0, int c1) {
-                return c0 > pos_z || (c1 <= lo_a && c0 >= c.sinks);
+            auto sees = [&](int v) {
+                return static_cast<unsigned>(v - w_lo) < static_cast<unsigned>(p.window) ||
+                       (v < c.sinks && v <= pos);
             };
-            auto sees = [&](int v) { return v <= pos && (v >= w_lo || v < c.sinks); };
             float m_ref = -INFINITY, l = 0.f;
             for (int g = 0; g < nst; ++g, ++n) {
                 if (!wait_all(&ctl.s_ready[h], n)) {
@@ -455,21 +491,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool rescale = false, done = false;
                 float alpha = 1.f;
                 const bool whole = all_see(base, base + kTokens);
-                bool one_pass = true;
-                if (__any_sync(0xffffffffu, m_ref == -INFINITY)) {
-                    // rows without a reference take the maximum of 16 columns that the
-                    // whole warp sees, where there are any
-                    int at = -1;
-                    bool some = whole;
-                    if (whole) {
-                        at = 0;
-                    } else {
+                // the columns that the row sees, a bit each
+                uint32_t see[4];
+                if (!whole) {
+                    const int from = w_lo - base, to = pos + 1 - base;
+                    const int first = min(c.sinks - base, to);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int c0 = base + 16 * i;
-                            if (all_see(c0, c0 + 16)) at = i;
-                            if (!none_sees(c0, c0 + 16)) some = true;
-                        }
+                    for (int k = 0; k < 4; ++k)
+                        see[k] = (below(to - 32 * k) & ~below(from - 32 * k)) | below(first - 32 * k);
+                }
+                if (__any_sync(0xffffffffu, m_ref == -INFINITY)) {
+                    // rows without a reference take the maximum of what they see of the last
+                    // 16 columns that some row sees (at the window's start a row that sees
+                    // anything of the stage sees the last ones)
+                    int at = 7;
+                    uint32_t bits = 0xffffu;
+                    if (!whole) {
+                        at = -1;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (__any_sync(0xffffffffu, (see[i >> 1] >> 16 * (i & 1) & 0xffffu) != 0)) {
+                                at = i;
+                                bits = see[i >> 1] >> 16 * (i & 1);
+                            }
                     }
                     if (at >= 0) {
                         uint32_t a[16];
@@ -477,13 +521,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld_wait16(a);
                         float mx = -INFINITY;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) mx = fmaxf(mx, __uint_as_float(a[j]) * sc);
+                        for (int j = 0; j < 16; ++j)
+                            if (bits >> j & 1) mx = fmaxf(mx, __uint_as_float(a[j]) * sc);
                         if (m_ref == -INFINITY) m_ref = mx;
-                    } else if (some) {
-                        one_pass = false;
                     }
                 }
-                if (one_pass) {
+                {
                     // P = 2^(s sc - m_ref) for 16 columns at a time (the next 16 loading
                     // meanwhile), kept in registers until the row's sum shows that no
                     // term exceeds 2^64 (nor is infinite). The reference may lag the
@@ -506,17 +549,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     };
                     auto edge = [&](uint32_t (&x)[16], int i) {
-                        const int c0 = base + 16 * i;
-                        if (none_sees(c0, c0 + 16)) {
+                        const uint32_t bits = see[i >> 1] >> 16 * (i & 1);
+                        if (!__any_sync(0xffffffffu, (bits & 0xffffu) != 0)) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j) pk[8 * i + j] = 0u;
                             return;
                         }
-                        if (!all_see(c0, c0 + 16)) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (!sees(c0 + j)) x[j] = __float_as_uint(hidden);
-                        }
+                        for (int j = 0; j < 16; ++j)
+                            if (!(bits >> j & 1)) x[j] = __float_as_uint(hidden);
                         math(x, i);
                     };
                     auto pass = [&](auto&& chunk) {
@@ -601,10 +642,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 tmem_wait_st();
-                // rows of V that no row sees: past the piece, between the sinks and the window
-                const int end = c.p0 + c.n_tok - base;  // behind the last query's token
-                const bool hides = c.lo > max(c.sinks, base) && c.sinks < base + kTokens;
-                if (end < kTokens || hides) {
+                // rows of V that no query sees: behind the request's last token, between the
+                // sinks and the first query's window
+                const int end = c.end - base;
+                const int z0 = max(c.hide0 - base, 0), z1 = min(c.hide1 - base, kTokens);
+                if (end < kTokens || z1 > z0) {
                     // Zeroed once the stage's V landed (whole 128-byte rows, so the swizzle
                     // does not matter), by every half that reads it, before its own PV (the
                     // other may read it meanwhile: it has zeroed the same rows). The slot's
@@ -622,8 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                       (cc & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                         }
                     };
-                    if (end < kTokens) zero_rows(end, kTokens);
-                    if (hides) zero_rows(max(c.sinks - base, 0), min(c.lo - base, kTokens));
+                    zero_rows(max(end, 0), kTokens);
+                    zero_rows(z0, z1);
                     fence_proxy_async_smem();  // (the PV waits for all four warps' arrivals)
                 }
                 if (last && usable(pi + 1) < n_pieces) query_ready();
@@ -635,54 +677,84 @@ __global__ void __launch_bounds__(kThreads, 1)
             // in the collective loads. A piece that the half's rows see nothing of leaves
             // them an empty state (a split tile's merge weighs it 0).
             if (ok && nst > 0 && !wait_all(&ctl.o_done[h], n_o++)) ok = false;
-            if (ok && (nst > 0 || (row_ok && c.n_pieces > 1))) {
+            if (ok && (nst > 0 || (c.n_st > 0 && c.n_pieces > 1))) {
                 tc_fence_after();
                 const bool seen = l > 0.f;
                 const float inv = seen ? 1.f / l : 0.f;
                 const float lse2 = seen ? m_ref + __log2f(l) : -INFINITY;
-                const int hq = c.hkv * G + gi;
-                const size_t grp = static_cast<size_t>(c.state) +
-                                   static_cast<size_t>(t) * c.n_pieces + c.piece;
-                const size_t row = static_cast<size_t>(c.q_begin + t) * p.num_qo_heads + hq;
-#pragma unroll 1
-                for (int c0 = 0; c0 < kHeadDim; c0 += 64) {
-                    uint32_t o[64];
-                    if (nst > 0) {
-                        tmem_ld64(t_o(h) + lane_off + c0, o);
-                    } else {
+                // The rows go out through shared memory, 128 bytes of each at a time, so that
+                // eight lanes write a whole line (a lane its own row: 32 lines a store,
+                // 300 -> 272 us without them). 16-byte chunk j of row i at j ^ (i % 8).
+                uint8_t* stage = sm + kOutOff + warp * kOutBytes;
+                const bool whole_tile = c.n_pieces == 1;
+                const size_t row_bytes = whole_tile ? kHeadDim * 2 : kHeadDim * 4;
+                uint8_t* dst0 = whole_tile ? reinterpret_cast<uint8_t*>(p.out)
+                                           : reinterpret_cast<uint8_t*>(p.part_o);
+                // row of the output, or of the partial states, of row RR of the tile
+                auto out_row = [&](uint32_t RR) {
+                    const uint32_t tt = RR * g_magic >> 16, gg = RR - tt * G;
+                    if (static_cast<int>(tt) >= c.n_tok) return int64_t{-1};
+                    return whole_tile
+                               ? static_cast<int64_t>(c.q_begin + tt) * p.num_qo_heads + c.hkv * G + gg
+                               : (static_cast<int64_t>(c.state) +
+                                  static_cast<int64_t>(tt) * c.n_pieces + c.piece) * G + gg;
+                };
+                auto send = [&](int byte0) {  // 128 bytes of every row, from byte0 on
+                    __syncwarp();
 #pragma unroll
-                        for (int j = 0; j < 64; ++j) o[j] = 0u;
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = 4 * i + (lane >> 3), j = lane & 7;
+                        const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * 128 +
+                                                                        ((j ^ (rr & 7)) << 4));
+                        const int64_t to = out_row(128 * h + 32 * wq + rr);
+                        if (to >= 0)
+                            *reinterpret_cast<uint4*>(dst0 + to * row_bytes + byte0 + j * 16) = w;
                     }
-                    if (!row_ok) continue;
-                    if (c.n_pieces == 1) {
-                        uint16_t* dst = p.out + row * kHeadDim + c0;
+                    __syncwarp();
+                };
+                if (whole_tile) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kHeadDim; c0 += 64) {
+                        uint32_t o[64];
+                        tmem_ld64(t_o(h) + lane_off + c0, o);
 #pragma unroll
-                        for (int j = 0; j < 64; j += 8) {
-                            uint4 w;
-                            w.x = pack_bf16x2(__uint_as_float(o[j]) * inv,
-                                              __uint_as_float(o[j + 1]) * inv);
-                            w.y = pack_bf16x2(__uint_as_float(o[j + 2]) * inv,
-                                              __uint_as_float(o[j + 3]) * inv);
-                            w.z = pack_bf16x2(__uint_as_float(o[j + 4]) * inv,
-                                              __uint_as_float(o[j + 5]) * inv);
-                            w.w = pack_bf16x2(__uint_as_float(o[j + 6]) * inv,
-                                              __uint_as_float(o[j + 7]) * inv);
-                            *reinterpret_cast<uint4*>(dst + j) = w;
+                        for (int j = 0; j < 8; ++j) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = pack_bf16x2(__uint_as_float(o[8 * j + 2 * k]) * inv,
+                                                   __uint_as_float(o[8 * j + 2 * k + 1]) * inv);
+                            *reinterpret_cast<uint4*>(stage + lane * 128 +
+                                                      ((j ^ (lane & 7)) << 4)) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                    } else {
-                        float* dst = p.part_o + (grp * G + gi) * kHeadDim + c0;
+                        send(c0 * 2);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
+                        uint32_t o[32];
+                        if (nst > 0) {
+                            tmem_ld32(t_o(h) + lane_off + c0, o);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 64; j += 4)
-                            *reinterpret_cast<float4*>(dst + j) =
-                                make_float4(__uint_as_float(o[j]) * inv,
-                                            __uint_as_float(o[j + 1]) * inv,
-                                            __uint_as_float(o[j + 2]) * inv,
-                                            __uint_as_float(o[j + 3]) * inv);
+                            for (int j = 0; j < 32; ++j) o[j] = 0u;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<float4*>(stage + lane * 128 +
+                                                       ((j ^ (lane & 7)) << 4)) =
+                                make_float4(__uint_as_float(o[4 * j]) * inv,
+                                            __uint_as_float(o[4 * j + 1]) * inv,
+                                            __uint_as_float(o[4 * j + 2]) * inv,
+                                            __uint_as_float(o[4 * j + 3]) * inv);
+                        send(c0 * 4);
                     }
                 }
-                if (row_ok) {
-                    if (c.n_pieces > 1)
-                        p.part_lse[grp * G + gi] = lse2;
+                const int64_t row = out_row(R);
+                if (row >= 0) {
+                    if (!whole_tile)
+                        p.part_lse[row] = lse2;
                     else if (p.lse != nullptr)
                         p.lse[row] = lse2 * kLn2;
                 }
@@ -705,6 +777,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ctl.vissued[s] > 0)
                 mbar_wait(&ctl.vfull[s], (ctl.vissued[s] - 1) & 1, nullptr, kWaitTimeoutNs);
         }
+        for (int h = 0; h < 2; ++h)
+            if (ctl.qissued[h] > 0)
+                mbar_wait(&ctl.q_ready[h], (ctl.qissued[h] - 1) & 1, nullptr, kWaitTimeoutNs);
     }
     if (warp == kMmaWarp) {
         tc_fence_after();
@@ -722,7 +797,8 @@ cudaError_t prefill_window_smem_bytes(int* bytes) {
 }
 
 cudaError_t launch_prefill_window(const CUtensorMap& tk, const CUtensorMap& tv,
-                                  const PrefillParams& p, int grid, cudaStream_t stream) {
+                                  const CUtensorMap& tq, const PrefillParams& p, int grid,
+                                  cudaStream_t stream) {
     if (grid < 1 || p.window < 1 || p.cta_begin == nullptr) return cudaErrorInvalidConfiguration;
     static std::atomic<uint64_t> done{0};
     int dev = 0;
@@ -740,7 +816,7 @@ cudaError_t launch_prefill_window(const CUtensorMap& tk, const CUtensorMap& tv,
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
-    return cudaLaunchKernelEx(&cfg, prefill_window_kernel, tk, tv, p);
+    return cudaLaunchKernelEx(&cfg, prefill_window_kernel, tk, tv, tq, p);
 }
 
 }  // namespace oxd
