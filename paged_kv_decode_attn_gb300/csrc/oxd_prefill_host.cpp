@@ -110,9 +110,16 @@ int64_t window_pairs(int64_t p0, int64_t p1, int64_t window, int64_t sinks) {
     return (mid - p0) * (p0 + mid + 1) / 2 + (p1 - mid) * most;
 }
 
-// What a piece costs the persistent kernel besides its stages, and what the merge of
-// split tiles costs a run, in stages (about 1.8 us each).
-constexpr double kPieceStages = 1.0, kMergeStages = 4.0;
+// What a piece costs the persistent kernel besides its stages (4.8 us), and what the
+// merge of split tiles costs a run, in stages (1.6 us each).
+constexpr double kPieceStages = 3.0, kMergeStages = 7.0;
+
+// Pieces of a tile of `stages` stages under a window at which it ends soonest when there
+// are SMs for all: a piece more shortens the others, and costs its tile's merge (32 queries
+// on 4096 tokens, 66 stages: 61 us whole, 24 with 4 pieces, 18 with 8, 35 with 33).
+int best_pieces(int stages) {
+    return std::max(1, static_cast<int>(std::sqrt(1.3 * stages) + 0.5));
+}
 
 // Shares tiles of `stages` out over persistent CTAs: whole tiles, the longest first, each
 // to the CTA with the least so far; or, where that ends sooner by more than the merge
@@ -152,45 +159,54 @@ void share_out(const std::vector<int>& stages, int num_sms, int cap,
     *lists = std::move(whole);
     if (cap < 2 || waves > 1) return;
 
-    const double share = (total + kPieceStages * n) / num_sms + kPieceStages;
+    // the tiles end to end, each CTA up to `most` stages and pieces: the least `most` that
+    // num_sms CTAs hold
     std::vector<std::vector<int>> c2(n);
-    std::vector<std::vector<std::pair<int, int>>> l2(1);
-    double load = 0, end = 0;
-    auto next_cta = [&] {
-        l2.push_back({});
-        load = 0;
-    };
-    for (int i = 0; i < n; ++i) {
-        c2[i] = {0};
-        int at = 0;
-        while (at < stages[i]) {
-            const bool more = static_cast<int>(l2.size()) < num_sms;
-            const double room = share - load - kPieceStages;
-            int take = stages[i] - at;
-            if (more && take > room + 0.5) {
-                const int fit = static_cast<int>(room);
-                if (fit >= 1 && static_cast<int>(c2[i].size()) < cap) {
-                    take = fit;
-                } else if (load > 0) {
-                    next_cta();
-                    continue;
+    std::vector<std::vector<std::pair<int, int>>> l2;
+    auto cut = [&](double most) {
+        l2.assign(1, {});
+        double load = 0;
+        auto next_cta = [&] {
+            l2.push_back({});
+            load = 0;
+        };
+        for (int i = 0; i < n; ++i) {
+            c2[i].assign(1, 0);
+            const int pieces = std::min(cap, best_pieces(stages[i]));
+            for (int at = 0; at < stages[i];) {
+                const int room = static_cast<int>(most - load - kPieceStages);
+                int take = stages[i] - at;
+                if (take > room) {
+                    // cut, or start at the next CTA; a tile that may not be cut once more
+                    // and does not fit whole is too much
+                    if (room >= 1 && static_cast<int>(c2[i].size()) < pieces)
+                        take = room;
+                    else if (load > 0) {
+                        next_cta();
+                        continue;
+                    } else {
+                        return false;
+                    }
                 }
+                if (static_cast<int>(l2.back().size()) == kWindowUnits) next_cta();
+                l2.back().push_back({i, static_cast<int>(c2[i].size()) - 1});
+                at += take;
+                c2[i].push_back(at);
+                load += take + kPieceStages;
             }
-            l2.back().push_back({i, static_cast<int>(c2[i].size()) - 1});
-            at += take;
-            c2[i].push_back(at);
-            load += take + kPieceStages;
-            end = std::max(end, load);
-            if (more && static_cast<int>(l2.back().size()) >= kWindowUnits) next_cta();
         }
+        return static_cast<int>(l2.size()) <= num_sms;
+    };
+    int lo = static_cast<int>((total + kPieceStages * n) / num_sms);  // too little, or just enough
+    int hi = static_cast<int>(whole_end - kMergeStages);              // where it pays
+    if (hi <= lo || !cut(hi)) return;
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        (cut(mid) ? hi : lo) = mid;
     }
-    for (const auto& l : l2)
-        if (static_cast<int>(l.size()) > kWindowUnits) return;
-    if (end + kMergeStages < whole_end) {
-        if (l2.back().empty()) l2.pop_back();
-        *cuts = std::move(c2);
-        *lists = std::move(l2);
-    }
+    cut(hi);
+    *cuts = std::move(c2);
+    *lists = std::move(l2);
 }
 
 // The planner of oxd_paged_prefill_plan (window 0) and oxd_window_prefill_plan.
@@ -383,6 +399,10 @@ oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sink
                 S = static_cast<int>(std::min<int64_t>(
                     {(t.stages + chunk - 1) / chunk, static_cast<int64_t>(cap),
                      static_cast<int64_t>(t.stages)}));
+            if (window > 0)
+                S = static_cast<int>(std::min<int64_t>(
+                    {static_cast<int64_t>(S), static_cast<int64_t>(best_pieces(t.stages)),
+                     resident / static_cast<int64_t>(tiles.size())}));
             S = std::max(1, S);
             std::vector<int> cuts(S + 1);
             for (int i = 0; i <= S; ++i)

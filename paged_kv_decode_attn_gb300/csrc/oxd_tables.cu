@@ -46,6 +46,9 @@ __global__ void __launch_bounds__(kTabThreads, 1)
     __shared__ int sums[3][kTabWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n_ctas = gridDim.x, cta = blockIdx.x;  // (the grid is one cluster)
+    // launched as a programmatic dependent: nothing in global memory before this
+    grid_dependency_wait();
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (cta == 0 && threadIdx.x == 0) *p.last_epoch = p.epoch;
     const int ps = 1 << p.page_shift;
     auto fail = [&](int code) { record_status(p.status, p.epoch, code); };
@@ -131,19 +134,35 @@ __global__ void __launch_bounds__(kTabThreads, 1)
             };
             // the first token that a new token's window holds
             const int seen = q.len - max(q.fresh, 1) + 1 - p.window;
-            for (int j = seg; j < q.need; j += stride) {
-                int page = page_of(j);
-                if (j >= q.held && page >= 0) {
-                    row[j] = page;
-                    if (page >= p.num_pages)
-                        fail(kDeviceBadPage);
-                    else if (p.refcount != nullptr)
-                        p.refcount[page] = 1;
+            // whether page j is out of every new token's sight
+            auto unseen = [&](int j) {
+                return p.window > 0 && (j << p.page_shift) >= p.sinks &&
+                       ((j + 1) << p.page_shift) <= seen;
+            };
+            // (kAhead loads in flight: a request's pages are one chain otherwise)
+            constexpr int kAhead = 8;
+            for (int j0 = seg; j0 < q.need; j0 += kAhead * stride) {
+                int pages[kAhead];
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a) {
+                    const int j = j0 + a * stride;
+                    pages[a] = j < q.need && (j >= q.held || !unseen(j)) ? page_of(j) : -1;
                 }
-                if (p.window > 0 && (j << p.page_shift) >= p.sinks &&
-                    ((j + 1) << p.page_shift) <= seen)
-                    page = -1;  // out of every new token's sight
-                if (q.first + j < p.num_indices) p.indices[q.first + j] = page;
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a) {
+                    const int j = j0 + a * stride;
+                    int page = pages[a];
+                    if (j >= q.need) break;
+                    if (j >= q.held && page >= 0) {
+                        row[j] = page;
+                        if (page >= p.num_pages)
+                            fail(kDeviceBadPage);
+                        else if (p.refcount != nullptr)
+                            p.refcount[page] = 1;
+                    }
+                    if (unseen(j)) page = -1;
+                    if (q.first + j < p.num_indices) p.indices[q.first + j] = page;
+                }
             }
             if (p.token_request != nullptr)
                 for (int t = seg; t < q.fresh && q.token0 + t < p.num_tokens; t += stride) {
@@ -197,13 +216,17 @@ cudaError_t launch_build_tables(const TablesParams& p, cudaStream_t stream) {
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kTabThreads);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    // (the kernel waits for the one before it: what that saves is its launch, 2 us of the
+    // smallest calls)
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, build_tables_kernel, p);
 }
 
