@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kPThreads)
     PrefillUnit u{};
     if (usable) u = p.units[blockIdx.x];
     const int n_st = usable ? (u.kv_valid + kNarrowStageTokens - 1) / kNarrowStageTokens : 0;
-    TileWindow sight;
+    TileWindow sight{};
     if constexpr (kWindow) sight.init(p, u);
 
     if (warp >= 5) {

@@ -367,3 +367,20 @@ def test_4bit_bad_pages_and_tables():
         out, lse = c.run()
         assert c.code == code
         assert_decode(out[keep], lse[keep], [x[keep] for x in ref])
+
+
+# ------------------------------------------------------------------ at random
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("seed", range(30))
+def test_random_decodes(seed, four):
+    rng = np.random.default_rng(2000 + seed)
+    B = int(rng.integers(1, 20))
+    lengths = [int(np.exp(rng.uniform(0, np.log(2000)))) * int(rng.random() > 0.1) for _ in range(B)]
+    G, Hkv = int(rng.integers(1, 33)), int(rng.choice([1, 2, 3, 4, 8]))
+    window, sinks = int(np.exp(rng.uniform(0, np.log(2500)))), int(rng.choice([0, 1, 4, 33, 130]))
+    ps, layout = int(rng.choice([8, 16, 32, 64])), str(rng.choice(["NHD", "HND"]))
+    c = (QuantCase if four else Case)(lengths, G, Hkv, ps, layout, window, sinks, seed=seed,
+                                      sigma=float(rng.choice([0.5, 1, 2])))
+    c.check(float(rng.choice([SCALE, -SCALE, 0.5])), f"{lengths} {G} {Hkv} {window} {sinks} {ps} {layout}",
+            max_splits=int(rng.choice([0, 0, 1, 5])))

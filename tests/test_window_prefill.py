@@ -269,3 +269,69 @@ def test_a_captured_run(rows):
     out.zero_()
     g.replay()
     Wr.assert_close(f64(out), f64(lse), c.reference())
+
+
+# ------------------------------------------------------------------ many pieces a CTA, and at random
+
+@gpu
+@pytest.mark.parametrize("rows", [128, 256])
+@pytest.mark.parametrize("layout,G,Hkv,window,sinks", [("NHD", 4, 8, 200, 4), ("HND", 1, 16, 40, 0),
+                                                       ("NHD", 12, 3, 333, 20)])
+def test_more_tiles_than_resident_ctas(rows, layout, G, Hkv, window, sinks):
+    lengths = [700, 64, 1300, 65, 900, 1, 500, 640, 777, 1000]
+    q_lens = [700, 64, 900, 1, 300, 1, 500, 63, 700, 640]
+    c = Case(lengths, q_lens, G, Hkv, 16, layout, window, sinks, seed=rows + G)
+    for splits in (0, 1):
+        out, lse = c.run(c.plan(tile_rows=rows, max_splits=splits), bind=True)
+        assert c.code == 0
+        ref = Wr.attention_torch(c.q, c.p.k, c.p.v, lengths, q_lens, window, sinks, SCALE)
+        Wr.assert_close(f64(out), f64(lse), ref, f"splits {splits}")
+
+
+@gpu
+@pytest.mark.parametrize("seed", range(40))
+def test_random_prefills(seed):
+    rng = np.random.default_rng(1000 + seed)
+    B = int(rng.integers(1, 6))
+    lengths = [int(np.exp(rng.uniform(0, np.log(1500)))) for _ in range(B)]
+    q_lens = [int(rng.integers(0, n + 1)) for n in lengths]
+    q_lens[0] = max(q_lens[0], 1)
+    G, Hkv = int(rng.choice([1, 2, 3, 4, 6, 8, 16, 40])), int(rng.choice([1, 2, 3]))
+    window, sinks = int(np.exp(rng.uniform(0, np.log(1200)))), int(rng.choice([0, 1, 4, 33, 130, 300]))
+    ps, layout = int(rng.choice([8, 16, 32, 64])), str(rng.choice(["NHD", "HND"]))
+    scale = float(rng.choice([SCALE, -SCALE, 0.5]))
+    c = Case(lengths, q_lens, G, Hkv, ps, layout, window, sinks, seed=seed, sigma=float(rng.choice([0.5, 1, 2])))
+    out, lse = c.run(c.plan(tile_rows=int(rng.choice([0, 128, 256])), max_splits=int(rng.choice([0, 1, 3]))),
+                     scale)
+    assert c.code == 0
+    ref = Wr.attention_torch(c.q, c.p.k, c.p.v, lengths, q_lens, window, sinks, scale)
+    Wr.assert_close(f64(out), f64(lse), ref, f"{lengths} {q_lens} {G} {Hkv} {window} {sinks} {ps}")
+
+
+@gpu
+@pytest.mark.parametrize("rows", [128, 256])
+def test_a_damaged_bound_list_is_reported_and_not_followed(rows):
+    """Random words over a bound work list: reported, nothing written outside the outputs."""
+    c = Case([1500, 300], [300, 40], 4, 2, 16, "NHD", 200, 9, seed=8)
+    plan = c.plan(tile_rows=rows)
+    n = len(c.q) * c.Hq
+    rng = np.random.default_rng(5)
+    out = torch.full((n * 128 + 256,), 77.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n + 8,), 77.0, device="cuda")
+    ws = torch.empty(plan.workspace_bytes + 256, dtype=torch.uint8, device="cuda")
+    for trial in range(12):
+        ws[plan.workspace_bytes:] = 55
+        oxd.oxd_prefill_plan_bind_workspace(plan, ws, plan.workspace_bytes)
+        words = ws[256:256 + plan.info.num_units * 64].view(torch.int32)
+        at = torch.as_tensor(rng.integers(0, len(words), 1 + trial * 5), device="cuda")
+        words[at] = torch.as_tensor(rng.integers(-2 ** 31, 2 ** 31, len(at)).astype(np.int32), device="cuda")
+        oxd.oxd_paged_prefill_run(plan, c.d_q, c.d_k, c.d_v, *c.tables, SCALE, out[128:-128], lse[4:-4],
+                                  ws, plan.workspace_bytes)
+        oxd.oxd_read_device_status(ws)
+        assert (out[:128] == 77).all() and (out[-128:] == 77).all() and (ws[plan.workspace_bytes:] == 55).all()
+        assert (lse[:4] == 77).all() and (lse[-4:] == 77).all()
+    words[:] = -1
+    oxd.oxd_paged_prefill_run(plan, c.d_q, c.d_k, c.d_v, *c.tables, SCALE, out[128:-128], lse[4:-4], ws,
+                              plan.workspace_bytes)
+    assert oxd.oxd_read_device_status(ws) == oxd.OXD_DEVICE_PLAN_MISMATCH
+    c.check(tile_rows=rows)

@@ -107,3 +107,31 @@ def assert_close(out, lse, ref, what=""):
         e = np.abs(np.where(none, 0, lse) - np.where(none, 0, r_lse))
         b = d + 2.0 ** -22 * (1 + np.abs(np.where(none, 0, r_lse)))
         assert (e <= b).all(), f"{what}: lse {(e / b).max():.2f} of its bound"
+
+
+def attention_torch(q, k, v, lengths, q_lens, window, sinks, sm_scale, device="cuda"):
+    """`attention` by torch in f64, for larger cases; the same outputs, as numpy arrays."""
+    import torch
+
+    n, Hq, _ = q.shape
+    qd = torch.as_tensor(q, dtype=torch.float64, device=device)
+    got = [torch.zeros((n, Hq, 128), dtype=torch.float64, device=device) for _ in range(3)]
+    lse, size = (torch.zeros((n, Hq), dtype=torch.float64, device=device) for _ in range(2))
+    lse -= np.inf
+    at = 0
+    for b, (length, ql) in enumerate(zip(lengths, q_lens)):
+        G = Hq // len(k[b])
+        pos = torch.arange(length - ql, length, device=device)[:, None]
+        j = torch.arange(length, device=device)
+        mask = (j <= pos) & ((j > pos - window) | (j < sinks))
+        for h in range(Hq):
+            kd, vd = (torch.as_tensor(x[b][h // G], dtype=torch.float64, device=device) for x in (k, v))
+            rows = qd[at:at + ql, h]
+            x = (rows @ kd.T * sm_scale).masked_fill(~mask, -np.inf)
+            w = torch.softmax(x, -1)
+            got[0][at:at + ql, h] = w @ vd
+            got[1][at:at + ql, h] = w @ vd.abs()
+            lse[at:at + ql, h] = torch.logsumexp(x, -1)
+            size[at:at + ql, h] = (rows.abs() @ kd.abs().T * abs(sm_scale)).masked_fill(~mask, 0).amax(-1)
+        at += ql
+    return [t.cpu().numpy() for t in (got[0], lse, got[1], size, got[2])]
