@@ -77,8 +77,10 @@ struct Ctl {
     uint64_t s_ready[2];  // the n-th scores of the half: phase n
     uint64_t p_ready[2];  // their P written (one arrival a warp)
     uint64_t o_done[2];   // the half's last PV of a piece
+    uint64_t vland;       // V of the k-th stage with rows to zero has landed: phase k (its vfull
+                          // comes when they are zeroed)
     uint64_t mma_done;
-    int kissued[kStages], vissued[kStages], qissued[2];
+    int kissued[kStages], vissued[kStages], qissued[2], landing, zeroed;
     uint32_t tmem;
     int flags[3];  // [0] abort, [1] pieces of this CTA
 };
@@ -88,6 +90,21 @@ constexpr int kOutOff = kListOff + kWindowUnits * static_cast<int>(sizeof(Piece)
 constexpr int kOutBytes = 32 * 128;
 constexpr int kSmemBytes = kOutOff + 8 * kOutBytes;
 static_assert(kSmemBytes <= 227 * 1024, "one CTA a SM");
+
+// The stages with rows of V that no query sees (zeroed before the product): [first, last]
+// and those from `end` on.
+struct HiddenStages {
+    int first, last, end;
+    __device__ __forceinline__ explicit HiddenStages(const Piece& c) {
+        const bool any = c.hide1 > max(c.hide0, 0);
+        first = any ? max(c.hide0, 0) / kTokens : 1;
+        last = any ? (c.hide1 - 1) / kTokens : 0;
+        end = max(c.end, 0) / kTokens;
+    }
+    __device__ __forceinline__ bool among(int g) const {
+        return (g >= first && g <= last) || g >= end;
+    }
+};
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -182,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ctl.vempty[s], 1);
             ctl.kissued[s] = ctl.vissued[s] = 0;
         }
+        ctl.landing = ctl.zeroed = 0;
         for (int h = 0; h < 2; ++h) {
             mbar_init(&ctl.q_ready[h], 128 % G == 0 ? 1 : 4);
             mbar_init(&ctl.s_ready[h], 1);
@@ -189,6 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ctl.o_done[h], 1);
             ctl.qissued[h] = 0;
         }
+        mbar_init(&ctl.vland, 1);
         mbar_init(&ctl.mma_done, 1);
         flags[0] = 0;
         fence_mbar_init();
@@ -258,8 +277,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         int next = page_of(0, 0), n = 0;  // n: stages so far
         bool ok = true;
+        // The V warp zeroes the rows of a stage that no query sees once they have landed,
+        // before it waits for the next slot (whole 128-byte rows, so the swizzle does not
+        // matter).
+        int z_piece = -1, z_stage = 0, z_n = 0, z_count = 0;
+        auto zero_pending = [&]() {
+            if (z_piece < 0) return true;
+            const Piece& c = list[z_piece];
+            const int slot = z_n % kStages, base = z_stage * kTokens;
+            z_piece = -1;
+            if (!__all_sync(0xffffffffu, mbar_wait(&ctl.vland, z_count & 1, flags, p.wait_ns)))
+                return false;
+            uint8_t* v0 = sm + kVOff + slot * kSlotBytes;
+            auto zero_rows = [&](int r0, int r1) {
+                for (int i = lane; i < (r1 - r0) * 16; i += 32) {
+                    const int row = r0 + (i >> 4), cc = i & 15;
+                    *reinterpret_cast<uint4*>(v0 + (cc >> 3) * kHalfBytes + row * 128 +
+                                              (cc & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            zero_rows(max(c.end - base, 0), kTokens);
+            zero_rows(max(c.hide0 - base, 0), min(c.hide1 - base, kTokens));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&full[slot]);
+                issued[slot] += 1;
+                ctl.zeroed += 1;
+            }
+            ++z_count;
+            return true;
+        };
         for (int pi = 0; pi < n_pieces && ok; ++pi) {
             const Piece& c = list[pi];
+            const HiddenStages hid(c);
             const int ca = p.layout == 0 ? c.hkv : 0;  // (d, A, B, page): NHD (d, head, token,
             const int cb = p.layout == 0 ? 0 : c.hkv;  // page), HND (d, token, head, page)
             for (int s = 0; s < c.n_st; ++s, ++n) {
@@ -271,6 +322,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     record_status(p.status, p.epoch, kDeviceBadPage);
                 const int page = bad ? 0 : next;
                 next = page_of(pi, s + 1);
+                if (!is_k && !zero_pending()) {
+                    ok = false;
+                    break;
+                }
                 int okw = 1;
                 if (lane == 0 && n >= kStages)
                     okw = mbar_wait(&empty[slot], ((n / kStages) + 1) & 1, flags, p.wait_ns) ? 1 : 0;
@@ -278,15 +333,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&full[slot], npg * ps * kHeadDim * 2);
+                const bool zero = !is_k && hid.among(s);
+                uint64_t* bar = zero ? &ctl.vland : &full[slot];
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, npg * ps * kHeadDim * 2);
+                    if (zero)
+                        ctl.landing += 1;
+                    else
+                        issued[slot] += 1;
+                }
                 __syncwarp();
                 if (lane < 2 * npg)
                     tma_load_4d((is_k ? ring_k(n) : ring_v(n)) + j * ps * 128 +
                                     ((lane & 1) ? kHalfBytes : 0),
-                                map, &full[slot], (lane & 1) * 64, ca, cb, page);
-                if (lane == 0) issued[slot] += 1;
+                                map, bar, (lane & 1) * 64, ca, cb, page);
+                if (zero) {
+                    z_piece = pi;
+                    z_stage = s;
+                    z_n = n;
+                }
             }
         }
+        if (ok && !is_k) ok = zero_pending();
         if (!ok && lane == 0) {
             flags[0] = 1;
             record_status(p.status, p.epoch, kDeviceWaitTimeout);
@@ -642,32 +710,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 tmem_wait_st();
-                // rows of V that no query sees: behind the request's last token, between the
-                // sinks and the first query's window
-                const int end = c.end - base;
-                const int z0 = max(c.hide0 - base, 0), z1 = min(c.hide1 - base, kTokens);
-                if (end < kTokens || z1 > z0) {
-                    // Zeroed once the stage's V landed (whole 128-byte rows, so the swizzle
-                    // does not matter), by every half that reads it, before its own PV (the
-                    // other may read it meanwhile: it has zeroed the same rows). The slot's
-                    // previous stage has been read, so this phase of vfull is the stage's.
-                    const int k = n0 + g;
-                    if (!wait_all(&ctl.vfull[k % kStages], k / kStages)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* v0 = sm + kVOff + (k % kStages) * kSlotBytes;
-                    auto zero_rows = [&](int r0, int r1) {
-                        for (int i = r; i < (r1 - r0) * 16; i += 128) {
-                            const int row = r0 + (i >> 4), cc = i & 15;
-                            *reinterpret_cast<uint4*>(v0 + (cc >> 3) * kHalfBytes + row * 128 +
-                                                      (cc & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                    };
-                    zero_rows(max(end, 0), kTokens);
-                    zero_rows(z0, z1);
-                    fence_proxy_async_smem();  // (the PV waits for all four warps' arrivals)
-                }
                 if (last && usable(pi + 1) < n_pieces) query_ready();
                 tc_fence_before();
                 __syncwarp();
@@ -777,6 +819,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ctl.vissued[s] > 0)
                 mbar_wait(&ctl.vfull[s], (ctl.vissued[s] - 1) & 1, nullptr, kWaitTimeoutNs);
         }
+        if (ctl.landing > ctl.zeroed)
+            mbar_wait(&ctl.vland, (ctl.landing - 1) & 1, nullptr, kWaitTimeoutNs);
         for (int h = 0; h < 2; ++h)
             if (ctl.qissued[h] > 0)
                 mbar_wait(&ctl.q_ready[h], (ctl.qissued[h] - 1) & 1, nullptr, kWaitTimeoutNs);
