@@ -515,14 +515,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
 
         int n = 0;        // scores of this half so far
-        int n0 = 0;       // stages of the CTA before the piece
         int n_o = 0;      // pieces of this half so far
         bool ok = true;
         if (usable(0) < n_pieces) {
             copy_query(list[usable(0)]);
             query_ready();
         }
-        for (int pi = 0; pi < n_pieces && ok; n0 += list[pi].n_st, ++pi) {
+        for (int pi = 0; pi < n_pieces && ok; ++pi) {
             const Piece c = list[pi];
             const int nst = c.nst[h];
             // (padding rows see what the tile's last query sees)

@@ -132,36 +132,37 @@ __global__ void __launch_bounds__(kTabThreads, 1)
                 const int at = q.free0 + j - q.held;
                 return at < n_free ? p.free_pages[at] : -1;
             };
+            // pages [dead0, dead1) are out of every new token's sight: behind the sinks, before
             // the first token that a new token's window holds
             const int seen = q.len - max(q.fresh, 1) + 1 - p.window;
-            // whether page j is out of every new token's sight
-            auto unseen = [&](int j) {
-                return p.window > 0 && (j << p.page_shift) >= p.sinks &&
-                       ((j + 1) << p.page_shift) <= seen;
+            const int dead0 = (p.sinks + ps - 1) >> p.page_shift;
+            const int dead1 = p.window > 0 ? max(dead0, max(seen, 0) >> p.page_shift) : dead0;
+            auto dead = [&](int j) {
+                return static_cast<unsigned>(j - dead0) < static_cast<unsigned>(dead1 - dead0);
             };
-            // (kAhead loads in flight: a request's pages are one chain otherwise)
-            constexpr int kAhead = 8;
+            const int fits = min(q.need, max(p.num_indices - q.first, 0));  // entries written
+            // (kAhead loads in flight: a request's pages are one chain otherwise; more of them
+            // are more code, which the small calls fetch for nothing)
+            constexpr int kAhead = 4;
+            int32_t* to = p.indices + q.first;
             for (int j0 = seg; j0 < q.need; j0 += kAhead * stride) {
                 int pages[kAhead];
 #pragma unroll
                 for (int a = 0; a < kAhead; ++a) {
                     const int j = j0 + a * stride;
-                    pages[a] = j < q.need && (j >= q.held || !unseen(j)) ? page_of(j) : -1;
+                    pages[a] = j < q.need ? page_of(j) : -1;
                 }
 #pragma unroll
                 for (int a = 0; a < kAhead; ++a) {
                     const int j = j0 + a * stride;
-                    int page = pages[a];
-                    if (j >= q.need) break;
-                    if (j >= q.held && page >= 0) {
-                        row[j] = page;
-                        if (page >= p.num_pages)
+                    if (j >= q.held && pages[a] >= 0) {
+                        row[j] = pages[a];
+                        if (pages[a] >= p.num_pages)
                             fail(kDeviceBadPage);
                         else if (p.refcount != nullptr)
-                            p.refcount[page] = 1;
+                            p.refcount[pages[a]] = 1;
                     }
-                    if (unseen(j)) page = -1;
-                    if (q.first + j < p.num_indices) p.indices[q.first + j] = page;
+                    if (j < fits) to[j] = dead(j) ? -1 : pages[a];
                 }
             }
             if (p.token_request != nullptr)
@@ -208,10 +209,13 @@ cudaError_t launch_build_tables(const TablesParams& p, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_relaxed);
     }
-    // a CTA for every 4096 entries
+    // a CTA for every 4096 entries, and no more than two requests a warp: 1024 requests of
+    // one page on one CTA take 33 us, on 16 5
     const int64_t entries = static_cast<int64_t>(p.num_indices) + p.num_tokens;
     int ctas = 1;
-    while (ctas < kMostTabCtas && ctas * int64_t{4096} < entries) ctas *= 2;
+    while (ctas < kMostTabCtas &&
+           (ctas * int64_t{4096} < entries || ctas * 2 * kTabWarps < p.batch))
+        ctas *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kTabThreads);
