@@ -103,6 +103,8 @@ __global__ void __launch_bounds__(kPThreads)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ps = p.page_size;
     const int G = p.group;
+    // launched as a programmatic dependent: nothing in global memory before this
+    if constexpr (kWindow) grid_dependency_wait();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPKStages; ++s) {
@@ -640,7 +642,7 @@ cudaError_t launch_prefill_narrow(const CUtensorMap& tk, const CUtensorMap& tv,
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = early ? 1 : 0;
+    cfg.numAttrs = early || p.window > 0 ? 1 : 0;  // (with a window it waits at its start)
     return cudaLaunchKernelEx(&cfg,
                               p.window > 0 ? paged_prefill_narrow_kernel<true>
                                            : paged_prefill_narrow_kernel<false>,

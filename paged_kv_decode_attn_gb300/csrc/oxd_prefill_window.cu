@@ -190,6 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto ring_v = [&](int n) { return s_base + kVOff + (n % kStages) * kSlotBytes; };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ps = p.page_size, G = p.group;
+    // launched as a programmatic dependent: nothing in global memory before this
+    grid_dependency_wait();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -859,6 +861,11 @@ cudaError_t launch_prefill_window(const CUtensorMap& tk, const CUtensorMap& tv,
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, prefill_window_kernel, tk, tv, tq, p);
 }
 
