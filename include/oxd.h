@@ -748,8 +748,8 @@ oxd_status oxd_copy_pages(const oxd_copy_pages_desc* desc, const oxd_kv_pools* s
  * Host-side errors (nothing enqueued): OXD_ERR_INVALID_ARGUMENT (NULL, sizes,
  * window < 1, sinks < 0, an array in another device's memory than the calling
  * thread's current one), OXD_ERR_UNSUPPORTED (head_dim, page size, G > 32,
- * window + sinks above 2^30, pools of 2^32 (token, head) rows or more, more than
- * 2^25 (request, KV head) pairs), OXD_ERR_ALIGNMENT, OXD_ERR_ALIAS (out, lse and
+ * window + sinks above 2^30, pools of more than 2^32 (token, head) rows, 2^25
+ * (request, KV head) pairs or more), OXD_ERR_ALIGNMENT, OXD_ERR_ALIAS (out, lse and
  * workspace must not overlap each other or any input),
  * OXD_ERR_WORKSPACE_TOO_SMALL, OXD_ERR_CUDA. Device-side: a visible page's index
  * outside the pool is recorded as OXD_DEVICE_BAD_PAGE and read as page 0; a

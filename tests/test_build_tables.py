@@ -271,3 +271,44 @@ def test_runs_are_equal_on_two_streams():
             got, code, _, _ = run(s, 16, 500, 4)
         assert code == 0
         compare(got, first)
+
+
+def test_slots_past_2_32():
+    """Page numbers near 2^31: slots are 64-bit."""
+    s = state([40, 9], [40, 1], 16, seed=14, held=[0, 1])
+    s["free"] = (np.arange(len(s["free"])) + 2 ** 31 - 100).astype(np.int32)
+    s["rows"][1, 0] = 2 ** 30 + 5
+    got, code, n_idx, n_tok = run({**s, "refcount": np.zeros(1)}, 16, refcount=False)
+    # (the pool of this call is declared as large as its reference counts: one page)
+    assert code == oxd.OXD_DEVICE_BAD_PAGE
+    ref = reference(s, 16, 0, 0, n_idx, n_tok)
+    compare(got, ref, skip=("refcount",))
+    assert got["slots"].max() > 2 ** 34
+
+
+def test_twenty_six_calls_in_a_row_in_place():
+    """Back to back, each a programmatic dependent of the one before."""
+    ps, B = 8, 70
+    s = state([3] * B, [1] * B, ps, seed=15, width=20, held=[1] * B, extra_free=B * 4)
+    lengths = dev(s["lengths"])
+    rows, held, taken = dev(s["rows"]), dev(s["held"]), dev([0])
+    free, ref_count = dev(s["free"]), dev(s["refcount"])
+    new = dev(s["new"])
+    n_idx = B * 20
+    d = oxd.make_build_tables_desc(B, ps, 20, len(s["refcount"]), n_idx, B, len(s["free"]))
+    outs = [torch.full((n,), -9, dtype=torch.int32, device="cuda") for n in (B + 1, n_idx, B, B + 1, B, B)]
+    slots = torch.full((B,), -9, dtype=torch.int64, device="cuda")
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    for _ in range(26):
+        oxd.oxd_build_tables(d, lengths, new, rows, held, held, free, taken, taken, ref_count, *outs[:3],
+                             *outs[3:], slots, ws)
+        lengths += 1
+    assert oxd.oxd_read_device_status(ws) == 0
+    at = {k: (v.copy() if isinstance(v, np.ndarray) else v) for k, v in s.items()}
+    for _ in range(26):
+        r = reference(at, ps, 0, 0, n_idx, B)
+        at.update(lengths=at["lengths"] + 1, held=r["held_out"], rows=r["rows"].astype(np.int32),
+                  taken=int(r["taken_out"][0]), refcount=r["refcount"])
+    assert np.array_equal(rows.cpu().numpy(), r["rows"]) and taken.item() == r["taken_out"][0]
+    assert np.array_equal(slots.cpu().numpy(), r["slots"])
+    assert np.array_equal(outs[0].cpu().numpy(), r["indptr"])

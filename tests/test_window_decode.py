@@ -384,3 +384,51 @@ def test_random_decodes(seed, four):
                                       sigma=float(rng.choice([0.5, 1, 2])))
     c.check(float(rng.choice([SCALE, -SCALE, 0.5])), f"{lengths} {G} {Hkv} {window} {sinks} {ps} {layout}",
             max_splits=int(rng.choice([0, 0, 1, 5])))
+
+
+# ------------------------------------------------------------------ far pages
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("layout", ["NHD", "HND"])
+def test_pools_past_2_32_bytes(layout, four):
+    """Pages at both ends of pools of more than 4 GiB each."""
+    ps, Hkv, G, n = 64, 2, 4, 300
+    width = 64 if four else 128
+    pages = (1 << 32) // (ps * Hkv * (64 if four else 256)) + 1000
+    rng = np.random.default_rng(21)
+    p = Wr.Paged([n], [1], Hkv, ps, layout, 200, 10, 21, spare=0)
+    at = np.asarray([3, pages - 1, 0, pages - 700, pages // 2])[:len(p.indices)]
+    shape = (pages, ps, Hkv, width) if layout == "NHD" else (pages, Hkv, ps, width)
+    dtype = torch.uint8 if four else torch.bfloat16
+    pools = [torch.empty(shape, dtype=dtype, device="cuda") for _ in "kv"]
+    scales = [torch.empty((pages, Hkv, ps, 4), dtype=torch.float16, device="cuda") for _ in "kv"] if four else []
+    k, v = p.k, p.v
+    for i, pool in enumerate(p.pools):
+        for j, page in enumerate(p.indices):
+            if page < 0:
+                continue
+            x = np.nan_to_num(pool[page])
+            if four:
+                c, s = R.hold(x)
+                pools[i][at[j]] = torch.as_tensor(c, device="cuda")
+                scales[i][at[j]] = torch.as_tensor(
+                    np.ascontiguousarray(s.swapaxes(0, 1) if layout == "NHD" else s), device="cuda")
+            else:
+                pools[i][at[j]] = bf16(x)
+    if four:
+        k, v = ([R.values(*R.hold(x)) for x in y] for y in (k, v))
+    q = p.queries(G * Hkv)
+    out, lse = torch.empty((1, G * Hkv, 128), dtype=torch.bfloat16, device="cuda"), torch.empty((1, G * Hkv), device="cuda")
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    d = oxd.make_window_decode_desc(1, G * Hkv, Hkv, ps, layout, pages, len(at), 200, 10)
+    tables = (dev(p.indptr), dev(np.where(p.indices < 0, -1, at)), dev(p.last))
+    if four:
+        oxd.oxd_quant_window_decode(d, bf16(q), oxd.KvPools(*pools, *scales), *tables, SCALE, out, lse, ws)
+    else:
+        oxd.oxd_window_decode(d, bf16(q), *pools, *tables, SCALE, out, lse, ws)
+    assert oxd.oxd_read_device_status(ws) == 0
+    ref = Wr.attention(q, k, v, [n], [1], 200, 10, SCALE)
+    if four:
+        assert_decode(out, lse, ref)
+    else:
+        Wr.assert_close(f64(out), f64(lse), ref)
