@@ -1,4 +1,6 @@
 """Block tables and token maps built on the GPU against plain Python (GPU)."""
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -312,3 +314,17 @@ def test_twenty_six_calls_in_a_row_in_place():
     assert np.array_equal(rows.cpu().numpy(), r["rows"]) and taken.item() == r["taken_out"][0]
     assert np.array_equal(slots.cpu().numpy(), r["slots"])
     assert np.array_equal(outs[0].cpu().numpy(), r["indptr"])
+
+
+@pytest.mark.parametrize("seed", range(30 * int(os.environ.get("OXD_FUZZ_SCALE", "1"))))
+def test_random_tables(seed):
+    rng = np.random.default_rng(3000 + seed)
+    B = int(np.exp(rng.uniform(0, np.log(1500))))
+    hi = int(np.exp(rng.uniform(0, np.log(3000))))
+    lengths = rng.integers(0, hi + 1, B)
+    new = np.minimum(lengths, rng.integers(0, int(np.exp(rng.uniform(0, np.log(hi + 1)))) + 1, B))
+    ps = int(rng.choice([8, 16, 32, 64]))
+    held = np.maximum(-(-(lengths - new) // ps) + rng.integers(-1, 3, B), 0)
+    window = int(rng.choice([0, 1, 30, 500]))
+    check(state(lengths, new, ps, seed, held=held, taken=int(rng.choice([0, 7]))), ps, window,
+          int(rng.choice([0, 1, 20, 100])), in_place=bool(rng.integers(2)))

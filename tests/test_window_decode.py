@@ -1,4 +1,6 @@
 """Decode with a sliding window and sinks against f64, bf16 and 4-bit pages (GPU)."""
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -372,7 +374,7 @@ def test_4bit_bad_pages_and_tables():
 # ------------------------------------------------------------------ at random
 
 @pytest.mark.parametrize("four", [False, True])
-@pytest.mark.parametrize("seed", range(30))
+@pytest.mark.parametrize("seed", range(30 * int(os.environ.get("OXD_FUZZ_SCALE", "1"))))
 def test_random_decodes(seed, four):
     rng = np.random.default_rng(2000 + seed)
     B = int(rng.integers(1, 20))

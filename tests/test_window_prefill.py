@@ -1,4 +1,6 @@
 """Causal prefill with a sliding window and sinks: planning on the CPU, runs against f64 (GPU)."""
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -289,7 +291,7 @@ def test_more_tiles_than_resident_ctas(rows, layout, G, Hkv, window, sinks):
 
 
 @gpu
-@pytest.mark.parametrize("seed", range(40))
+@pytest.mark.parametrize("seed", range(40 * int(os.environ.get("OXD_FUZZ_SCALE", "1"))))
 def test_random_prefills(seed):
     rng = np.random.default_rng(1000 + seed)
     B = int(rng.integers(1, 6))
