@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                      static_cast<int64_t>(u.n_pages) * ps &&
                  u.b >= 0 && u.b < p.batch && u.hkv >= 0 && u.hkv < p.num_kv_heads &&
                  u.n_tok >= 1 && u.n_tok <= T && u.n_tok * G <= kPrefillRows && u.q_begin >= 0 &&
-                 u.q_begin + u.n_tok <= p.n_q_tokens && u.p0 >= 0 && u.n_pieces >= 1 &&
+                 u.q_begin <= p.n_q_tokens - u.n_tok && u.p0 >= 0 && u.n_pieces >= 1 &&
                  u.piece >= 0 && u.piece < u.n_pieces;
             if (ok && u.n_pieces > 1)
                 ok = u.state >= 0 &&

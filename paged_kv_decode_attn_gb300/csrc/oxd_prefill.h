@@ -37,7 +37,7 @@ struct PrefillUnit {
     int32_t qo_b;       // qo_indptr[b], L_b and indptr[b] as planned: the
     int32_t kv_len;     // kernel checks the device tables against them
     int32_t page_base;
-    int32_t pad;
+    int32_t q_len;      // the request's query tokens
 };
 static_assert(sizeof(PrefillUnit) == 64, "units are 64 bytes");
 

@@ -362,6 +362,7 @@ oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sink
             u.qo_b = qo_indptr[t.b];
             u.kv_len = static_cast<int32_t>(L);
             u.page_base = indptr[t.b];
+            u.q_len = qo_indptr[t.b + 1] - qo_indptr[t.b];
             units.push_back(u);
         }
         return true;

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kPThreads)
                      static_cast<int64_t>(u.n_pages) * ps &&
                  u.b >= 0 && u.b < p.batch && u.hkv >= 0 && u.hkv < p.num_kv_heads &&
                  u.n_tok >= 1 && u.n_tok <= T && u.q_begin >= 0 &&
-                 u.q_begin + u.n_tok <= p.n_q_tokens && u.p0 >= 0 && u.n_pieces >= 1 &&
+                 u.q_begin <= p.n_q_tokens - u.n_tok && u.p0 >= 0 && u.n_pieces >= 1 &&
                  u.piece >= 0 && u.piece < u.n_pieces;
             if (ok && u.n_pieces > 1)
                 ok = u.state >= 0 &&
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kPThreads)
                 }
                 uint8_t* v0 = sm + kPVOff + (g % kPVStages) * kPSlotBytes;
                 auto zero_rows = [&](int r0, int r1) {
-                    const int n16 = (r1 - r0) * 16;
+                    const int n16 = (max(r1, r0) - r0) * 16;
                     for (int i = r; i < n16; i += kPSoftmaxThreads) {
                         const int row = r0 + (i >> 4), c = i & 15;
                         *reinterpret_cast<uint4*>(v0 + (c >> 3) * kPHalf + row * 128 +
@@ -485,7 +485,8 @@ __global__ void __launch_bounds__(kPThreads)
                 };
                 zero_rows(nvalid, kNarrowStageTokens);
                 if constexpr (kWindow)
-                    zero_rows(sight.hidden0(base), sight.hidden1(base, kNarrowStageTokens));
+                    zero_rows(sight.hidden0(base, kNarrowStageTokens),
+                              sight.hidden1(base, kNarrowStageTokens));
                 fence_proxy_async_smem();
             }
             tc_fence_before();

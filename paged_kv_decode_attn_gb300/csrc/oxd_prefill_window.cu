@@ -88,7 +88,7 @@ struct Ctl {
     uint64_t mma_done;
     int kissued[kStages], vissued[kStages], qissued[2], landing, zeroed;
     uint32_t tmem;
-    int flags[3];  // [0] abort, [1] pieces of this CTA
+    int flags[3];  // [0] abort, [1] pieces of this CTA, [2] its first unit
 };
 constexpr int kListOff = kCtlOff + (static_cast<int>(sizeof(Ctl)) + 15) / 16 * 16;
 // a softmax warp's outputs on their way out: 32 rows of 128 bytes
@@ -126,11 +126,13 @@ __device__ __forceinline__ Piece make_piece(const PrefillParams& p, const Prefil
     const int ps = p.page_size, G = p.group;
     Piece c{};
     TileWindow w;
-    bool ok = u.n_pages >= 1 && u.kv_valid >= 1 && u.kv_begin >= 0 && u.kv_begin % kTokens == 0 &&
+    bool ok = u.n_pages >= 1 && u.kv_valid >= 1 && u.kv_valid < (1 << 30) && u.kv_begin >= 0 &&
+              u.kv_begin % kTokens == 0 &&
               static_cast<int64_t>(u.kv_valid) <= static_cast<int64_t>(u.n_pages) * ps &&
               u.b >= 0 && u.b < p.batch && u.hkv >= 0 && u.hkv < p.num_kv_heads && u.n_tok >= 1 &&
               u.n_tok <= p.tile_tokens && u.n_tok * G <= kPrefillRows && u.q_begin >= 0 &&
-              u.q_begin + u.n_tok <= p.n_q_tokens && u.p0 >= 0 && u.p0 < (1 << 30) &&
+              u.q_begin <= p.n_q_tokens - u.n_tok && u.p0 >= 0 && u.p0 < u.kv_len &&
+              u.kv_len < (1 << 30) && u.q_len >= 1 && u.q_len <= u.kv_len &&
               u.n_pieces >= 1 && u.piece >= 0 && u.piece < u.n_pieces;
     if (ok) {
         w.init(p, u);
@@ -145,12 +147,6 @@ __device__ __forceinline__ Piece make_piece(const PrefillParams& p, const Prefil
         record_status(p.status, p.epoch, kDevicePlanMismatch);
         return c;
     }
-    // the device tables must be the ones the plan was made from
-    const int b = u.b;
-    const int64_t L =
-        static_cast<int64_t>(p.indptr[b + 1] - p.indptr[b] - 1) * ps + p.last_page_len[b];
-    if (p.qo_indptr[b] != u.qo_b || p.indptr[b] != u.page_base || L != u.kv_len)
-        record_status(p.status, p.epoch, kDevicePlanMismatch);
     c.n_st = (u.kv_valid + kTokens - 1) / kTokens;
     c.pages = u.n_pages;
     c.first = u.page_base + u.kv_begin / ps;
@@ -162,7 +158,7 @@ __device__ __forceinline__ Piece make_piece(const PrefillParams& p, const Prefil
     // query sees. (With skipped pages in between: the rest of the sinks' pages, and of the
     // first page behind them if that is the first query's.)
     const int begin = u.kv_begin;
-    const int lo = u.kv_len - (p.qo_indptr[b + 1] - p.qo_indptr[b]) - p.window + 1;
+    const int lo = u.kv_len - u.q_len - p.window + 1;
     c.hide0 = w.sinks;
     c.hide1 = max(min((w.front + begin / ps) * ps, lo), lo - w.skip * ps) - begin;
     c.end = u.kv_len - w.skip * ps - begin;
@@ -253,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) {
             if (!ok) record_status(p.status, p.epoch, kDevicePlanMismatch);
             flags[1] = n;
+            flags[2] = a;
         }
     }
     tc_fence_before();
@@ -297,15 +294,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!__all_sync(0xffffffffu, mbar_wait(&ctl.vland, z_count & 1, flags, p.wait_ns)))
                 return false;
             uint8_t* v0 = sm + kVOff + slot * kSlotBytes;
-            auto zero_rows = [&](int r0, int r1) {
-                for (int i = lane; i < (r1 - r0) * 16; i += 32) {
+            auto zero_rows = [&](int r0, int r1) {  // (none where r1 is not above r0 >= 0)
+                for (int i = lane; i < (max(r1, r0) - r0) * 16; i += 32) {
                     const int row = r0 + (i >> 4), cc = i & 15;
                     *reinterpret_cast<uint4*>(v0 + (cc >> 3) * kHalfBytes + row * 128 +
                                               (cc & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
             };
-            zero_rows(max(c.end - base, 0), kTokens);
-            zero_rows(max(c.hide0 - base, 0), min(c.hide1 - base, kTokens));
+            zero_rows(min(max(c.end - base, 0), kTokens), kTokens);
+            zero_rows(min(max(c.hide0 - base, 0), kTokens), min(c.hide1 - base, kTokens));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -363,6 +360,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (ok && !is_k) ok = zero_pending();
+        if (is_k) {
+            // the device tables must be the ones the plan was made from (read here, off the
+            // way to the first products)
+            for (int i = lane; i < n_pieces; i += 32) {
+                const PrefillUnit u = p.units[flags[2] + i];
+                if (list[i].n_st == 0 || u.b < 0 || u.b >= p.batch) continue;
+                const int64_t L =
+                    static_cast<int64_t>(p.indptr[u.b + 1] - p.indptr[u.b] - 1) * ps +
+                    p.last_page_len[u.b];
+                if (p.qo_indptr[u.b] != u.qo_b || p.indptr[u.b] != u.page_base || L != u.kv_len)
+                    record_status(p.status, p.epoch, kDevicePlanMismatch);
+            }
+            __syncwarp();
+        }
         if (!ok && lane == 0) {
             flags[0] = 1;
             record_status(p.status, p.epoch, kDeviceWaitTimeout);

@@ -32,10 +32,12 @@ struct TileWindow {
     }
     // Rows [hidden0, hidden1) of a stage of `n` tokens that starts at `base` are tokens
     // that no row sees.
-    __device__ __forceinline__ int hidden0(int base) const { return max(sinks - base, 0); }
+    __device__ __forceinline__ int hidden0(int base, int n) const {
+        return min(max(sinks - base, 0), n);
+    }
     __device__ __forceinline__ int hidden1(int base, int n) const { return min(lo - base, n); }
     __device__ __forceinline__ bool hides(int base, int n) const {
-        return hidden1(base, n) > hidden0(base);
+        return hidden1(base, n) > hidden0(base, n);
     }
 };
 

@@ -332,6 +332,17 @@ def test_a_damaged_bound_list_is_reported_and_not_followed(rows):
         oxd.oxd_read_device_status(ws)
         assert (out[:128] == 77).all() and (out[-128:] == 77).all() and (ws[plan.workspace_bytes:] == 55).all()
         assert (lse[:4] == 77).all() and (lse[-4:] == 77).all()
+    # every field of every unit at the ends of its type
+    for field in range(16):
+        for value in (-2 ** 31, -1, 0, 2 ** 30, 2 ** 31 - 1):
+            oxd.oxd_prefill_plan_bind_workspace(plan, ws, plan.workspace_bytes)
+            words.view(-1, 16)[:, field] = value
+            oxd.oxd_paged_prefill_run(plan, c.d_q, c.d_k, c.d_v, *c.tables, SCALE, out[128:-128],
+                                      lse[4:-4], ws, plan.workspace_bytes)
+            oxd.oxd_read_device_status(ws)
+            assert (out[:128] == 77).all() and (out[-128:] == 77).all()
+            assert (lse[:4] == 77).all() and (lse[-4:] == 77).all()
+            assert (ws[plan.workspace_bytes:] == 55).all()
     words[:] = -1
     oxd.oxd_paged_prefill_run(plan, c.d_q, c.d_k, c.d_v, *c.tables, SCALE, out[128:-128], lse[4:-4], ws,
                               plan.workspace_bytes)
