@@ -465,7 +465,8 @@ typedef struct {
 typedef struct {
     int32_t tile_tokens;        /* query tokens per tile: tile_rows / G */
     int32_t num_tiles;
-    int32_t num_units;          /* CTAs per run: pieces of all tiles */
+    int32_t num_units;          /* pieces of all tiles: a CTA each per run (those of 256-row
+                                   tiles under a window share one CTA a SM) */
     int32_t num_split_tiles;
     int32_t max_pieces;
     int32_t num_merge_rows;     /* output rows merged from pieces (0: one launch) */

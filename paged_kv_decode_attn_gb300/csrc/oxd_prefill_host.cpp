@@ -485,6 +485,17 @@ oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sink
     return OXD_OK;
 }
 
+// The same for a C entry: lists too long for the host's memory are a status.
+oxd_status plan_or_no_memory(const oxd_paged_prefill_desc* desc, int window, int sinks,
+                             const int32_t* qo_indptr, const int32_t* indptr, const int32_t* last,
+                             int device, oxd_prefill_plan* plan_out, size_t* ws_out) {
+    try {
+        return plan_prefill(desc, window, sinks, qo_indptr, indptr, last, device, plan_out, ws_out);
+    } catch (const std::bad_alloc&) {
+        return OXD_ERR_NO_MEMORY;
+    }
+}
+
 }  // namespace
 
 extern "C" {
@@ -492,7 +503,7 @@ extern "C" {
 oxd_status oxd_paged_prefill_plan(const oxd_paged_prefill_desc* desc, const int32_t* qo_indptr,
                                   const int32_t* indptr, const int32_t* last, int device,
                                   oxd_prefill_plan* plan_out, size_t* ws_out) {
-    return plan_prefill(desc, 0, 0, qo_indptr, indptr, last, device, plan_out, ws_out);
+    return plan_or_no_memory(desc, 0, 0, qo_indptr, indptr, last, device, plan_out, ws_out);
 }
 
 oxd_status oxd_window_prefill_plan(const oxd_paged_prefill_desc* desc, int32_t window,
@@ -501,7 +512,8 @@ oxd_status oxd_window_prefill_plan(const oxd_paged_prefill_desc* desc, int32_t w
                                    size_t* ws_out) {
     if (window < 1 || sinks < 0) return OXD_ERR_INVALID_ARGUMENT;
     if (static_cast<int64_t>(window) + sinks > kMaxWindowTokens) return OXD_ERR_UNSUPPORTED;
-    return plan_prefill(desc, window, sinks, qo_indptr, indptr, last, device, plan_out, ws_out);
+    return plan_or_no_memory(desc, window, sinks, qo_indptr, indptr, last, device, plan_out,
+                             ws_out);
 }
 
 oxd_status oxd_prefill_plan_get_info(oxd_prefill_plan plan, oxd_prefill_plan_info* info) {
