@@ -16,7 +16,8 @@
 //     rows are copied while the last stage's softmax runs, its first score
 //     MMAs follow the last PV, and a half's epilogue overlaps the other half's products;
 //   * every stage takes one pass over its scores against the row's reference (the
-//     first: the maximum of 16 columns; a lagging reference is as good, see below),
+//     first: the maximum of the last 16 columns seen, each row its own; a lagging
+//     reference is as good, see below),
 //     16 columns at a time, at the window's edges masked by a bit a column; a warp's
 //     rows are few tokens, so most blocks of 16 columns there are seen by none of them
 //     and cost nothing. A pass whose sum shows a term above 2^64 is done again in two
@@ -116,9 +117,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// The lowest n bits (all of 32, none for a negative n).
-__device__ __forceinline__ uint32_t below(int n) {
-    return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u;
+// The lowest n bits (all of 64, none for a negative n).
+__device__ __forceinline__ unsigned long long below(int n) {
+    return n >= 64 ? ~0ull : (1ull << max(n, 0)) - 1ull;
 }
 
 // Unit `u` as a piece; n_st 0 (recorded) if it is not one that this plan can have.
@@ -578,38 +579,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float alpha = 1.f;
                 const bool whole = all_see(base, base + kTokens);
                 // the columns that the row sees, a bit each
-                uint32_t see[4];
+                unsigned long long see[2] = {~0ull, ~0ull};
                 if (!whole) {
                     const int from = w_lo - base, to = pos + 1 - base;
                     const int first = min(c.sinks - base, to);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        see[k] = (below(to - 32 * k) & ~below(from - 32 * k)) | below(first - 32 * k);
+                    for (int k = 0; k < 2; ++k)
+                        see[k] = (below(to - 64 * k) & ~below(from - 64 * k)) | below(first - 64 * k);
                 }
                 if (__any_sync(0xffffffffu, m_ref == -INFINITY)) {
                     // rows without a reference take the maximum of what they see of the last
-                    // 16 columns that some row sees (at the window's start a row that sees
-                    // anything of the stage sees the last ones)
-                    int at = 7;
-                    uint32_t bits = 0xffffu;
-                    if (!whole) {
-                        at = -1;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (__any_sync(0xffffffffu, (see[i >> 1] >> 16 * (i & 1) & 0xffffu) != 0)) {
-                                at = i;
-                                bits = see[i >> 1] >> 16 * (i & 1);
-                            }
-                    }
-                    if (at >= 0) {
+                    // block of 16 columns of which they see some (one block, where a window
+                    // starts or a stage is seen whole; up to three at its end, where a warp's
+                    // rows end in different ones: with the last block alone the others' rows
+                    // took two passes, 8 prompts of 2048 with 16 query and 8 KV heads at
+                    // window 512 165 us, 125 so)
+#pragma unroll 1
+                    for (int i = 7; i >= 0; --i) {
+                        const uint32_t bits =
+                            static_cast<uint32_t>((i >= 4 ? see[1] : see[0]) >> (16 * (i & 3))) & 0xffffu;
+                        const bool want = m_ref == -INFINITY && bits != 0;
+                        if (!__any_sync(0xffffffffu, want)) continue;
                         uint32_t a[16];
-                        tmem_ld16_async(ts + lane_off + 16 * at, a);
+                        tmem_ld16_async(ts + lane_off + 16 * i, a);
                         tmem_ld_wait16(a);
                         float mx = -INFINITY;
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
                             if (bits >> j & 1) mx = fmaxf(mx, __uint_as_float(a[j]) * sc);
-                        if (m_ref == -INFINITY) m_ref = mx;
+                        if (want) m_ref = mx;
+                        if (!__any_sync(0xffffffffu, m_ref == -INFINITY)) break;
                     }
                 }
                 {
@@ -635,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     };
                     auto edge = [&](uint32_t (&x)[16], int i) {
-                        const uint32_t bits = see[i >> 1] >> 16 * (i & 1);
+                        const uint32_t bits = static_cast<uint32_t>(see[i >> 2] >> 16 * (i & 3));
                         if (!__any_sync(0xffffffffu, (bits & 0xffffu) != 0)) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j) pk[8 * i + j] = 0u;
