@@ -9,9 +9,10 @@
 // in L2. In NHD pools a CTA takes two KV heads where it can (64 bytes of codes a head:
 // half a 128-byte line).
 //
-// 256 requests U{128..16384} x 8 heads, groups of 8, window 4096: 202 us, 79 % of the copy
-// rate. Issue and latency bound it: 572 instructions a chunk, 56 % of the issue slots with
-// 3.1 warps a scheduler. 8 requests x 8 heads of 1024 tokens 9.1 us (latencies).
+// 256 requests U{128..16384} x 8 heads, groups of 8, window 4096: 197 us, 81 % of the copy
+// rate; between the ends of streams it runs at 94 % (of which 572 instructions a chunk take
+// 56 % of the issue slots), a CTA's start and end cost 8 us of one wave. 8 requests x 8
+// heads of 1024 tokens 7.6 us (latencies).
 #include <algorithm>
 
 #include "oxd_decode_quant_state.cuh"
@@ -121,6 +122,19 @@ __global__ void __launch_bounds__(kWinThreads, QW::kCtas)
     const int wl2 = p.heads == 2 ? 1 : 2;  // log2 of the warps a head has
     const int hd = warp >> wl2, w = warp & ((1 << wl2) - 1);
 
+    // query rows, 16 bytes a thread and head, on their way while the tables are read and
+    // the first chunks asked for (with the merge of two heads side by side: 256 requests
+    // 202 -> 197 us, one 7.9 -> 6.8)
+    auto row0 = [&](int head) {
+        return static_cast<size_t>(b) * p.num_qo_heads + (h0 + head) * p.group + part * kRows;
+    };
+    uint4 qv[2];
+#pragma unroll
+    for (int head = 0; head < 2; ++head)
+        if (head < p.heads && threadIdx.x < rows * 16)
+            qv[head] = __ldg(reinterpret_cast<const uint4*>(p.q + row0(head) * kHeadDim) +
+                             threadIdx.x);
+
     Stream in;
     in.head = h0 + hd;
     in.vis = visible_tokens(p, b);
@@ -133,18 +147,14 @@ __global__ void __launch_bounds__(kWinThreads, QW::kCtas)
     in.page = 0;
     in.look_up(p, lane);
 
-    // query rows, 16 bytes a thread, then their fragments
-    auto row0 = [&](int head) {
-        return static_cast<size_t>(b) * p.num_qo_heads + (h0 + head) * p.group + part * kRows;
-    };
-    for (int i = threadIdx.x; i < p.heads * rows * 16; i += kWinThreads) {
-        const int head = i >= rows * 16 ? 1 : 0, at = i - head * rows * 16;
-        *reinterpret_cast<uint4*>(base + QW::kRawOff + head * QW::kQHeadBytes + at * 16) =
-            __ldg(reinterpret_cast<const uint4*>(p.q + row0(head) * kHeadDim) + at);
-    }
     const uint32_t ring = smem_addr(base) + warp * QW::kRingBytes;
     for (int i = 0; i < QW::kSlots; ++i) in.refill(p, ring + i * QW::kSlotBytes, lane);
-    __syncthreads();
+#pragma unroll
+    for (int head = 0; head < 2; ++head)
+        if (head < p.heads && threadIdx.x < rows * 16)
+            *reinterpret_cast<uint4*>(base + QW::kRawOff + head * QW::kQHeadBytes +
+                                      threadIdx.x * 16) = qv[head];
+    // (convert_query has a thread read the 16 bytes of a head that it wrote)
     float* sc = reinterpret_cast<float*>(base + QW::kScOff);
     for (int head = 0; head < p.heads; ++head)
         convert_query<1>(base + QW::kRawOff + head * QW::kQHeadBytes, rows, p.scale_log2,
@@ -177,10 +187,10 @@ __global__ void __launch_bounds__(kWinThreads, QW::kCtas)
             red_l + warp * kRows, lane);
     __syncthreads();
     if (p.splits > 1) cluster_wait();
-    for (int head = 0; head < p.heads; ++head)
-        merge_states(p, base, QW::kRingBytes, red_m, red_l, kRows, kPOffset, head << wl2, 1 << wl2,
-                     row0(head), rows, base + QW::kXchgOff + head * exchange_bytes(rows, p.splits),
-                     warp, kWinWarps, lane);
+    // (a head's rows by the warps that streamed it)
+    merge_states(p, base, QW::kRingBytes, red_m, red_l, kRows, kPOffset, hd << wl2, 1 << wl2,
+                 row0(hd), rows, base + QW::kXchgOff + hd * exchange_bytes(rows, p.splits), w,
+                 1 << wl2, lane);
 }
 
 }  // namespace
