@@ -203,12 +203,16 @@ cudaError_t window_kernel_ready(void (*kernel)(WindowParams), int which, int mos
 
 // CTAs a stream. As many as still leave all of them resident at once (a cluster sits in
 // one GPC, so that fewer large ones fit), each with at least a chunk a warp (`least`
-// tokens); more than eight only for four chunks a warp: eight requests x 8 heads of 1024
-// tokens over 4 bits take 9.2 us with 8 and 12.0 with 12, 16 x 1 head of 8192 over bf16
-// 25 and 19. Long streams that fill the GPU are cut in two all the same, so that the
-// last to start end sooner (64 x 8 heads of 4096: 164 -> 158 us).
+// tokens); more than eight only for four chunks a warp: 16 requests x 1 head of 8192 over
+// bf16 take 25 us with 8 and 19 with 12.
+// Where that is one, streams of 4096 tokens and more are cut in two all the same, so that
+// the last to start end sooner and the SMs are filled more evenly (bf16: 64 x 8 heads of
+// 4096 164 -> 158 us). Over 4 bits, where a stream's end costs more of its time, that pays
+// up to two waves of the GPU, if the last of them fills at most 85 % of their room (320
+// streams of 4096 57 -> 46 us, 440 58 -> 55, 1024 of mixed lengths 202 -> 193; but 608
+// 60 -> 66, 1216 115 -> 126): `ends_cost`.
 inline int window_splits(const WindowParams& p, const WindowOccupancy& occ, int64_t streams,
-                         int least, int max_splits) {
+                         int least, bool ends_cost, int max_splits) {
     const int64_t most = std::min<int64_t>(
         static_cast<int64_t>(p.window) + p.sinks,
         static_cast<int64_t>(p.num_indices) << p.page_shift);
@@ -217,8 +221,9 @@ inline int window_splits(const WindowParams& p, const WindowOccupancy& occ, int6
     int c = 1;
     for (int i = 2; i <= cap; ++i)
         if (occ.clusters[i] >= streams && most >= int64_t{i} * least * (i > 8 ? 4 : 1)) c = i;
-    const bool full = streams * 4 >= int64_t{occ.clusters[1]} * 3;
-    return full && cap > 1 && most >= 4096 ? 2 : c;
+    if (c > 1 || cap == 1 || most < 4096) return c;
+    const int64_t room = std::max(occ.clusters[1], 1), waves = (streams + room - 1) / room;
+    return ends_cost && (waves > 2 || streams * 20 > room * waves * 17) ? 1 : 2;
 }
 
 inline cudaError_t window_launch(void (*kernel)(WindowParams), const WindowParams& p,

@@ -398,7 +398,7 @@ cudaError_t launch(WindowParams& p, int max_splits, cudaStream_t stream, bool pd
         [](int c) { return C::kXchgOff + exchange_bytes(C::kRows, c); }, &occ);
     if (e != cudaSuccess) return e;
     p.heads = 1;
-    p.splits = window_splits(p, *occ, streams, kWinWarps * kChunk, max_splits);
+    p.splits = window_splits(p, *occ, streams, kWinWarps * kChunk, false, max_splits);
     return window_launch(window_decode_kernel<C>, p, streams,
                          C::kXchgOff + exchange_bytes(std::min(C::kRows, p.group), p.splits),
                          stream, pdl);

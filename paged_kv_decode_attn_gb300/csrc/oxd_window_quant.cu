@@ -6,13 +6,13 @@
 // does with a chunk is the 4-bit decode's (oxd_decode_quant_state.cuh): tokens as the
 // M dimension of mma.sync, one N tile of 8 query heads. A larger group is cut into
 // parts of 8 heads, CTAs of their own that start together and find each other's rows
-// in L2. In NHD pools a CTA takes two KV heads where it can (64 bytes of codes a head:
-// half a 128-byte line).
+// in L2. In NHD pools a CTA takes two KV heads where there are many (64 bytes of codes a
+// head: half a 128-byte line).
 //
 // 256 requests U{128..16384} x 8 heads, groups of 8, window 4096: 197 us, 81 % of the copy
 // rate; between the ends of streams it runs at 94 % (of which 572 instructions a chunk take
 // 56 % of the issue slots), a CTA's start and end cost 8 us of one wave. 8 requests x 8
-// heads of 1024 tokens 7.6 us (latencies).
+// heads of 1024 tokens 7.4 us, one request 5.5 (latencies).
 #include <algorithm>
 
 #include "oxd_decode_quant_state.cuh"
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kWinThreads, QW::kCtas)
 
     // query rows, 16 bytes a thread and head, on their way while the tables are read and
     // the first chunks asked for (with the merge of two heads side by side: 256 requests
-    // 202 -> 197 us, one 7.9 -> 6.8)
+    // 202 -> 197 us, one 7.9 -> 6.8, 5.5 with a KV head a CTA)
     auto row0 = [&](int head) {
         return static_cast<size_t>(b) * p.num_qo_heads + (h0 + head) * p.group + part * kRows;
     };
@@ -198,16 +198,19 @@ __global__ void __launch_bounds__(kWinThreads, QW::kCtas)
 cudaError_t launch_window_quant(WindowParams p, int max_splits, cudaStream_t stream, bool pdl) {
     // (rows rounded up to a multiple of the CTAs are fewer than this, bytes to 16)
     constexpr int kMostSmem = QW::kXchgOff + 2 * (kRows + kMaxWindowSplits) * (kHeadDim + 1) * 4;
-    p.heads = p.layout == 0 && p.num_kv_heads % 2 == 0 ? 2 : 1;
-    const int64_t streams = static_cast<int64_t>(p.batch) * (p.num_kv_heads / p.heads) *
-                            ((p.group + kRows - 1) / kRows);
     const WindowOccupancy* occ = nullptr;
     const cudaError_t e = window_kernel_ready(
         window_quant_kernel, 0, kMostSmem,
         [](int c) { return QW::kXchgOff + 2 * exchange_bytes(kRows, c); }, &occ);
     if (e != cudaSuccess) return e;
-    p.splits = window_splits(p, *occ, streams, kWinWarps / p.heads * kChunk, max_splits);
-    return window_launch(window_quant_kernel, p, streams,
+    const int64_t streams =
+        static_cast<int64_t>(p.batch) * p.num_kv_heads * ((p.group + kRows - 1) / kRows);
+    // two KV heads a CTA (NHD) only where the CTAs of one would not all be resident: 76
+    // requests x 8 heads of 1024 tokens 24.1 us with two, 21.0 with one, 152 36.4 and 38.8
+    p.heads = p.layout == 0 && p.num_kv_heads % 2 == 0 && streams > occ->clusters[1] ? 2 : 1;
+    p.splits = window_splits(p, *occ, streams / p.heads, kWinWarps / p.heads * kChunk, true,
+                             max_splits);
+    return window_launch(window_quant_kernel, p, streams / p.heads,
                          QW::kXchgOff + p.heads * exchange_bytes(std::min(kRows, p.group), p.splits),
                          stream, pdl);
 }

@@ -344,6 +344,20 @@ def test_4bit_every_split(splits, G, Hkv):
     QuantCase([900, 40, 0], G, Hkv, 16, "NHD", 500, 20, seed=splits).check(max_splits=splits)
 
 
+@pytest.mark.parametrize("G", [1, 3, 8, 12])
+@pytest.mark.parametrize("batch,window,sinks", [(700, 40, 3), (330, 4096, 5), (330, 4100, 0), (900, 4096, 17)])
+def test_4bit_more_streams_than_the_gpu_holds(batch, window, sinks, G):
+    """Two KV heads a CTA, and (from 4096 tokens) streams cut in two although not all fit."""
+    rng = np.random.default_rng(batch + G)
+    lengths = rng.integers(0, 80, batch)
+    lengths[[3, batch - 1]] = 5000, 4400
+    c = QuantCase(list(map(int, lengths)), G, 2, 16, "NHD", window, sinks, seed=G)
+    out, lse = c.check()
+    o, z = c.check(max_splits=1)
+    if window < 4096:
+        assert torch.equal(o, out) and torch.equal(z, lse)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1.0])
 def test_4bit_scales(scale):
     QuantCase([200, 31], 4, 2, 16, "NHD", 90, 4, seed=8).check(scale)
