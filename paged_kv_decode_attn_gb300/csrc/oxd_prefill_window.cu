@@ -26,7 +26,7 @@
 // last token) are zeroed before the product, by the V warp as they land. Every wait is
 // bounded (OXD_DEVICE_WAIT_TIMEOUT); on abort the MMAs and copies in flight are drained.
 //
-// 8 prompts of 2048 (GQA4 x 8 heads) at window 1024 take 251 us, 1066 TFLOP/s, at 4096
+// 8 prompts of 2048 (GQA4 x 8 heads) at window 1024 take 253 us, 1055 TFLOP/s, at 4096
 // 720 us, 1338. What bounds it is the chain of a half, softmax (0.73 us), PV and the next
 // scores (0.85), as tensor memory has room for one score buffer a half (tensor pipe 47 %,
 // issue slots 36 %), and 3.5 us of a tile's 18 for its ends.
