@@ -13,6 +13,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <chrono>
 #include <functional>
 #include <cmath>
 #include <cstdlib>
@@ -70,13 +71,22 @@ struct oxd_plan_s {
 namespace {
 
 
-// Run epochs: never 0 and increasing over the process, so a status word left
-// in a workspace by an earlier run never passes for a later run's.
-std::atomic<uint32_t> g_epoch{0};
+// Run epochs: increasing over the process (for 2^29 runs), so a status word left in a
+// workspace by an earlier run never passes for a later one's. A workspace may also hold
+// any other data, whose words must not pass for the run's either: epochs lie in
+// [0xd0000000, 0xf0000000), below -2.6e8 as integers and -8e9 as F32 or bf16 numbers, from a
+// random one on (counted from 1, a request's lengths {30, 5} read as code 30 of run 5).
+uint32_t random_start() noexcept {
+    try {
+        return std::random_device{}();
+    } catch (...) {  // no source of random numbers
+        return static_cast<uint32_t>(
+            std::chrono::steady_clock::now().time_since_epoch().count());
+    }
+}
 uint32_t next_epoch() {
-    uint32_t e = g_epoch.fetch_add(1, std::memory_order_relaxed) + 1;
-    while (e == 0) e = g_epoch.fetch_add(1, std::memory_order_relaxed) + 1;
-    return e;
+    static std::atomic<uint32_t> counter{random_start()};
+    return 0xd0000000u + (counter.fetch_add(1, std::memory_order_relaxed) & 0x1fffffffu);
 }
 
 // Cost of one more work unit on a CTA (its epilogue and the refill of the
