@@ -858,8 +858,10 @@ oxd_status oxd_window_prefill_plan(const oxd_paged_prefill_desc* desc, int32_t w
  * row_pages) is listed as empty and recorded as OXD_DEVICE_BAD_POSITION, and so
  * is a *taken outside [0, num_free] (nothing is taken then) and a table longer
  * than num_indices or num_tokens (cut off there). Where the free list ends,
- * pages are listed as -1 and not counted as held (OXD_DEVICE_NO_PAGES); a free
- * page outside the pool is listed as it is (OXD_DEVICE_BAD_PAGE).
+ * pages are listed as -1 and not counted as held (OXD_DEVICE_NO_PAGES); an entry of
+ * the free list outside the pool, a negative one too (the padding of a list, say), is
+ * taken, held and listed as it is, its slots -1 if it is negative
+ * (OXD_DEVICE_BAD_PAGE, in the step that takes it).
  */
 typedef struct {
     int32_t batch;          /* B >= 1 */

@@ -130,6 +130,8 @@ __global__ void __launch_bounds__(kTabThreads, 1)
             const Request q = req[i];
             const int seg = (w % k) * 32 + lane, stride = k * 32;
             int32_t* row = p.rows + static_cast<size_t>(b0 + i) * p.row_pages;
+            // pages that it has after this step (the free list may end before its need)
+            const int have = min(q.need, q.held + max(n_free - q.free0, 0));
             // page j of the request: what its row lists, or the next free page
             auto page_of = [&](int j) {
                 if (j < q.held) return row[j];
@@ -159,9 +161,11 @@ __global__ void __launch_bounds__(kTabThreads, 1)
 #pragma unroll
                 for (int a = 0; a < kAhead; ++a) {
                     const int j = j0 + a * stride;
-                    if (j >= q.held && pages[a] >= 0) {
+                    if (j >= q.held && j < have) {
+                        // (what the free list says, a page or not: the row must not go on
+                        // listing what it held there before)
                         row[j] = pages[a];
-                        if (pages[a] >= p.num_pages)
+                        if (pages[a] < 0 || pages[a] >= p.num_pages)
                             fail(kDeviceBadPage);
                         else if (p.refcount != nullptr)
                             p.refcount[pages[a]] = 1;
