@@ -832,8 +832,12 @@ oxd_status oxd_window_prefill_plan(const oxd_paged_prefill_desc* desc, int32_t w
  *   - qo_indptr, token_request, positions: the new tokens, request by request in
  *     order of position, as the appends and the prefill take them;
  *   - slots: where each goes, page * page_size + position % page_size.
- * Entries of token_request, positions and slots behind the last new token are -1;
- * entries of indices behind indptr[B] are left as they were.
+ * Entries of token_request, positions and slots behind the last new token are -1
+ * (an append records such a token as OXD_DEVICE_BAD_POSITION and writes no row for
+ * it: num_tokens is best the step's count of new tokens); entries of indices behind
+ * indptr[B] are left as they were. A request's pages stay in its row when they leave
+ * its window: to give them to others is the caller's, by entries added to
+ * free_pages.
  *
  *   lengths, new_tokens  device int32 [B] (new_tokens may be NULL: none are new)
  *   page_rows     device int32 [B][row_pages], updated in place
@@ -855,13 +859,16 @@ oxd_status oxd_window_prefill_plan(const oxd_paged_prefill_desc* desc, int32_t w
  * and taken_out as above), OXD_ERR_WORKSPACE_TOO_SMALL, OXD_ERR_CUDA.
  * Device-side: a request whose length, count of new tokens or held pages is
  * outside its bounds (negative, more new tokens than tokens, more pages than
- * row_pages) is listed as empty and recorded as OXD_DEVICE_BAD_POSITION, and so
- * is a *taken outside [0, num_free] (nothing is taken then) and a table longer
- * than num_indices or num_tokens (cut off there). Where the free list ends,
- * pages are listed as -1 and not counted as held (OXD_DEVICE_NO_PAGES); an entry of
- * the free list outside the pool, a negative one too (the padding of a list, say), is
- * taken, held and listed as it is, its slots -1 if it is negative
- * (OXD_DEVICE_BAD_PAGE, in the step that takes it).
+ * row_pages, as when it outgrows its row) is listed as empty and recorded as
+ * OXD_DEVICE_BAD_POSITION. Its new tokens are in no token map, so the tokens of the
+ * requests behind it come earlier than in rows packed for all of them: an append of
+ * such rows writes them into the wrong requests. Recorded as the same are a *taken
+ * outside [0, num_free] (nothing is taken then) and a table longer than num_indices
+ * or num_tokens (cut off there). Where the free list ends, pages are listed as -1 and
+ * not counted as held (OXD_DEVICE_NO_PAGES). An entry of the free list outside the
+ * pool, a negative one too (the padding of a list, say), is taken, held and listed
+ * as it is, its slots -1 if it is negative (OXD_DEVICE_BAD_PAGE, in the step that
+ * takes it).
  */
 typedef struct {
     int32_t batch;          /* B >= 1 */
@@ -908,7 +915,9 @@ oxd_status oxd_plan_destroy(oxd_plan plan);
  * the code is OXD_DEVICE_OK, OXD_ERR_DEVICE_STATUS otherwise, OXD_ERR_CUDA if
  * the copy failed. This is the one call that blocks the host. The replays of a
  * captured call count as one run: a code that one of them recorded is read after
- * later ones too.
+ * later ones too. Runs that share a workspace share its status: the next one that
+ * starts ends the code of the one before it, so where every error of a chain of
+ * launches matters (tables, append, decode) each takes a workspace of its own.
  */
 oxd_status oxd_read_device_status(const void* workspace, void* stream, int32_t* code);
 
