@@ -804,6 +804,9 @@ oxd_status oxd_quant_window_decode(const oxd_window_decode_desc* desc, const voi
  * copied. A row of K and V that no query of the call sees may hold anything; one
  * that some query sees has to be finite for the others' sake (a masked row of V
  * enters the product with weight 0, as in the prefill without a window).
+ * A query with a NaN score among those that it sees gets NaN, out and lse, as in the
+ * window decode (the plan without a window: lse -inf). A window that holds every
+ * request whole is run as none.
  * Errors: as oxd_paged_prefill_plan, and OXD_ERR_INVALID_ARGUMENT for window < 1
  * or sinks < 0, OXD_ERR_UNSUPPORTED for window + sinks above 2^30.
  */

@@ -144,6 +144,8 @@ struct MergeParams {
     float s_to_ln;                // factor taking s to natural log (1, or ln 2 for log2)
     int32_t max_count;            // most states of any entry: rows of more than 16 states
                                   // (D = 128) are merged by two warps, half a row each
+    int32_t nan_states;           // 1: weights that sum to NaN give lse NaN (entries in a
+                                  // workspace); 0: -inf
 };
 
 // Fused RoPE + paged append (oxd_append.cu).

@@ -53,7 +53,7 @@ __device__ __forceinline__ bool locate_row(const MergeParams& p, const int4* ent
     return true;
 }
 
-template <int kHalves>
+template <int kHalves, bool kNan = false>
 __device__ __forceinline__ void merge_row(const MergeParams& p, const RowJob& j) {
     // state i of row r: s[(first + i) * R + r], v[((first + i) * R + r) * D]
     const float* s = p.s + j.first * p.R + j.r;
@@ -61,10 +61,10 @@ __device__ __forceinline__ void merge_row(const MergeParams& p, const RowJob& j)
     uint16_t* out = p.out + static_cast<size_t>(j.row0 + j.r) * p.D;
     float* lse = p.lse != nullptr ? p.lse + j.row0 + j.r : nullptr;
     if constexpr (kHalves == 2)
-        merge_states_half_row(s, static_cast<size_t>(p.R), v, static_cast<size_t>(p.R) * p.D,
+        merge_states_half_row<kNan>(s, static_cast<size_t>(p.R), v, static_cast<size_t>(p.R) * p.D,
                               j.count, p.s_to_ln, out, lse, threadIdx.x & 31, j.half);
     else
-        merge_states_row(s, static_cast<size_t>(p.R), v, static_cast<size_t>(p.R) * p.D, j.count,
+        merge_states_row<kNan>(s, static_cast<size_t>(p.R), v, static_cast<size_t>(p.R) * p.D, j.count,
                          p.D, p.s_to_ln, out, lse, threadIdx.x & 31);
 }
 
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32) merge_kernel(const MergeP
     if (locate_row<kHalves>(p, nullptr, &j)) merge_row<kHalves>(p, j);
 }
 
-template <class SL, int kHalves>
+template <class SL, int kHalves, bool kNan = false>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     split_merge_kernel(const MergeParams p, const __grid_constant__ SL inl) {
     // The entry list and the stamp were written before the decode kernel
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     const bool have = (p.ws_stamp == nullptr || *p.ws_stamp == p.stamp) &&  // this plan's entries
                       locate_row<kHalves>(p, entries, &j);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (have) merge_row<kHalves>(p, j);
+    if (have) merge_row<kHalves, kNan>(p, j);
 }
 
 // Rows of more than 16 states of 128 columns take two warps (one pass each).
@@ -132,10 +132,14 @@ cudaError_t launch_split_merge(const MergeParams& p, const SplitList* splits,
     if (halves_for(p) == 2) {
         if (splits != nullptr)
             return cudaLaunchKernelEx(&cfg, split_merge_kernel<SplitList, 2>, p, *splits);
+        if (p.nan_states)
+            return cudaLaunchKernelEx(&cfg, split_merge_kernel<NoList, 2, true>, p, NoList{0});
         return cudaLaunchKernelEx(&cfg, split_merge_kernel<NoList, 2>, p, NoList{0});
     }
     if (splits != nullptr)
         return cudaLaunchKernelEx(&cfg, split_merge_kernel<SplitList, 1>, p, *splits);
+    if (p.nan_states)
+        return cudaLaunchKernelEx(&cfg, split_merge_kernel<NoList, 1, true>, p, NoList{0});
     return cudaLaunchKernelEx(&cfg, split_merge_kernel<NoList, 1>, p, NoList{0});
 }
 

@@ -7,11 +7,13 @@
 //   out = sum_i w_i v_i / sum_i w_i (rounded once to bf16),
 //   lse = M + ln sum_i w_i.
 // -inf states weigh nothing; a row whose states are all -inf gets out = 0 and
-// lse = -inf. Each lane owns 4 consecutive columns; the weighted sum visits
-// the states in order. A row of up to 16 states (one pass) is merged with
-// every lane holding all the log-sums; longer rows reduce them across the
-// warp. A given launch always takes the same path for a row, so results are
-// deterministic. Loads go through L2 (ld.global.cg): the states may have been
+// lse = -inf. With kNan a row whose weights sum to NaN gets lse = NaN instead of -inf:
+// a windowed prefill's piece with NaN scores has the log-sum +inf and NaN values, so
+// that its row is NaN whatever the other states are. Each lane owns 4 consecutive
+// columns; the weighted sum visits the states in order. A row of up to 16 states (one
+// pass) is merged with every lane holding all the log-sums; longer rows reduce them
+// across the warp. A given launch always takes the same path for a row, so results
+// are deterministic. Loads go through L2 (ld.global.cg): the states may have been
 // written by other CTAs of a still-running grid.
 #pragma once
 
@@ -25,6 +27,12 @@ __device__ __forceinline__ uint32_t merge_pack_bf16x2(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
+template <bool kNan>
+__device__ __forceinline__ float merged_lse(float M, float W) {
+    return W > 0.f ? M + logf(W) : kNan && W != 0.f ? NAN : -INFINITY;
+}
+
+template <bool kNan>
 __device__ __forceinline__ void merge_states_row(const float* s, size_t s_stride, const float* v,
                                                  size_t v_stride, int count, int D,
                                                  float s_to_ln, uint16_t* out_row,
@@ -78,7 +86,7 @@ __device__ __forceinline__ void merge_states_row(const float* s, size_t s_stride
             packed.y = merge_pack_bf16x2(acc.z * inv, acc.w * inv);
             *reinterpret_cast<uint2*>(out_row + lane * 4) = packed;
         }
-        if (lane == 0 && lse_out != nullptr) *lse_out = W > 0.f ? M + logf(W) : -INFINITY;
+        if (lane == 0 && lse_out != nullptr) *lse_out = merged_lse<kNan>(M, W);
         return;
     }
     // lane i's first log-sum (state i) is loaded once, before the values,
@@ -145,7 +153,7 @@ __device__ __forceinline__ void merge_states_row(const float* s, size_t s_stride
         packed.y = merge_pack_bf16x2(acc.z * inv, acc.w * inv);
         *reinterpret_cast<uint2*>(out_row + c) = packed;
     }
-    if (lane == 0 && lse_out != nullptr) *lse_out = W > 0.f ? M + logf(W) : -INFINITY;
+    if (lane == 0 && lse_out != nullptr) *lse_out = merged_lse<kNan>(M, W);
 }
 
 // The same merge for one half of a 128-column row: columns [64 half, 64 half
@@ -154,6 +162,7 @@ __device__ __forceinline__ void merge_states_row(const float* s, size_t s_stride
 // states is merged with every lane holding all the log-sums; longer rows
 // reduce them across the warp, with the arithmetic, weights and state order
 // merge_states_row uses for them. lse_out is written by the half-0 warp.
+template <bool kNan>
 __device__ __forceinline__ void merge_states_half_row(const float* s, size_t s_stride,
                                                       const float* v, size_t v_stride, int count,
                                                       float s_to_ln, uint16_t* out_row,
@@ -193,7 +202,7 @@ __device__ __forceinline__ void merge_states_half_row(const float* s, size_t s_s
         const float inv = W > 0.f ? 1.f / W : 0.f;
         *reinterpret_cast<uint32_t*>(out_row + c) = merge_pack_bf16x2(acc.x * inv, acc.y * inv);
         if (half == 0 && lane == 0 && lse_out != nullptr)
-            *lse_out = W > 0.f ? M + logf(W) : -INFINITY;
+            *lse_out = merged_lse<kNan>(M, W);
         return;
     }
     const float s_lane =
@@ -245,7 +254,7 @@ __device__ __forceinline__ void merge_states_half_row(const float* s, size_t s_s
         }
     }
     *reinterpret_cast<uint32_t*>(out_row + c) = merge_pack_bf16x2(acc.x * inv, acc.y * inv);
-    if (half == 0 && lane == 0 && lse_out != nullptr) *lse_out = W > 0.f ? M + logf(W) : -INFINITY;
+    if (half == 0 && lane == 0 && lse_out != nullptr) *lse_out = merged_lse<kNan>(M, W);
 }
 
 }  // namespace oxd

@@ -74,6 +74,9 @@ struct PrefillParams {
     int32_t wait_prior;             // 1: launched early behind another grid, which must
                                     // complete before this one does (griddepcontrol.wait)
     int64_t wait_ns;                // limit of a pipeline wait (> 0)
+    int32_t nan_rows;               // 1 (windowed plans): a row with NaN scores gets out and lse
+                                    // NaN (a piece of one the log-sum +inf, by which the merge
+                                    // knows it); 0: lse -inf
     int32_t window;                 // 0: no window; else a query at position p sees tokens
     int32_t sinks;                  // j > p - window or j < sinks
     const int32_t* cta_begin;       // the persistent kernel's: units of CTA c are

@@ -35,6 +35,7 @@ using namespace oxd;
 struct oxd_prefill_plan_s {
     oxd_paged_prefill_desc desc;
     int device;  // -1: host-only plan
+    int nan_rows;       // 1: made by oxd_window_prefill_plan
     int window, sinks;  // window 0: none
     int group;
     bool narrow;  // 128-row tiles on the narrow kernel, else 256-row tiles
@@ -235,6 +236,7 @@ oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sink
                             : q * (L - q) + q * (q + 1) / 2;
         longest = std::max(longest, L);
     }
+    const int nan_rows = window > 0 ? 1 : 0;
     // a window that holds every request whole is none
     if (window >= longest) window = 0;
     const int64_t nq = qo_indptr[B];
@@ -421,6 +423,7 @@ oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sink
     oxd_prefill_plan P = new (std::nothrow) oxd_prefill_plan_s();
     if (P == nullptr) return OXD_ERR_NO_MEMORY;
     P->desc = d;
+    P->nan_rows = nan_rows;
     P->window = window;
     P->sinks = sinks;
     P->device = plan_device;
@@ -682,6 +685,7 @@ oxd_status oxd_paged_prefill_run(oxd_prefill_plan plan, const void* q, const voi
     p.num_pages = d.num_pages;
     p.scale_log2 = sm_scale * 1.4426950408889634f;  // log2(e)
     p.wait_ns = d.wait_timeout_ns > 0 ? d.wait_timeout_ns : kWaitTimeoutNs;
+    p.nan_rows = plan->nan_rows;
     p.window = plan->window;
     p.sinks = plan->sinks;
     p.cta_begin = reinterpret_cast<const int32_t*>(ws + plan->off_ctas);
@@ -712,6 +716,7 @@ oxd_status oxd_paged_prefill_run(oxd_prefill_plan plan, const void* q, const voi
         mp.D = kHeadDim;
         mp.s_to_ln = 0.693147180559945309f;  // partial LSEs are log2
         mp.max_count = plan->max_pieces;
+        mp.nan_states = p.nan_rows;
         if (launch_split_merge(mp, nullptr, s, plan->ev_after == nullptr) != cudaSuccess)
             return OXD_ERR_CUDA;
     }

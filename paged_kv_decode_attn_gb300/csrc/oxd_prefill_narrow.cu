@@ -504,7 +504,8 @@ __global__ void __launch_bounds__(kPThreads)
                     break;
                 }
                 tc_fence_after();
-                const bool seen = l > 0.f;  // a piece may lie wholly past a row's position
+                // a piece may lie wholly past a row's position
+                const bool seen = l > 0.f || (p.nan_rows && l != 0.f);
                 const float inv = seen ? 1.f / l : 0.f;
                 const float lse2 = seen ? m_ref + __log2f(l) : -INFINITY;
                 const int hq = u.hkv * G + gi;
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(kPThreads)
                         const size_t grp =
                             static_cast<size_t>(u.state) +
                             static_cast<size_t>(t) * u.n_pieces + u.piece;
-                        p.part_lse[grp * G + gi] = lse2;
+                        p.part_lse[grp * G + gi] = seen && l != l ? INFINITY : lse2;
                     }
                 }
             }

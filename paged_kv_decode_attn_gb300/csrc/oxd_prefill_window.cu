@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && nst > 0 && !wait_all(&ctl.o_done[h], n_o++)) ok = false;
             if (ok && (nst > 0 || (c.n_st > 0 && c.n_pieces > 1))) {
                 tc_fence_after();
-                const bool seen = l > 0.f;
+                const bool seen = l != 0.f;  // (NaN scores: out and lse are NaN)
                 const float inv = seen ? 1.f / l : 0.f;
                 const float lse2 = seen ? m_ref + __log2f(l) : -INFINITY;
                 // The rows go out through shared memory, 128 bytes of each at a time, so that
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t row = out_row(R);
                 if (row >= 0) {
                     if (!whole_tile)
-                        p.part_lse[row] = lse2;
+                        p.part_lse[row] = l != l ? INFINITY : lse2;
                     else if (p.lse != nullptr)
                         p.lse[row] = lse2 * kLn2;
                 }
