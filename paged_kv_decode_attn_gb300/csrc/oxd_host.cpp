@@ -308,7 +308,8 @@ const char* oxd_device_status_string(int32_t code) {
         case OXD_DEVICE_PLAN_MISMATCH: return "device block tables differ from the plan";
         case OXD_DEVICE_WAIT_TIMEOUT: return "pipeline wait timed out";
         case OXD_DEVICE_SHARED_PAGE: return "append target page is shared (reference count not 1)";
-        case OXD_DEVICE_BAD_POSITION: return "append position outside the request's block table";
+        case OXD_DEVICE_BAD_POSITION:
+            return "request, position, length or table entry outside its bounds";
         case OXD_DEVICE_NO_PAGES: return "no free pages left";
     }
     return "unknown device status";

@@ -1,4 +1,4 @@
-"""A workspace may hold any data before a run: none of it reads as the run's status."""
+"""The device status: its texts, and that a workspace may hold any data before a run without it reading as one."""
 import ctypes
 import os
 import subprocess
@@ -73,3 +73,8 @@ def test_lengths_left_in_the_workspace_are_no_status():
         pytest.skip("no CUDA device")
     r = subprocess.run([sys.executable, "-c", CHILD % ROOT], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_the_text_of_a_bad_position_fits_the_tables_and_decodes_too():
+    text = oxd.oxd_device_status_string(oxd.OXD_DEVICE_BAD_POSITION)
+    assert "append" not in text and all(w in text for w in ("position", "length", "table entry"))
