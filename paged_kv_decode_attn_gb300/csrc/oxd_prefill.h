@@ -87,8 +87,9 @@ struct PrefillParams {
 // `front` (with the sinks), then those from front + skip on (from the first token of its
 // first query's window). Its cached tokens are counted without the skipped pages: token
 // v of a tile is token v of the request, or v + skip pages from `front` pages on, and so
-// are kv_begin, kv_valid and n_pages of its pieces. In that count a query at position p
-// (count it by window_position) sees the tokens v <= p with v > p - window or v < sinks.
+// are kv_begin, kv_valid and n_pages of its pieces. Counted so, a query's own position is
+// skip pages lower too (TileWindow::p0 is the first one's); one at p sees the tokens v <= p
+// with v > p - window or v < sinks.
 struct WindowPages {
     int32_t front, skip;
 };
@@ -121,7 +122,6 @@ cudaError_t launch_prefill_narrow(const CUtensorMap& tk, const CUtensorMap& tv,
 // stages of the two-half kernel, one CTA a SM, each with up to kWindowUnits units. Their
 // n_pages fills the last stage where the request has the pages.
 constexpr int kWindowUnits = 32;
-cudaError_t prefill_window_smem_bytes(int* bytes);
 // tq: q as (d, head, token) with a box of 64 x G x (128 / G) and the 128-byte swizzle,
 // used where G divides 128.
 cudaError_t launch_prefill_window(const CUtensorMap& tk, const CUtensorMap& tv,

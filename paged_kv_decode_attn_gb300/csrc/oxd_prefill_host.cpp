@@ -276,8 +276,9 @@ oxd_status plan_prefill(const oxd_paged_prefill_desc* desc, int window, int sink
     const int rows = narrow ? kNarrowRows : kPrefillRows;
     const int stage_tokens = narrow ? kNarrowStageTokens : kPrefillStageTokens;
     const int T = rows / G;
-    int ctas_per_sm = 0;
-    if (plan_device >= 0) {
+    // (the persistent kernel of windows has a CTA's shared memory to itself on an SM)
+    int ctas_per_sm = window > 0 && !narrow ? 1 : 0;
+    if (plan_device >= 0 && ctas_per_sm == 0) {
         int prev = 0;
         if (cudaGetDevice(&prev) != cudaSuccess) return OXD_ERR_CUDA;
         if (cudaSetDevice(device) != cudaSuccess) return OXD_ERR_CUDA;

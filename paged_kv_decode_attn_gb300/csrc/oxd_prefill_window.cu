@@ -852,11 +852,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-cudaError_t prefill_window_smem_bytes(int* bytes) {
-    *bytes = kSmemBytes;
-    return cudaSuccess;
-}
-
 cudaError_t launch_prefill_window(const CUtensorMap& tk, const CUtensorMap& tv,
                                   const CUtensorMap& tq, const PrefillParams& p, int grid,
                                   cudaStream_t stream) {
