@@ -9,9 +9,11 @@
 // The state (held, taken) may be updated in place: it is written behind a cluster
 // barrier that every CTA passes after it has read it.
 //
-// 64 requests' step takes 4.1 us, 8 prompts 4.6 (one launch's latencies), 1024 requests of
-// 512 pages 10: 16 SMs' instructions, where the bytes would take 0.6 of the whole GPU's.
-// The decode step that such tables are for takes a hundred times as long.
+// In a graph 64 requests' step takes 4.1 us, 8 prompts 4.6 (one launch's latencies; 6.8 as
+// calls, by the host's time), 1024 requests of 128..16384 tokens 13.1, of 512 pages each 10:
+// 16 SMs' instructions, where the bytes would take 0.6 of the whole GPU's. For 1024 requests
+// that is a hundredth of the decode step that such tables are for; for one request the
+// tables take about as long as it (5.2).
 #include <algorithm>
 #include <atomic>
 

@@ -211,6 +211,18 @@ cudaError_t window_kernel_ready(void (*kernel)(WindowParams), int which, int mos
 // up to two waves of the GPU, if the last of them fills at most 85 % of their room (320
 // streams of 4096 57 -> 46 us, 440 58 -> 55, 1024 of mixed lengths 202 -> 193; but 608
 // 60 -> 66, 1216 115 -> 126): `ends_cost`.
+// 4096 is on the safe side: two CTAs against one by window and streams of that length,
+//          512 streams   640          800          1000         1600
+//   bf16 1024  47/44     60/63        69/67        86/78        129/122 us
+//   bf16 2048  83/83     107/118      124/127      156/150      241/236
+//   bf16 4096  156/159   203/232      237/248      298/294      466/464
+//   bf16 8192  302/316   398/451      466/491      586/581      925/922
+//   4 bits 1024  23/19   28/32        33/33        37/34        54/50
+//   4 bits 2048  36/34   48/59        52/60        60/61        90/90
+//   4 bits 4096  59/60   83/110       92/112       105/114      161/169
+//   4 bits 8192  105/114 154/213      172/216      198/219      304/330
+// (at 2048 two would gain where a second wave is nearly empty and lose elsewhere; below,
+// they lose).
 inline int window_splits(const WindowParams& p, const WindowOccupancy& occ, int64_t streams,
                          int least, bool ends_cost, int max_splits) {
     const int64_t most = std::min<int64_t>(

@@ -23,10 +23,13 @@
 //     of weights is not rounded).
 //
 // HBM bounds it where there is work for all SMs: 256 requests U{128..16384} x 8 heads,
-// groups of 8, window 4096, 548 us, the copy rate; 64 x 8 heads of 512 tokens 23.3 us,
-// 84 % (one wave: 3 us of it a CTA's start and end). One request x 8 heads of 1024 tokens
-// 5.3 us: the chain tables, page index, rows, cluster merge. 16 x 1 head of 8256 tokens
-// with 32 rows 19 us, 52 %: a chunk's chain of waits with 10 warps a SM.
+// groups of 8, window 4096, 528 to 537 us by the lengths drawn, 7.15 TB/s of reads (a
+// copy, half of it writes, runs at 6.77); 64 x 8 heads of 512 tokens 22.9 us in a graph, 86 %
+// of the copy rate (one wave: 3 us of it a CTA's start and end). One request x 8 heads of 1024
+// tokens 5.2 us in a graph, 5.9 as a call: the chain tables, page index, rows, cluster merge.
+// Groups of 17 to 32, in two parts that both copy and read all rows: 16 x 1 head of 8256
+// tokens 18.7 us in a graph, 54 % (copies, fragments and waits a byte are doubled, over 10
+// warps a SM), 64 x 8 heads of 4096 212, 75 %.
 #include <cuda_bf16.h>
 
 #include <algorithm>
