@@ -26,7 +26,7 @@
 // last token) are zeroed before the product, by the V warp as they land. Every wait is
 // bounded (OXD_DEVICE_WAIT_TIMEOUT); on abort the MMAs and copies in flight are drained.
 //
-// 8 prompts of 2048 (GQA4 x 8 heads) at window 1024 take 248 to 253 us, 1060 TFLOP/s, at
+// 8 prompts of 2048 (GQA4 x 8 heads) at window 1024 take 248 to 254 us, 1060 TFLOP/s, at
 // 4096 725 us, 1330. What the first loses against the rate of a matrix product, of a tile's 18.1
 // us: 3.5 for its ends; a stage's chain, softmax (0.73 us), PV and the next scores (0.85),
 // 1.6 us where its products alone are 1.3; and 11 % of the tokens in its stages, which

@@ -23,13 +23,13 @@
 //     of weights is not rounded).
 //
 // HBM bounds it where there is work for all SMs: 256 requests U{128..16384} x 8 heads,
-// groups of 8, window 4096, 528 to 537 us by the lengths drawn, 7.15 TB/s of reads (a
-// copy, half of it writes, runs at 6.77); 64 x 8 heads of 512 tokens 22.9 us in a graph, 86 %
-// of the copy rate (one wave: 3 us of it a CTA's start and end). One request x 8 heads of 1024
-// tokens 5.2 us in a graph, 5.9 as a call: the chain tables, page index, rows, cluster merge.
-// Groups of 17 to 32, in two parts that both copy and read all rows: 16 x 1 head of 8256
-// tokens 18.7 us in a graph, 54 % (copies, fragments and waits a byte are doubled, over 10
-// warps a SM), 64 x 8 heads of 4096 212, 75 %.
+// groups of 8, window 4096, 547 us with other inputs from call to call, 528 to 537 with the
+// same ones (7.15 TB/s of reads; a copy, half of it writes, runs at 6.77); 64 x 8 heads of up
+// to 512 tokens 23.7 us, 83 % of the copy rate (one wave: 3 us of it a CTA's start and end).
+// One request x 8 heads of 1024 tokens 5.6 us, 5.2 in a graph: the chain tables, page index,
+// rows, cluster merge. Groups of 17 to 32, in two parts that both copy and read all rows: 16
+// x 1 head of 8256 tokens 20.4 us, 49 % (copies, fragments and waits a byte are doubled, over
+// 10 warps a SM), 64 x 8 heads of 4096 212, 75 %.
 #include <cuda_bf16.h>
 
 #include <algorithm>

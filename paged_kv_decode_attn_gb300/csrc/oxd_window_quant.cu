@@ -12,7 +12,7 @@
 // 256 requests U{128..16384} x 8 heads, groups of 8, window 4096: 197 us, 81 % of the copy
 // rate; between the ends of streams it runs at 94 % (of which 572 instructions a chunk take
 // 56 % of the issue slots), a CTA's start and end cost 8 us of one wave. In a graph 8 requests
-// x 8 heads of 1024 tokens take 7.4 us, one request 5.5 (latencies; 8.0 and 6.0 as calls).
+// x 8 heads of 1024 tokens take 7.4 us, one request 5.5 (latencies; 7.8 and 6.0 as calls).
 // Larger groups pay for every part, which unpacks and converts the codes again: 64 x 8 heads
 // of 4096 tokens 60 us with groups of 8, 105 with 16, 202 with 32 (floor 45).
 #include <algorithm>
